@@ -104,6 +104,20 @@ int check_quantize_args(const void *x, int64_t rows, int64_t cols, int scaling, 
   return FP8L_OK;
 }
 
+bool misaligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+// Checks shared by the norm entry points.
+int check_norm(int64_t rows, int64_t cols, int kind, int dtype, int pdtype) {
+  if ((kind != FP8L_LAYERNORM && kind != FP8L_RMSNORM) ||
+      (dtype != FP8L_BF16 && dtype != FP8L_F32) || (pdtype != FP8L_BF16 && pdtype != FP8L_F32))
+    return FP8L_EINVAL;
+  if (rows < 0 || rows > (int64_t)1 << 30 || cols < 1 || cols > FP8L_NORM_MAX_COLS)
+    return FP8L_ESHAPE;
+  return FP8L_OK;
+}
+
+bool bad_eps(float eps) { return !(eps >= 0.f && eps <= 3.402823466e38f); }
+
 }  // namespace
 
 extern "C" {
@@ -340,6 +354,94 @@ int fp8_swiglu_bwd(const void *dh, const void *a, const void *b, int64_t rows, i
   const fp8l::Fp8Out qb = {dbq, dbqt, db_scale, db_scale_t, db_amax};
   hipError_t e = fp8l::swiglu_bwd_launch(dh, a, b, rows, hidden, scaling, da, db, qa, qb,
                                          workspace, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FP8L_OK : FP8L_EHIP;
+}
+
+size_t fp8_layernorm_workspace_bytes(int64_t rows, int64_t cols, int scaling) {
+  if (check_norm(rows, cols, 0, 0, 0) != FP8L_OK || bad_scaling(scaling)) return 0;
+  return fp8l::norm_workspace_bytes(rows, cols, scaling);
+}
+
+int fp8_layernorm_fwd(const void *x, int64_t rows, int64_t cols, int kind, int dtype,
+                      const void *weight, const void *bias, int pdtype, float eps, void *y,
+                      float *mean, float *rstd, void *stream) {
+  const int s = check_norm(rows, cols, kind, dtype, pdtype);
+  if (s != FP8L_OK) return s;
+  if (bad_eps(eps) || (rows > 0 && (!x || !y))) return FP8L_EINVAL;
+  if (misaligned(x) || misaligned(weight) || misaligned(bias) || misaligned(y) ||
+      misaligned4(mean) || misaligned4(rstd))
+    return FP8L_EALIGN;
+  const fp8l::NormIn in = {x, weight, bias, pdtype == FP8L_F32, kind == FP8L_RMSNORM, eps,
+                           rows, cols};
+  hipError_t e = fp8l::norm_fwd_launch(in, dtype == FP8L_F32, y, mean, rstd,
+                                       static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FP8L_OK : FP8L_EHIP;
+}
+
+int fp8_layernorm_quantize(const void *x, int64_t rows, int64_t cols, int kind,
+                           const void *weight, const void *bias, int pdtype, float eps,
+                           int scaling, void *y, float *mean, float *rstd, void *q, void *qt,
+                           float *scale, float *scale_t, float *amax_out, void *workspace,
+                           size_t workspace_bytes, void *stream) {
+  const int s = check_norm(rows, cols, kind, FP8L_BF16, pdtype);
+  if (s != FP8L_OK) return s;
+  if (scaling != FP8L_TENSORWISE && scaling != FP8L_ROWWISE) return FP8L_EINVAL;
+  if (bad_eps(eps)) return FP8L_EINVAL;
+  const bool rw = scaling == FP8L_ROWWISE;
+  const bool rows_only = rw && !qt && rows > 0;
+  if (cols % 16 != 0 || (!rows_only && rows % 16 != 0)) return FP8L_ESHAPE;
+  if (rows > 0 && (!x || !q || (!qt && !rows_only))) return FP8L_EINVAL;
+  // scale vectors may be NULL only where they have no entries
+  if (!scale && (!rw || rows > 0)) return FP8L_EINVAL;
+  if (!scale_t && qt) return FP8L_EINVAL;
+  if (!scale_t && !rw) return FP8L_EINVAL;
+  if (!rows_only && rows > 0 && !y && (!rstd || (kind == FP8L_LAYERNORM && !mean)))
+    return FP8L_EINVAL;
+  if (misaligned(x) || misaligned(weight) || misaligned(bias) || misaligned(y) ||
+      misaligned(q) || misaligned(qt))
+    return FP8L_EALIGN;
+  for (const float *f : {(const float *)mean, (const float *)rstd, (const float *)scale,
+                         (const float *)scale_t, (const float *)amax_out})
+    if (misaligned4(f)) return FP8L_EALIGN;
+  const fp8l::NormIn in = {x, weight, bias, pdtype == FP8L_F32, kind == FP8L_RMSNORM, eps,
+                           rows, cols};
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  hipError_t e;
+  if (rows_only) {
+    e = fp8l::norm_rows_launch(in, y, mean, rstd, q, scale, amax_out, st);
+  } else {
+    if (rw && !scale_t) return FP8L_OK;          // no rows, no column scales wanted
+    if (!workspace) return FP8L_EINVAL;
+    if (workspace_bytes < fp8l::norm_workspace_bytes(rows, cols, scaling)) return FP8L_EWORKSPACE;
+    if (misaligned(workspace)) return FP8L_EALIGN;
+    e = fp8l::norm_quantize_launch(in, scaling, y, mean, rstd,
+                                   {q, qt, scale, scale_t, amax_out}, workspace, st);
+  }
+  return e == hipSuccess ? FP8L_OK : FP8L_EHIP;
+}
+
+int fp8_layernorm_bwd(const void *dy, const void *x, const void *weight, const float *mean,
+                      const float *rstd, int64_t rows, int64_t cols, int kind, int dtype,
+                      int pdtype, void *dx, float *dweight, float *dbias, void *workspace,
+                      size_t workspace_bytes, void *stream) {
+  const int s = check_norm(rows, cols, kind, dtype, pdtype);
+  if (s != FP8L_OK) return s;
+  if (!dx && !dweight && !dbias) return FP8L_EINVAL;
+  if (rows > 0 && (!dy || !x || !rstd || (kind == FP8L_LAYERNORM && !mean))) return FP8L_EINVAL;
+  if (misaligned(dy) || misaligned(x) || misaligned(weight) || misaligned(dx))
+    return FP8L_EALIGN;
+  for (const float *f : {mean, rstd, (const float *)dweight, (const float *)dbias})
+    if (misaligned4(f)) return FP8L_EALIGN;
+  if (dweight || dbias) {
+    if (!workspace) return FP8L_EINVAL;
+    if (workspace_bytes < fp8l::norm_workspace_bytes(rows, cols, FP8L_TENSORWISE))
+      return FP8L_EWORKSPACE;
+    if (misaligned(workspace)) return FP8L_EALIGN;
+  }
+  const fp8l::NormIn in = {x, weight, nullptr, pdtype == FP8L_F32, kind == FP8L_RMSNORM, 0.f,
+                           rows, cols};
+  hipError_t e = fp8l::norm_bwd_launch(dy, in, dtype == FP8L_F32, mean, rstd, dx, dweight, dbias,
+                                       workspace, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? FP8L_OK : FP8L_EHIP;
 }
 

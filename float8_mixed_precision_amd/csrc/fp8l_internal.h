@@ -111,6 +111,23 @@ __device__ __forceinline__ U4 load16(const void *p) {
   return {v.x, v.y, v.z, v.w};
 }
 
+// Two fp32 values as a bf16 pair (a in the low half), round to nearest even.
+__device__ __forceinline__ uint32_t bf16x2_bits(float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b16x2 __attribute__((ext_vector_type(2)));
+  const f32x2 v = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, b16x2));
+}
+
+// One normalized value.  The norm's statistics pass and the cast that
+// normalizes again both call this, so the fixed sequence of roundings makes
+// them see the same y.
+__device__ __forceinline__ float norm_value(float x, float mean, float rstd, float w, float b) {
+#pragma clang fp contract(off)
+  const float xh = (x - mean) * rstd;
+  return __builtin_fmaf(xh, w, b);
+}
+
 // ---------------------------------------------------------- host launchers --
 
 // Quantize (amax partials -> scales -> cast + transpose), all enqueued on
@@ -147,6 +164,44 @@ struct Fp8Out {
   void *q, *qt;
   float *scale, *scale_t, *amax;
 };
+
+// The cast half of a quantize with its partial maxima wherever a producer
+// put them: tensorwise part[nparts]; rowwise rowpart[row_slices][rows] and
+// colpart[col_slices][cols].  With rstd, the values quantized are not x but
+// its layer norm (norm_value of the row's mean and rstd, weight w and bias b,
+// rounded to bf16); mean NULL counts as 0, w as 1, b as 0.
+struct CastSource {
+  const void *x;
+  const void *w, *b;
+  int wf32;
+  const float *mean, *rstd;
+  const uint32_t *part;
+  int nparts;
+  const uint16_t *rowpart, *colpart;
+  int row_slices, col_slices;
+};
+hipError_t quantize_cast_launch(const CastSource &src, int64_t rows, int64_t cols, int scaling,
+                                const Fp8Out &o, hipStream_t stream);
+
+// Layer norm (norm.hip).  w, b: bf16, or fp32 with wf32; NULL for 1 and 0.
+struct NormIn {
+  const void *x;
+  const void *w, *b;
+  int wf32, rms;
+  float eps;
+  int64_t rows, cols;
+};
+size_t norm_workspace_bytes(int64_t rows, int64_t cols, int scaling);
+hipError_t norm_fwd_launch(const NormIn &in, int f32, void *y, float *mean, float *rstd,
+                           hipStream_t stream);
+hipError_t norm_rows_launch(const NormIn &in, void *y, float *mean, float *rstd, void *q,
+                            float *scale, float *amax_out, hipStream_t stream);
+// y NULL: not written, and the cast normalizes x again (mean and rstd needed)
+hipError_t norm_quantize_launch(const NormIn &in, int scaling, void *y, float *mean, float *rstd,
+                                const Fp8Out &o, void *workspace, hipStream_t stream);
+hipError_t norm_bwd_launch(const void *dy, const NormIn &in, int f32, const float *mean,
+                           const float *rstd, void *dx, float *dw, float *db, void *workspace,
+                           hipStream_t stream);
 
 // SwiGLU producers (swiglu.hip): the elementwise pass writes its bf16
 // outputs with their amax partial maxima, then each output's quantize

@@ -276,13 +276,39 @@ __global__ __launch_bounds__(256) void k_finalize_rowwise(
 // MODE_RW: scale / scale_t are inputs (from k_finalize_rowwise).
 // MODE_GIVEN: scale[0] is a tensorwise multiplier given by the caller.
 // FMT: 0 = E4M3 codes, 1 = E5M2 codes (scale onto 57344).
+// NORM: x is normalized on the way (nm: the layer norm's parameters and
+// statistics), so that a norm whose y nobody else reads is not written out.
 constexpr int MODE_TW = 0, MODE_RW = 1, MODE_GIVEN = 2;
-template <int MODE, int FMT>
+struct CastNorm {
+  const void *w, *b;
+  int wf32;
+  const float *mean, *rstd;
+};
+// 8 columns of a norm parameter (`none` where the pointer is NULL)
+__device__ __forceinline__ void load_param8(float (&f)[8], const void *p, int wf32, float none,
+                                            int c) {
+  if (!p) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = none;
+  } else if (wf32) {
+    const float4 *v = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + c);
+    const float4 a = v[0], b = v[1];
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  } else {
+    const U4 v = load16(static_cast<const uint16_t *>(p) + c);
+    f[0] = bf16_to_f32(v.x & 0xFFFFu); f[1] = bf16_to_f32(v.x >> 16);
+    f[2] = bf16_to_f32(v.y & 0xFFFFu); f[3] = bf16_to_f32(v.y >> 16);
+    f[4] = bf16_to_f32(v.z & 0xFFFFu); f[5] = bf16_to_f32(v.z >> 16);
+    f[6] = bf16_to_f32(v.w & 0xFFFFu); f[7] = bf16_to_f32(v.w >> 16);
+  }
+}
+template <int MODE, int FMT, bool NORM = false>
 __global__ __launch_bounds__(CT_THREADS) void k_cast_transpose(
     const uint16_t *__restrict__ x, int rows, int cols, int tiles_c,
     float *__restrict__ scale, float *__restrict__ scale_t,
     const uint32_t *__restrict__ part, int nparts, float *__restrict__ amax_out,
-    uint8_t *__restrict__ q, uint8_t *__restrict__ qt) {
+    uint8_t *__restrict__ q, uint8_t *__restrict__ qt, CastNorm nm) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[CT_T * CT_T];
   const int tid = threadIdx.x;
   // block -> (tile_r, tile_c): groups of CT_GROUP row tiles (the last one
@@ -333,6 +359,12 @@ __global__ __launch_bounds__(CT_THREADS) void k_cast_transpose(
     }
   }
 
+  float nw[8], nb[8];             // NORM: weight and bias of the 8 columns
+  if (NORM) {
+    load_param8(nw, nm.w, nm.wf32, 1.f, col_ok ? c : 0);
+    load_param8(nb, nm.b, nm.wf32, 0.f, col_ok ? c : 0);
+  }
+
 #pragma unroll
   for (int pass = 0; pass < CT_PASSES; ++pass) {
     const int rl = pass * (CT_THREADS / 4) + rg * 4;   // local row of the 4-row group
@@ -360,6 +392,16 @@ __global__ __launch_bounds__(CT_THREADS) void k_cast_transpose(
         f[2] = bf16_to_f32(v.y & 0xFFFFu); f[3] = bf16_to_f32(v.y >> 16);
         f[4] = bf16_to_f32(v.z & 0xFFFFu); f[5] = bf16_to_f32(v.z >> 16);
         f[6] = bf16_to_f32(v.w & 0xFFFFu); f[7] = bf16_to_f32(v.w >> 16);
+        if (NORM) {
+          const float m = nm.mean ? nm.mean[r + j] : 0.f, rs = nm.rstd[r + j];
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const uint32_t y = bf16x2_bits(norm_value(f[e], m, rs, nw[e], nb[e]),
+                                           norm_value(f[e + 1], m, rs, nw[e + 1], nb[e + 1]));
+            f[e] = bf16_to_f32(y & 0xFFFFu);
+            f[e + 1] = bf16_to_f32(y >> 16);
+          }
+        }
         const float s = srs[j];
         const uint32_t q0 = fp8x4<FMT>(f[0] * s, f[1] * s, f[2] * s, f[3] * s);
         const uint32_t q1 = fp8x4<FMT>(f[4] * s, f[5] * s, f[6] * s, f[7] * s);
@@ -476,41 +518,61 @@ size_t quantize_workspace_bytes(int64_t rows, int64_t cols, int scaling) {
 
 namespace {
 
-template <int FMT>
-hipError_t finish_fmt(const void *x, int64_t rows, int64_t cols, bool rowwise, int nparts,
-                      void *q, void *qt, float *scale, float *scale_t, float *amax_out,
-                      void *workspace, hipStream_t stream) {
-  const uint16_t *xb = static_cast<const uint16_t *>(x);
+template <int FMT, bool NORM>
+hipError_t cast_fmt(const CastSource &src, int64_t rows, int64_t cols, bool rowwise,
+                    const Fp8Out &o, hipStream_t stream) {
+  const uint16_t *xb = static_cast<const uint16_t *>(src.x);
   const int R = (int)rows, C = (int)cols;
+  const CastNorm nm = {src.w, src.b, src.wf32, src.mean, src.rstd};
   if (rowwise) {
-    const AmaxGeom g = amax_geom(rows, cols);
-    uint16_t *rowpart, *colpart;
-    quantize_rowwise_partials(workspace, rows, cols, &rowpart, &colpart);
     const int64_t nbr = cdiv(rows, FR_OUT), nbc = cdiv(cols, FR_OUT);
     if (nbr + nbc > 0)
       hipLaunchKernelGGL(k_finalize_rowwise<FMT>, dim3((unsigned)(nbr + nbc)), dim3(256), 0,
-                         stream, rowpart, colpart, R, C, (int)g.tiles_c, (int)g.tiles_r,
-                         (int)nbr, scale, scale_t, amax_out);
-  } else if (nparts == 0) {
-    hipLaunchKernelGGL(k_finalize_tw_empty<FMT>, dim3(1), dim3(64), 0, stream, scale,
-                       scale_t, amax_out);
+                         stream, src.rowpart, src.colpart, R, C, src.row_slices, src.col_slices,
+                         (int)nbr, o.scale, o.scale_t, o.amax);
+  } else if (src.nparts == 0) {
+    hipLaunchKernelGGL(k_finalize_tw_empty<FMT>, dim3(1), dim3(64), 0, stream, o.scale,
+                       o.scale_t, o.amax);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t ct_r = cdiv(rows, CT_T), ct_c = cdiv(cols, CT_T);
   if (ct_r * ct_c > 0) {
     if (!rowwise)
-      hipLaunchKernelGGL((k_cast_transpose<MODE_TW, FMT>), dim3((unsigned)(ct_r * ct_c)),
-                         dim3(CT_THREADS), 0, stream, xb, R, C, (int)ct_c, scale, scale_t,
-                         static_cast<const uint32_t *>(workspace), nparts, amax_out,
-                         static_cast<uint8_t *>(q), static_cast<uint8_t *>(qt));
+      hipLaunchKernelGGL((k_cast_transpose<MODE_TW, FMT, NORM>), dim3((unsigned)(ct_r * ct_c)),
+                         dim3(CT_THREADS), 0, stream, xb, R, C, (int)ct_c, o.scale, o.scale_t,
+                         src.part, src.nparts, o.amax, static_cast<uint8_t *>(o.q),
+                         static_cast<uint8_t *>(o.qt), nm);
     else
-      hipLaunchKernelGGL((k_cast_transpose<MODE_RW, FMT>), dim3((unsigned)(ct_r * ct_c)),
-                         dim3(CT_THREADS), 0, stream, xb, R, C, (int)ct_c, scale, scale_t,
-                         nullptr, 0, nullptr, static_cast<uint8_t *>(q),
-                         static_cast<uint8_t *>(qt));
+      hipLaunchKernelGGL((k_cast_transpose<MODE_RW, FMT, NORM>), dim3((unsigned)(ct_r * ct_c)),
+                         dim3(CT_THREADS), 0, stream, xb, R, C, (int)ct_c, o.scale, o.scale_t,
+                         nullptr, 0, nullptr, static_cast<uint8_t *>(o.q),
+                         static_cast<uint8_t *>(o.qt), nm);
   }
   return hipGetLastError();
+}
+
+// the partial maxima where quantize_launch's own first pass puts them
+template <int FMT>
+hipError_t finish_fmt(const void *x, int64_t rows, int64_t cols, bool rowwise, int nparts,
+                      void *q, void *qt, float *scale, float *scale_t, float *amax_out,
+                      void *workspace, hipStream_t stream) {
+  CastSource src = {};
+  src.x = x;
+  if (rowwise) {
+    const AmaxGeom g = amax_geom(rows, cols);
+    uint16_t *rowpart, *colpart;
+    quantize_rowwise_partials(workspace, rows, cols, &rowpart, &colpart);
+    src.rowpart = rowpart;
+    src.colpart = colpart;
+    src.row_slices = (int)g.tiles_c;
+    src.col_slices = (int)g.tiles_r;
+  } else {
+    src.part = static_cast<const uint32_t *>(workspace);
+    src.nparts = nparts;
+  }
+  const Fp8Out o = {q, qt, scale, scale_t, amax_out};
+  return cast_fmt<FMT, false>(src, rows, cols, rowwise, o, stream);
 }
 
 // first pass (amax partial maxima of x), then the second half
@@ -593,8 +655,17 @@ hipError_t quantize_scaled_launch(const void *x, int64_t rows, int64_t cols,
     hipLaunchKernelGGL((k_cast_transpose<MODE_GIVEN, 0>), dim3((unsigned)(ct_r * ct_c)),
                        dim3(CT_THREADS), 0, stream, static_cast<const uint16_t *>(x), (int)rows,
                        (int)cols, (int)ct_c, const_cast<float *>(scale), nullptr, nullptr, 0,
-                       nullptr, static_cast<uint8_t *>(q), static_cast<uint8_t *>(qt));
+                       nullptr, static_cast<uint8_t *>(q), static_cast<uint8_t *>(qt),
+                       CastNorm{});
   return hipGetLastError();
+}
+
+hipError_t quantize_cast_launch(const CastSource &src, int64_t rows, int64_t cols, int scaling,
+                                const Fp8Out &o, hipStream_t stream) {
+  const bool rw = (scaling & FP8L_ROWWISE) != 0;
+  if (src.rstd) return cast_fmt<0, true>(src, rows, cols, rw, o, stream);  // norms: E4M3 only
+  if (scaling & FP8L_E5M2) return cast_fmt<1, false>(src, rows, cols, rw, o, stream);
+  return cast_fmt<0, false>(src, rows, cols, rw, o, stream);
 }
 
 hipError_t encode_launch(const float *in, uint8_t *out, int64_t n, int fmt,

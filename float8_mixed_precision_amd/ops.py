@@ -26,12 +26,16 @@ EXPORTS = ("fp8_linear_workspace_bytes", "fp8_linear_quantize",
            "fp8_linear_quantize_noalloc", "fp8_linear_amax",
            "fp8_linear_quantize_scaled", "fp8_linear_fwd", "fp8_linear_bwd",
            "fp8_linear_bwd_w_f32", "fp8_linear_bwd_x_acc", "fp8_linear_gemm_grouped",
-           "fp8_linear_encode_e4m3",
+           "fp8_layernorm_workspace_bytes", "fp8_layernorm_fwd", "fp8_layernorm_quantize",
+           "fp8_layernorm_bwd", "fp8_linear_encode_e4m3",
            "fp8_linear_encode_e5m2", "fp8_swiglu_workspace_bytes", "fp8_swiglu_fwd",
            "fp8_swiglu_bwd", "fp8_linear_status_string", "fp8_linear_version")
 
 
 FP8L_MAX_GROUP = 4
+FP8L_LAYERNORM, FP8L_RMSNORM = 0, 1
+FP8L_BF16, FP8L_F32 = 0, 1
+FP8L_NORM_MAX_COLS = 16384
 
 
 class GemmProblem(ctypes.Structure):
@@ -87,6 +91,16 @@ def lib() -> ctypes.CDLL:
     L.fp8_swiglu_bwd.restype = I
     L.fp8_swiglu_bwd.argtypes = ([P, P, P, i64, i64, I, P, P] + [P] * 10
                                  + [P, ctypes.c_size_t, P])
+    F = ctypes.c_float
+    L.fp8_layernorm_workspace_bytes.restype = ctypes.c_size_t
+    L.fp8_layernorm_workspace_bytes.argtypes = [i64, i64, I]
+    L.fp8_layernorm_fwd.restype = I
+    L.fp8_layernorm_fwd.argtypes = [P, i64, i64, I, I, P, P, I, F, P, P, P, P]
+    L.fp8_layernorm_quantize.restype = I
+    L.fp8_layernorm_quantize.argtypes = ([P, i64, i64, I, P, P, I, F, I] + [P] * 8
+                                         + [P, ctypes.c_size_t, P])
+    L.fp8_layernorm_bwd.restype = I
+    L.fp8_layernorm_bwd.argtypes = ([P] * 5 + [i64, i64, I, I, I, P, P, P, P, ctypes.c_size_t, P])
     L.fp8_linear_encode_e4m3.restype = I
     L.fp8_linear_encode_e4m3.argtypes = [P, P, i64, P]
     L.fp8_linear_encode_e5m2.restype = I
@@ -346,6 +360,168 @@ def fp8_swiglu_bwd(dh: torch.Tensor, a: torch.Tensor, b: torch.Tensor, rowwise: 
                                 _p(qb.scale_t), _p(qb.amax), _p(workspace), workspace.numel(),
                                 _stream(stream)), "fp8_swiglu_bwd")
     return da, db, qa, qb
+
+
+# ------------------------------------------------------------ layer norm --
+
+_DTYPES = {torch.bfloat16: FP8L_BF16, torch.float32: FP8L_F32}
+
+
+class _on_device:
+    """Makes the device of tensor t current around a call (a default stream
+    is that of the current device) and checks that the other tensors given
+    (None allowed) are on it, dense, and of the stated type and shape."""
+
+    def __init__(self, t, **tensors):
+        for name, (u, dtype, shape) in tensors.items():
+            if u is None:
+                continue
+            if u.device != t.device:
+                raise ValueError("%s is on %s, not on %s" % (name, u.device, t.device))
+            if u.dtype != dtype or tuple(u.shape) != tuple(shape):
+                raise ValueError("%s must be %s %s, not %s %s" % (
+                    name, dtype, tuple(shape), u.dtype, tuple(u.shape)))
+            if not u.is_contiguous():
+                raise ValueError("%s must be contiguous" % name)
+        self.guard = (torch.cuda.device(t.device)
+                      if t.device.type == "cuda"
+                      and t.device.index != torch.cuda.current_device() else None)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *a):
+        if self.guard is not None:
+            self.guard.__exit__(*a)
+
+
+def _norm_params(x, weight, bias):
+    """Checked dtypes of a norm call: (type of x, type of weight and bias)."""
+    if x.dim() != 2 or x.dtype not in _DTYPES:
+        raise ValueError("x must be a [rows, cols] bf16 or fp32 matrix")
+    ps = [p for p in (weight, bias) if p is not None]
+    if any(p.dtype != ps[0].dtype or p.dtype not in _DTYPES for p in ps):
+        raise ValueError("weight and bias must be both bf16 or both fp32")
+    return x.dtype, ps[0].dtype if ps else torch.float32
+
+
+def fp8_layernorm_workspace_bytes(rows: int, cols: int, rowwise: bool = False) -> int:
+    return int(lib().fp8_layernorm_workspace_bytes(rows, cols, _scaling(rowwise)))
+
+
+def alloc_layernorm_workspace(rows: int, cols: int, device, rowwise: bool = False) -> torch.Tensor:
+    """Workspace of fp8_layernorm_quantize (with this scaling) and
+    fp8_layernorm_bwd for an x of [rows, cols]; needs no clearing."""
+    return torch.empty(max(fp8_layernorm_workspace_bytes(rows, cols, rowwise), 256),
+                       dtype=torch.uint8, device=device)
+
+
+def fp8_layernorm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                      bias: Optional[torch.Tensor] = None, eps: float = 1e-5, rms: bool = False,
+                      y: Optional[torch.Tensor] = None, mean: Optional[torch.Tensor] = None,
+                      rstd: Optional[torch.Tensor] = None, stream=None):
+    """(y, mean, rstd) of the layer norm of x [rows, cols] (bf16 or fp32; the
+    RMS form with ``rms``, whose mean is None): y in x's type, the
+    statistics fp32 [rows], kept for fp8_layernorm_bwd."""
+    xd, pd = _norm_params(x, weight, bias)
+    rows, cols = x.shape
+    f32 = torch.float32
+    with _on_device(x, x=(x, xd, x.shape), weight=(weight, pd, (cols,)), bias=(bias, pd, (cols,)),
+                    y=(y, xd, x.shape), mean=(mean, f32, (rows,)), rstd=(rstd, f32, (rows,))):
+        if y is None:
+            y = torch.empty_like(x)
+        if mean is None and not rms:
+            mean = torch.empty(rows, dtype=f32, device=x.device)
+        if rstd is None:
+            rstd = torch.empty(rows, dtype=f32, device=x.device)
+        _check(lib().fp8_layernorm_fwd(
+            _p(x), rows, cols, int(rms), _DTYPES[xd], _p(weight), _p(bias), _DTYPES[pd], eps,
+            _p(y), None if rms else _p(mean), _p(rstd), _stream(stream)), "fp8_layernorm_fwd")
+    return y, None if rms else mean, rstd
+
+
+def fp8_layernorm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                           bias: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                           rms: bool = False, rowwise: bool = False, transposed: bool = True,
+                           y: Optional[torch.Tensor] = None, mean: Optional[torch.Tensor] = None,
+                           rstd: Optional[torch.Tensor] = None, out: Optional[Quantized] = None,
+                           workspace: Optional[torch.Tensor] = None, want_stats: bool = True,
+                           stream=None):
+    """(Quantized, mean, rstd): the E4M3 quantize of the layer norm of a bf16
+    x [rows, cols].  The normed y itself is stored only if a tensor ``y`` is
+    given for it.  transposed=False (rowwise only) is the serving form: the
+    codes and scales of each row alone, any number of rows; there
+    want_stats=False leaves mean and rstd out (None)."""
+    _, pd = _norm_params(x, weight, bias)
+    rows, cols = x.shape
+    if not transposed and not rowwise:
+        raise ValueError("codes without their transposed copy are rowwise")
+    bf, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
+    ns, nst = (rows, cols) if rowwise else (1, 1)
+    na = rows if not transposed else rows + cols if rowwise else 1
+    dev = x.device
+    if out is None:
+        if transposed:
+            out = alloc_quantized(rows, cols, rowwise, dev)
+        else:
+            out = Quantized(torch.empty((rows, cols), dtype=u8, device=dev), None,
+                            torch.empty(rows, dtype=f32, device=dev), None,
+                            torch.empty(rows, dtype=f32, device=dev))
+    if transposed or want_stats:
+        if mean is None and not rms:
+            mean = torch.empty(rows, dtype=f32, device=dev)
+        if rstd is None:
+            rstd = torch.empty(rows, dtype=f32, device=dev)
+    with _on_device(x, x=(x, bf, x.shape), weight=(weight, pd, (cols,)), bias=(bias, pd, (cols,)),
+                    y=(y, bf, x.shape), mean=(mean, f32, (rows,)), rstd=(rstd, f32, (rows,)),
+                    q=(out.q, u8, (rows, cols)),
+                    qt=(out.qt if transposed else None, u8, (cols, rows)),
+                    scale=(out.scale, f32, (ns,)),
+                    scale_t=(out.scale_t if transposed else None, f32, (nst,)),
+                    amax=(out.amax, f32, (na,))):
+        if transposed and workspace is None:
+            workspace = alloc_layernorm_workspace(rows, cols, dev, rowwise)
+        _check(lib().fp8_layernorm_quantize(
+            _p(x), rows, cols, int(rms), _p(weight), _p(bias), _DTYPES[pd], eps,
+            _scaling(rowwise), _p(y), None if rms else _p(mean), _p(rstd), _p(out.q),
+            _p(out.qt) if transposed else None, _p(out.scale),
+            _p(out.scale_t) if transposed else None, _p(out.amax), _p(workspace),
+            workspace.numel() if workspace is not None else 0, _stream(stream)),
+            "fp8_layernorm_quantize")
+    return out, None if rms else mean, rstd
+
+
+def fp8_layernorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor],
+                      mean: Optional[torch.Tensor], rstd: torch.Tensor, rms: bool = False,
+                      dx: Optional[torch.Tensor] = None, dweight: Optional[torch.Tensor] = None,
+                      dbias: Optional[torch.Tensor] = None, want_x: bool = True,
+                      want_w: bool = True, want_b: bool = True,
+                      workspace: Optional[torch.Tensor] = None, stream=None):
+    """(dx, dweight, dbias) of the layer norm for the gradient dy of y: dx in
+    x's type, dweight and dbias fp32 [cols]; None where not wanted."""
+    xd, pd = _norm_params(x, weight, None)
+    rows, cols = x.shape
+    f32, dev = torch.float32, x.device
+    with _on_device(x, x=(x, xd, x.shape), dy=(dy, xd, x.shape), weight=(weight, pd, (cols,)),
+                    mean=(mean, f32, (rows,)), rstd=(rstd, f32, (rows,)), dx=(dx, xd, x.shape),
+                    dweight=(dweight, f32, (cols,)), dbias=(dbias, f32, (cols,))):
+        if want_x and dx is None:
+            dx = torch.empty_like(x)
+        if want_w and dweight is None:
+            dweight = torch.empty(cols, dtype=f32, device=dev)
+        if want_b and dbias is None:
+            dbias = torch.empty(cols, dtype=f32, device=dev)
+        dx, dweight, dbias = (dx if want_x else None, dweight if want_w else None,
+                              dbias if want_b else None)
+        if workspace is None and (want_w or want_b):
+            workspace = alloc_layernorm_workspace(rows, cols, dev)
+        _check(lib().fp8_layernorm_bwd(
+            _p(dy), _p(x), _p(weight), None if rms else _p(mean), _p(rstd), rows, cols, int(rms),
+            _DTYPES[xd], _DTYPES[pd], _p(dx), _p(dweight), _p(dbias), _p(workspace),
+            workspace.numel() if workspace is not None else 0, _stream(stream)),
+            "fp8_layernorm_bwd")
+    return dx, dweight, dbias
 
 
 def fp8_linear_encode_e4m3(x: torch.Tensor, out: Optional[torch.Tensor] = None,

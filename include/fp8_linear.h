@@ -354,6 +354,89 @@ FP8L_API int fp8_swiglu_bwd(const void *dh, const void *a, const void *b, int64_
                             void *stream);
 
 /*
+ * Layer norm, and its RMS form: the norm in front of the feed-forward block,
+ * as the producer of the fp8 operand that the block's first linears read.
+ *
+ *   mean = sum_c x[r][c] / cols                         (FP8L_RMSNORM: 0)
+ *   rstd = 1 / sqrt( sum_c (x[r][c] - mean)^2 / cols + eps )
+ *   y[r][c] = (x[r][c] - mean) rstd w[c] + b[c]
+ *
+ * computed in fp32 (the variance about the mean) and rounded once to y's
+ * type.  A row that holds a NaN or an infinity gives NaN in that row only.
+ *
+ *   kind      FP8L_LAYERNORM or FP8L_RMSNORM
+ *   dtype     FP8L_BF16 or FP8L_F32: type of x and y (and dy, dx)
+ *   pdtype    FP8L_BF16 or FP8L_F32: type of weight and bias
+ *   weight    [cols], or NULL for 1;  bias [cols], or NULL for 0
+ *   eps       finite, >= 0
+ *   mean, rstd [rows] fp32 (written; either may be NULL where not wanted;
+ *             FP8L_RMSNORM does not write mean)
+ *
+ * Norms take any number of rows, and any 1 <= cols <= FP8L_NORM_MAX_COLS
+ * except where codes are written (multiples of 16): FP8L_ESHAPE otherwise.
+ * x, y, dy, dx, weight and bias need 16-byte alignment, as every tensor.
+ * Outputs must not overlap inputs or one another.
+ */
+#define FP8L_LAYERNORM 0
+#define FP8L_RMSNORM   1
+#define FP8L_BF16      0
+#define FP8L_F32       1
+#define FP8L_NORM_MAX_COLS 16384
+
+/*
+ * Bytes of device workspace that fp8_layernorm_quantize with this scaling
+ * and fp8_layernorm_bwd need for an x of [rows, cols] (one size serves
+ * both); 0 for invalid arguments.
+ */
+FP8L_API size_t fp8_layernorm_workspace_bytes(int64_t rows, int64_t cols, int scaling);
+
+/* y (and mean, rstd) of x. */
+FP8L_API int fp8_layernorm_fwd(const void *x, int64_t rows, int64_t cols, int kind, int dtype,
+                               const void *weight, const void *bias, int pdtype, float eps,
+                               void *y, float *mean, float *rstd, void *stream);
+
+/*
+ * The norm of a bf16 x with fp8_linear_quantize's definition applied to the
+ * bf16 y: codes E4M3, scaling FP8L_TENSORWISE or FP8L_ROWWISE.
+ *
+ *   q, qt, scale, scale_t, amax_out  as fp8_linear_quantize's for x = y
+ *   y    [rows, cols] bf16 (written), or NULL where only the codes are
+ *        wanted: y is then never stored, and mean (FP8L_LAYERNORM) and rstd
+ *        must be given, since the cast reads them back
+ *   qt = NULL (FP8L_ROWWISE only): no transposed copy and no scale_t, for
+ *        serving; amax_out is then [rows], any number of rows is valid, the
+ *        workspace is not used (it may be NULL), and y, mean and rstd are
+ *        all optional
+ * With qt, rows is a multiple of 16; cols always is.
+ */
+FP8L_API int fp8_layernorm_quantize(const void *x, int64_t rows, int64_t cols, int kind,
+                                    const void *weight, const void *bias, int pdtype, float eps,
+                                    int scaling, void *y, float *mean, float *rstd, void *q,
+                                    void *qt, float *scale, float *scale_t, float *amax_out,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of the norm, from dy and the forward pass's x, mean and rstd
+ * (xh = (x - mean) rstd, g = dy w; bias does not enter):
+ *
+ *   dx[r][c]   = rstd ( g - sum_c g / cols - xh sum_c (g xh) / cols )
+ *                (FP8L_RMSNORM: without the first sum)
+ *   dweight[c] = sum_r dy xh,   dbias[c] = sum_r dy       (fp32)
+ *
+ * dx, dweight and dbias may each be NULL to skip it (not all three).  mean
+ * may be NULL for FP8L_RMSNORM.  The order of the sums over rows is fixed:
+ * equal calls give equal bits.  With no rows dweight and dbias are zeros.
+ * The workspace holds partial sums (not needed when dweight and dbias are
+ * both NULL); contents undefined on entry and exit, not shared by calls in
+ * flight together.
+ */
+FP8L_API int fp8_layernorm_bwd(const void *dy, const void *x, const void *weight,
+                               const float *mean, const float *rstd, int64_t rows, int64_t cols,
+                               int kind, int dtype, int pdtype, void *dx, float *dweight,
+                               float *dbias, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/*
  * The element conversion the quantize kernels use, exposed for testing it on
  * every fp32 input: out[i] = e4m3_sat_rne(in[i]) (definition above; a NaN
  * input gives a NaN code).  in: n fp32, out: n bytes, both device pointers.
