@@ -9,7 +9,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libfp8linear.so")
-SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "swiglu.hip", "norm.hip"]
+SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "swiglu.hip"]
 # measurement support, kept out of the method's library: the MFMA-only
 # throughput and one-instruction probes, and the HBM streaming probes that
 # bench.py reports beside the rooflines

@@ -183,7 +183,7 @@ struct CastSource {
 hipError_t quantize_cast_launch(const CastSource &src, int64_t rows, int64_t cols, int scaling,
                                 const Fp8Out &o, hipStream_t stream);
 
-// Layer norm (norm.hip).  w, b: bf16, or fp32 with wf32; NULL for 1 and 0.
+// Layer norm (norm.h).  w, b: bf16, or fp32 with wf32; NULL for 1 and 0.
 struct NormIn {
   const void *x;
   const void *w, *b;

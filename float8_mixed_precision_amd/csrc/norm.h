@@ -24,6 +24,11 @@
 // (quantize.hip) reads x again, mostly from the Infinity Cache, and
 // normalizes it once more: y itself is neither written nor read unless the
 // caller asks for it.
+//
+// Part of quantize.hip (included at its end): the norm is the first half of
+// a quantize.
+#pragma once
+
 #include "fp8l_internal.h"
 
 #include <type_traits>
@@ -31,10 +36,10 @@
 namespace fp8l {
 namespace {
 
-constexpr int MODE_Y = 0;      // y
-constexpr int MODE_ROWS = 1;   // y (optional), codes and scale of each row
-constexpr int MODE_TW = 2;     // y (optional), one |y| maximum per workgroup
-constexpr int MODE_RW = 3;     // y (optional), row maxima, column maxima per workgroup
+constexpr int NORM_Y = 0;      // y
+constexpr int NORM_ROWS = 1;   // y (optional), codes and scale of each row
+constexpr int NORM_TW = 2;     // y (optional), one |y| maximum per workgroup
+constexpr int NORM_RW = 3;     // y (optional), row maxima, column maxima per workgroup
 
 struct NormArgs {
   const void *x;
@@ -46,10 +51,10 @@ struct NormArgs {
   int cols;
   void *y;
   float *mean, *rstd;
-  uint8_t *q;                  // MODE_ROWS
+  uint8_t *q;                  // NORM_ROWS
   float *scale, *amax;
-  uint32_t *part;              // MODE_TW
-  uint16_t *rowpart, *colpart; // MODE_RW: [rows], [gridDim.x][cols]
+  uint32_t *part;              // NORM_TW
+  uint16_t *rowpart, *colpart; // NORM_RW: [rows], [gridDim.x][cols]
 };
 
 // Eight values of a row held by a thread, as loaded.
@@ -294,7 +299,7 @@ template <class T, int LAY, int TPR, int CH, int MODE>
 __global__ __launch_bounds__(block_threads<TPR>()) void k_norm(NormArgs p) {
   constexpr int G = block_threads<TPR>() / TPR;
   constexpr bool BF = sizeof(T) == 2;
-  static_assert(MODE == MODE_Y || (BF && LAY == LAY_ALIGNED), "codes come from bf16 rows of whole chunks");
+  static_assert(MODE == NORM_Y || (BF && LAY == LAY_ALIGNED), "codes come from bf16 rows of whole chunks");
   __shared__ float red[2][16];
   __shared__ uint32_t redu[16];
   const int t = threadIdx.x % TPR;
@@ -353,25 +358,25 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_norm(NormArgs p) {
         for (int j = 0; j < 4; ++j) yb[k][j] = bf16x2_bits(f[2 * j], f[2 * j + 1]);
         if (p.y && ok)
           store_chunk<LAY, TPR>(static_cast<uint16_t *>(p.y) + r * cols, yb[k], k, t, cols);
-        if (MODE != MODE_Y) {
+        if (MODE != NORM_Y) {
           const uint32_t keep =
               ok && chunk_start<TPR>(k, t) < cols ? 0x7FFF7FFFu : 0u;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint32_t m = yb[k][j] & keep;
             rm = max_u16x2(rm, m);
-            if (MODE == MODE_RW) cm[k][j] = max_u16x2(cm[k][j], m);
+            if (MODE == NORM_RW) cm[k][j] = max_u16x2(cm[k][j], m);
           }
         }
       } else {
         if (ok) store_chunk<LAY, TPR>(static_cast<float *>(p.y) + r * cols, f, k, t, cols);
       }
     }
-    if (MODE == MODE_TW) tw_max = max_u16x2(tw_max, rm);
-    if (MODE == MODE_RW || MODE == MODE_ROWS) {
+    if (MODE == NORM_TW) tw_max = max_u16x2(tw_max, rm);
+    if (MODE == NORM_RW || MODE == NORM_ROWS) {
       const uint32_t am = row_umax<TPR>(hmax16(rm), redu);
-      if (MODE == MODE_RW && t == 0 && ok) p.rowpart[r] = (uint16_t)am;
-      if (MODE == MODE_ROWS) {
+      if (MODE == NORM_RW && t == 0 && ok) p.rowpart[r] = (uint16_t)am;
+      if (MODE == NORM_ROWS) {
         const float a = bf16_to_f32(am);
         const float s = scale_from_amax<0>(a);
         if (t == 0 && ok) {
@@ -393,7 +398,7 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_norm(NormArgs p) {
       }
     }
   }
-  if (MODE == MODE_TW) {
+  if (MODE == NORM_TW) {
     __shared__ uint32_t tw[16];
     const uint32_t m = wave_umax(hmax16(tw_max));
     if ((threadIdx.x & 63) == 0) tw[threadIdx.x >> 6] = m;
@@ -405,7 +410,7 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_norm(NormArgs p) {
       p.part[blockIdx.x] = a;
     }
   }
-  if (MODE == MODE_RW) {
+  if (MODE == NORM_RW) {
     // the column maxima of the workgroup's row groups meet in LDS (integer
     // maxima: any order gives the same result)
     constexpr int SPAN = TPR * 8 * CH;            // columns a group covers
@@ -622,8 +627,6 @@ __global__ __launch_bounds__(64 * FIN_SLICES) void k_norm_bwd_finish(
   }
 }
 
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 // ---------------------------------------------------------------- launch --
 
 constexpr int kComputeUnits = 256;
@@ -756,8 +759,8 @@ hipError_t norm_fwd_launch(const NormIn &in, int f32, void *y, float *mean, floa
   int nb;
   return with_layout(in.cols, [&](auto lay) {
     constexpr int LAY = decltype(lay)::value;
-    return f32 ? launch_norm<float, LAY, MODE_Y>(a, kMaxBlocks, &nb, stream)
-               : launch_norm<uint16_t, LAY, MODE_Y>(a, kMaxBlocks, &nb, stream);
+    return f32 ? launch_norm<float, LAY, NORM_Y>(a, kMaxBlocks, &nb, stream)
+               : launch_norm<uint16_t, LAY, NORM_Y>(a, kMaxBlocks, &nb, stream);
   });
 }
 
@@ -769,7 +772,7 @@ hipError_t norm_rows_launch(const NormIn &in, void *y, float *mean, float *rstd,
   a.scale = scale;
   a.amax = amax_out;
   int nb;
-  return launch_norm<uint16_t, LAY_ALIGNED, MODE_ROWS>(a, kMaxBlocks, &nb, stream);
+  return launch_norm<uint16_t, LAY_ALIGNED, NORM_ROWS>(a, kMaxBlocks, &nb, stream);
 }
 
 hipError_t norm_quantize_launch(const NormIn &in, int scaling, void *y, float *mean, float *rstd,
@@ -791,8 +794,8 @@ hipError_t norm_quantize_launch(const NormIn &in, int scaling, void *y, float *m
   }
   if (in.rows > 0) {
     const hipError_t e =
-        rw ? launch_norm<uint16_t, LAY_ALIGNED, MODE_RW>(a, kMaxSlices, &nb, stream)
-           : launch_norm<uint16_t, LAY_ALIGNED, MODE_TW>(a, TW_MAX_BLOCKS, &nb, stream);
+        rw ? launch_norm<uint16_t, LAY_ALIGNED, NORM_RW>(a, kMaxSlices, &nb, stream)
+           : launch_norm<uint16_t, LAY_ALIGNED, NORM_TW>(a, TW_MAX_BLOCKS, &nb, stream);
     if (e != hipSuccess) return e;
   }
   if (rw) src.col_slices = nb;

@@ -681,3 +681,5 @@ hipError_t encode_launch(const float *in, uint8_t *out, int64_t n, int fmt,
 }
 
 }  // namespace fp8l
+
+#include "norm.h"
