@@ -357,6 +357,69 @@ int fp8_swiglu_bwd(const void *dh, const void *a, const void *b, int64_t rows, i
   return e == hipSuccess ? FP8L_OK : FP8L_EHIP;
 }
 
+size_t fp8_gated_workspace_bytes(int64_t M, int64_t H, int scaling) {
+  if (M < 0 || M > (int64_t)1 << 30 || bad_dim(H) || bad_scaling(scaling)) return 0;
+  return fp8l::gated_workspace_bytes(M, H, scaling);
+}
+
+int fp8_gated_fwd(const void *xq, const float *sx, const void *w1q, const float *sw1,
+                  const void *w3q, const float *sw3, int64_t M, int64_t H, int64_t K, int scaling,
+                  void *a, void *b, void *h, void *hq, void *hqt, float *scale, float *scale_t,
+                  float *amax_out, void *workspace, size_t workspace_bytes, void *stream) {
+  if (scaling != FP8L_TENSORWISE && scaling != FP8L_ROWWISE) return FP8L_EINVAL;
+  if (M < 0 || M > (int64_t)1 << 30 || bad_dim(H) || bad_dim(K)) return FP8L_ESHAPE;
+  if (bad_gemm_sizes(M, H, K)) return FP8L_ESHAPE;
+  const bool quant = hq || hqt || scale || scale_t || amax_out;
+  if (quant && M % 16 != 0) return FP8L_ESHAPE;
+  int s = check_gemm_operands(xq, sx, w1q, sw1, h, M, H, K);
+  if (s == FP8L_OK) s = check_gemm_operands(xq, sx, w3q, sw3, h, M, H, K);
+  if (s != FP8L_OK) return s;
+  if (M * H > 0 && !a != !b) return FP8L_EINVAL;
+  if (misaligned(a) || misaligned(b)) return FP8L_EALIGN;
+  if (quant) {
+    s = check_quantize_args(h, M, H, scaling, hq, hqt, scale, scale_t, amax_out);
+    if (s != FP8L_OK) return s;
+    if (!workspace) return FP8L_EINVAL;
+    if (workspace_bytes < fp8l::gated_workspace_bytes(M, H, scaling)) return FP8L_EWORKSPACE;
+    if (misaligned(workspace)) return FP8L_EALIGN;
+  }
+  const fp8l::Fp8Out o = {hq, hqt, scale, scale_t, amax_out};
+  hipError_t e = fp8l::gated_fwd_launch(
+      static_cast<const uint8_t *>(xq), sx, static_cast<const uint8_t *>(w1q), sw1,
+      static_cast<const uint8_t *>(w3q), sw3, M, H, K, scaling, static_cast<uint16_t *>(a),
+      static_cast<uint16_t *>(b), static_cast<uint16_t *>(h), quant ? &o : nullptr, workspace,
+      static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FP8L_OK : FP8L_EHIP;
+}
+
+int fp8_gated_bwd(const void *dyq, const float *sdy, const void *w2tq, const float *sw2t,
+                  const void *a, const void *b, int64_t M, int64_t H, int64_t D, int scaling,
+                  void *da, void *db, void *daq, void *daqt, float *da_scale, float *da_scale_t,
+                  float *da_amax, void *dbq, void *dbqt, float *db_scale, float *db_scale_t,
+                  float *db_amax, void *workspace, size_t workspace_bytes, void *stream) {
+  if (bad_scaling(scaling)) return FP8L_EINVAL;
+  if (bad_dim(M) || bad_dim(H) || bad_dim(D)) return FP8L_ESHAPE;
+  if (bad_gemm_sizes(M, H, D)) return FP8L_ESHAPE;
+  int s = check_gemm_operands(dyq, sdy, w2tq, sw2t, da, M, H, D);
+  if (s == FP8L_OK)
+    s = check_quantize_args(da, M, H, scaling, daq, daqt, da_scale, da_scale_t, da_amax);
+  if (s == FP8L_OK)
+    s = check_quantize_args(db, M, H, scaling, dbq, dbqt, db_scale, db_scale_t, db_amax);
+  if (s != FP8L_OK) return s;
+  if (M * H > 0 && (!a || !b)) return FP8L_EINVAL;
+  if (!workspace) return FP8L_EINVAL;
+  if (workspace_bytes < fp8l::gated_workspace_bytes(M, H, scaling)) return FP8L_EWORKSPACE;
+  if (misaligned(a) || misaligned(b) || misaligned(workspace)) return FP8L_EALIGN;
+  const fp8l::Fp8Out qa = {daq, daqt, da_scale, da_scale_t, da_amax};
+  const fp8l::Fp8Out qb = {dbq, dbqt, db_scale, db_scale_t, db_amax};
+  hipError_t e = fp8l::gated_bwd_launch(
+      static_cast<const uint8_t *>(dyq), sdy, static_cast<const uint8_t *>(w2tq), sw2t,
+      static_cast<const uint16_t *>(a), static_cast<const uint16_t *>(b), M, H, D, scaling,
+      static_cast<uint16_t *>(da), static_cast<uint16_t *>(db), qa, qb, workspace,
+      static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FP8L_OK : FP8L_EHIP;
+}
+
 size_t fp8_layernorm_workspace_bytes(int64_t rows, int64_t cols, int scaling) {
   if (check_norm(rows, cols, 0, 0, 0) != FP8L_OK || bad_scaling(scaling)) return 0;
   return fp8l::norm_workspace_bytes(rows, cols, scaling);

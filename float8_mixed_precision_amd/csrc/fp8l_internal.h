@@ -244,4 +244,17 @@ hipError_t gemm_f32_launch(const uint8_t *A, const float *sa, const uint8_t *B,
                            const float *sb, int rowwise, int fmt_a, int64_t M, int64_t N,
                            int64_t K, float *C, hipStream_t stream);
 
+// Gated feed-forward (gated.h).  o NULL: h is not quantized (any M); a and b
+// both NULL: not stored.
+size_t gated_workspace_bytes(int64_t M, int64_t H, int scaling);
+hipError_t gated_fwd_launch(const uint8_t *xq, const float *sx, const uint8_t *w1q,
+                            const float *s1, const uint8_t *w3q, const float *s3, int64_t M,
+                            int64_t H, int64_t K, int scaling, uint16_t *a, uint16_t *b,
+                            uint16_t *h, const Fp8Out *o, void *workspace, hipStream_t stream);
+hipError_t gated_bwd_launch(const uint8_t *dyq, const float *sdy, const uint8_t *w2tq,
+                            const float *sw2t, const uint16_t *a, const uint16_t *b, int64_t M,
+                            int64_t H, int64_t D, int scaling, uint16_t *da, uint16_t *db,
+                            const Fp8Out &qa, const Fp8Out &qb, void *workspace,
+                            hipStream_t stream);
+
 }  // namespace fp8l

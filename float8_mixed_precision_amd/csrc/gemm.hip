@@ -116,6 +116,8 @@ constexpr uint32_t OOB_C = 0xFFFFFF00u;  // output offset that is dropped
 // that the next kernel would have to write back (measured: the GEMMs of the
 // FFN step 3% faster, the amax passes after them faster too).
 constexpr int C_STORE_AUX = 2;
+// h, da and db are read again right away, by the cast that follows.
+constexpr int GATE_STORE_AUX = 0;
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
@@ -187,6 +189,96 @@ struct GemmGroup {
 static_assert(NUM_XCD == sched::XCDS && MAX_GROUP == sched::MAX_PROBLEMS &&
               sched::MAX_WG == 32, "schedule layout");
 static_assert(sizeof(GemmGroup) <= 4096, "kernel arguments");
+
+// What the kernel does with a finished tile:
+//  EPI_NONE   the plain GEMM: C (bf16, fp32 or accumulated).
+//  EPI_GATE   both projections of a gated feed-forward and the gate:
+//             a = A B^T, b = A B2^T, h = silu(a) * b.  A tile is 256 rows x
+//             128 columns of h: its B slab holds 128 rows of B and the same
+//             128 rows of B2, dealt so that every wave's 128 slab rows are 64
+//             of each, for the same columns.  A wave's accumulators j and
+//             j + 4 are then a and b of the same elements and the gate needs
+//             no exchange.  C receives h; a and b are stored where wanted.
+//  EPI_DGATE  the gradient through the gate: with dh = A B^T (rounded to
+//             bf16, as the plain GEMM writes it) and the forward pass's a and
+//             b read where the tile is finished, C receives
+//             da = dh * b * silu'(a), C2 receives db = dh * silu(a).
+// Both forms take the amax partial maxima of what they write (of h, or of da
+// and db) where `maxima` is set: tensorwise one u32 per wave of the launch in
+// part[o], rowwise the row maxima over each wave's columns in
+// rowpart[o][slice][M] and the column maxima over its rows in
+// colpart[o][slice][N], one slice per wave column / wave row of the tiles.
+constexpr int EPI_NONE = 0, EPI_GATE = 1, EPI_DGATE = 2;
+struct GateArgs : GemmGroup {
+  const uint8_t *B2;           // EPI_GATE
+  const float *sb2;
+  uint16_t *a, *b;             // EPI_GATE: stored unless NULL; EPI_DGATE: read
+  uint16_t *C2;                // EPI_DGATE
+  int maxima;
+  uint32_t *part[2];
+  uint16_t *rowpart[2], *colpart[2];
+};
+template <int EPI>
+struct ArgsOf {
+  typedef GateArgs type;
+};
+template <>
+struct ArgsOf<EPI_NONE> {
+  typedef GemmGroup type;
+};
+
+// silu(x) = x s and silu'(x) = s + x s (1 - s), s = 1 / (1 + e^-x), in fp32
+// with the hardware exponential and reciprocal (1 ulp each).  The exponent's
+// product -x log2(e) is rounded once, which the exponential turns into a
+// relative error of |x| 2^-24: s and silu are within (|x| + 4) 2^-23 of exact,
+// relatively (below x = -87, where s leaves the normal range, silu may be
+// flushed to 0: absolute error under 2^-119).  The table of exact values that
+// the elementwise kernels use (swiglu.hip) would not fit beside the operand
+// stages in LDS; both round to the same bf16 except where the value lies that
+// close to a rounding border.
+__device__ __forceinline__ float gate_sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.44269504088896341f));
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// bf16 pairs: h = bf16(fl32(silu(a) * b))
+__device__ __forceinline__ uint32_t gate_fwd2(uint32_t a, uint32_t b) {
+  const float a0 = bf16_lo(a), a1 = bf16_hi(a);
+  return bf16x2_bits((a0 * gate_sigmoid(a0)) * bf16_lo(b), (a1 * gate_sigmoid(a1)) * bf16_hi(b));
+}
+
+// bf16 pairs: da = bf16(fl32(fl32(dh * b) * silu'(a))), db = bf16(fl32(dh * silu(a)))
+__device__ __forceinline__ void gate_bwd2(uint32_t dh, uint32_t a, uint32_t b, uint32_t &da,
+                                          uint32_t &db) {
+  const float a0 = bf16_lo(a), a1 = bf16_hi(a);
+  const float g0 = bf16_lo(dh), g1 = bf16_hi(dh);
+  const float s0 = gate_sigmoid(a0), s1 = gate_sigmoid(a1);
+  const float u0 = a0 * s0, u1 = a1 * s1;
+  da = bf16x2_bits((g0 * bf16_lo(b)) * __builtin_fmaf(u0, 1.0f - s0, s0),
+                   (g1 * bf16_hi(b)) * __builtin_fmaf(u1, 1.0f - s1, s1));
+  db = bf16x2_bits(g0 * u0, g1 * u1);
+}
+
+// per-half maxima of two u16 pairs, in one instruction
+__device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                                __builtin_bit_cast(u16x2, b)));
+}
+
+// Maximum over each 8 (LANES = 8) or 16 neighbouring lanes, in all of them
+// (DPP: quad permutations, then a mirror within 8 and within 16 lanes).
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, true));
+  if (LANES == 16)
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true));
+  return v;
+}
 
 // element i of a kernel-argument array for a wave-uniform i (selects, so the
 // array is never copied to private memory)
@@ -288,6 +380,7 @@ struct TileCoord {
   int pi, m0, n0;
   bool valid;
 };
+template <int TN = BN>
 __device__ __forceinline__ TileCoord decode_tile(const GemmGroup &g, int b, int i, int G) {
   const int x = b % NUM_XCD;
   const int l = b / NUM_XCD;
@@ -321,9 +414,36 @@ __device__ __forceinline__ TileCoord decode_tile(const GemmGroup &g, int b, int 
     const int first_m = (q / group) * GROUP_M;
     const int gm = min(tiles_m - first_m, GROUP_M);
     const int in_group = q % group;
-    return {pi, (first_m + in_group % gm) * BM, (in_group / gm) * BN, true};
+    return {pi, (first_m + in_group % gm) * BM, (in_group / gm) * TN, true};
   }
   return {0, 0, 0, false};
+}
+
+// EPI_GATE, rowwise: the 4 scales of lane l of a wave whose rows start at m
+// and whose columns start at n: lanes 0-31 the wave's 128 rows, lanes 32-47
+// its 64 columns of B, lanes 48-63 of B2.  Indices are clamped into the
+// arrays (the outputs past them are not stored).
+__device__ __forceinline__ v4f gate_scales(const GateArgs &g, int l, int m, int n) {
+  const float *p = l < 32 ? g.sa[0] : l < 48 ? g.sb[0] : g.sb2;
+  const int last = (l < 32 ? g.M[0] : g.N[0]) - 1;
+  const int i = l < 32 ? m + l * 4 : n + (l & 15) * 4;
+  return (v4f){p[min(i, last)], p[min(i + 1, last)], p[min(i + 2, last)], p[min(i + 3, last)]};
+}
+
+// Column maxima of a wave: cm holds 8 columns as u16 pairs in every lane, the
+// same columns in each group of LANES lanes; dst is the lane's first column.
+template <int LANES>
+__device__ __forceinline__ void store_colmax(const uint32_t (&cm)[4], int lane, bool col_ok,
+                                             uint16_t *dst) {
+  v4u r;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    uint32_t m = cm[d];
+#pragma unroll
+    for (int o = LANES; o < 64; o <<= 1) m = pk_max(m, (uint32_t)__shfl_xor((int)m, o));
+    r[d] = m;
+  }
+  if (lane < LANES && col_ok) *reinterpret_cast<v4u *>(dst) = r;
 }
 
 // KFULL: K % 128 == 0 (no K tail, no per-chunk K check).  RW: rowwise
@@ -334,9 +454,21 @@ __device__ __forceinline__ TileCoord decode_tile(const GemmGroup &g, int b, int 
 // B and the A fragment.  ACC (bf16 output only): C holds a bf16 matrix on
 // entry and receives bf16(fl32(C) + fl32(bf16 result)), the sum of two
 // gradient contributions as bf16 tensors add.
-template <bool KFULL, bool RW, bool F32, int FA, bool ACC>
-__global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(GemmGroup g) {
+// EPI: what becomes of a finished tile (EPI_NONE above for the plain GEMM;
+// the others write bf16 and take one problem).
+template <bool KFULL, bool RW, bool F32, int FA, bool ACC, int EPI = EPI_NONE>
+__global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>::type g) {
   static_assert(!(F32 && ACC), "accumulation is into a bf16 output");
+  static_assert(EPI == EPI_NONE || (!F32 && !ACC), "gate forms write bf16");
+  // rowwise scales two tiles ahead by DMA; EPI_GATE, whose columns come from
+  // two tensors, loads each tile's scales beside its last k-tile instead
+  constexpr bool RWT = RW && EPI != EPI_GATE;
+  // stores every lane has certainly issued after an epilogue began (EPI_GATE
+  // without a and b: h's alone), which the next tile's first wait may leave
+  // in flight; 48 of EPI_DGATE's 64 (the counter has 6 bits)
+  constexpr int IN_FLIGHT = EPI == EPI_GATE ? 16 : EPI == EPI_DGATE ? 48 : EPI_STORES;
+  // column of the matrix per tile column of the operand slab
+  constexpr int TN = EPI == EPI_GATE ? BN / 2 : BN;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[EPI_OFF + EPI_BYTES];
   const int G = gridDim.x;
   const int tid = threadIdx.x;
@@ -369,9 +501,9 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(GemmGroup g) {
   int a_pi, a_m0, a_n0, b_pi, b_m0, b_n0, c_pi, c_m0, c_n0;
   bool a_ok, b_ok, c_ok;
   {
-    const TileCoord t0 = decode_tile(g, blockIdx.x, 0, G);
-    const TileCoord t1 = decode_tile(g, blockIdx.x, 1, G);
-    const TileCoord t2 = decode_tile(g, blockIdx.x, 2, G);
+    const TileCoord t0 = decode_tile<TN>(g, blockIdx.x, 0, G);
+    const TileCoord t1 = decode_tile<TN>(g, blockIdx.x, 1, G);
+    const TileCoord t2 = decode_tile<TN>(g, blockIdx.x, 2, G);
     a_pi = t0.pi; a_m0 = t0.m0; a_n0 = t0.n0; a_ok = t0.valid;
     b_pi = t1.pi; b_m0 = t1.m0; b_n0 = t1.n0; b_ok = t1.valid;
     c_pi = t2.pi; c_m0 = t2.m0; c_n0 = t2.n0; c_ok = t2.valid;
@@ -393,7 +525,8 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(GemmGroup g) {
     const int lr_v = lane_v >> 3;                                               \
     const int ce_v = (lane_v & 7) ^ lr_v;                                       \
     _Pragma("unroll") for (int q = 0; q < 16; ++q) {                            \
-      const int row = wave * 64 + (q & 7) * 8 + lr_v;                           \
+      const int row = (EPI == EPI_GATE && q >= 8 ? wave >> 1 : wave) * 64 +     \
+                      (q & 7) * 8 + lr_v;                                       \
       voff[q] = (uint32_t)(row * d_K + ((q & 1) ? ce_v ^ 1 : ce_v) * 16);       \
     }                                                                           \
   } while (0)
@@ -415,8 +548,10 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(GemmGroup g) {
     d_rsA = __builtin_amdgcn_make_buffer_rsrc(                                  \
         (void *)(pick(g.A, pi_) + (size_t)m0_ * K_), (short)0,                  \
         d_valid ? (M_ - m0_) * K_ : 0, 0x00020000);                             \
+    const uint8_t *B_ = pick(g.B, pi_);                                         \
+    if constexpr (EPI == EPI_GATE) B_ = (wave & 1) ? g.B2 : B_;                 \
     d_rsB = __builtin_amdgcn_make_buffer_rsrc(                                  \
-        (void *)(pick(g.B, pi_) + (size_t)n0_ * K_), (short)0,                  \
+        (void *)(B_ + (size_t)n0_ * K_), (short)0,                              \
         d_valid ? (N_ - n0_) * K_ : 0, 0x00020000);                             \
     if (K_ != d_K) {                                                            \
       d_K = K_;                                                                 \
@@ -576,7 +711,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(GemmGroup g) {
     FP8P_DADV();
   }
   // rowwise: the first two tiles' scales
-  if (RW) {
+  if (RWT) {
     FP8P_SCALES(a_ok, a_pi, a_m0, a_n0, 0);
     FP8P_SCALES(b_ok, b_pi, b_m0, b_n0, 1);
   }
@@ -592,10 +727,12 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(GemmGroup g) {
   // what it wrote.
 #define FP8P_RCP_AT(BUF)                                                          \
   (reinterpret_cast<v4f *>(epi + (BUF) * SCALE_BYTES) + rcp_slot(hw_lane(), wm, wn))
-  if (RW) {                                       // tile 0's scales
+  if (RWT) {                                      // tile 0's scales
     v4f *r_ = FP8P_RCP_AT(0);
     *r_ = recip4(*r_);
   }
+  // EPI_GATE, EPI_DGATE: tensorwise maxima of this wave's outputs so far (u16 pairs)
+  uint32_t tmax0 = 0, tmax1 = 0;
   int st = 0;          // stage of the current unit
   for (int tile = 0;; ++tile) {
     const TileCoord tc = {a_pi, a_m0, a_n0, a_ok};
@@ -607,7 +744,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(GemmGroup g) {
     a_pi = b_pi; a_m0 = b_m0; a_n0 = b_n0; a_ok = b_ok;
     b_pi = c_pi; b_m0 = c_m0; b_n0 = c_n0; b_ok = c_ok;
     {
-      const TileCoord t3 = decode_tile(g, blockIdx.x, tile + 3, G);
+      const TileCoord t3 = decode_tile<TN>(g, blockIdx.x, tile + 3, G);
       c_pi = t3.pi; c_m0 = t3.m0; c_n0 = t3.n0; c_ok = t3.valid;
     }
     ++cur;
@@ -651,16 +788,20 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(GemmGroup g) {
     // instructions.
 #define FP8P_LAST(MF)                                                             \
   do {                                                                            \
+    v4f *rn_ = nullptr;                                                           \
+    v4f sn_ = {};                                                                 \
+    if constexpr (EPI == EPI_GATE && RW) {                                        \
+      sn_ = gate_scales(g, hw_lane(), m0 + wm * WM, n0 + wn * (WN / 2));          \
+      rn_ = reinterpret_cast<v4f *>(epi) + hw_lane();                             \
+    }                                                                             \
     FP8P_H1(st, MF)                                                               \
     if (nk == 1 && !F32 && !RW)                                                   \
-      wait_vmcnt<EPI_STORES>();                                                   \
+      wait_vmcnt<IN_FLIGHT>();                                                    \
     else                                                                          \
       wait_vmcnt0();                                                              \
     wait_lgkm0();                                                                 \
     barrier_lds();                                                                \
-    v4f *rn_ = nullptr;                                                           \
-    v4f sn_ = {};                                                                 \
-    if (RW) {                                                                     \
+    if (RWT) {                                                                    \
       rn_ = FP8P_RCP_AT((tile + 1) & 1);                                          \
       sn_ = *rn_;                                                                 \
     }                                                                             \
@@ -677,7 +818,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(GemmGroup g) {
       // (vmcnt counts in issue order): all but those.
       FP8P_H1(st, FP8P_MFZ)
       if (!F32)
-        wait_vmcnt<EPI_STORES + (RW ? SCALE_DMAS : 0)>();
+        wait_vmcnt<IN_FLIGHT + (RWT ? SCALE_DMAS : 0)>();
       else
         wait_vmcnt0();
       wait_lgkm0();
@@ -731,7 +872,113 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(GemmGroup g) {
     // rowwise: the tile's reciprocal scales
     const float *tab = reinterpret_cast<const float *>(epi + (tile & 1) * SCALE_BYTES);
     uint8_t *stg = epi + RW_STAGE_OFF;            // rowwise staging
-    if (RW && F32) {
+    // EPI_DGATE: a and b read, db written at the offsets of da in C
+    __amdgpu_buffer_rsrc_t rsGA = rsC, rsGB = rsC, rsC2 = rsC;
+    if constexpr (EPI == EPI_DGATE) {
+      rsGA = __builtin_amdgcn_make_buffer_rsrc(g.a, (short)0, M * N * 2, 0x00020000);
+      rsGB = __builtin_amdgcn_make_buffer_rsrc(g.b, (short)0, M * N * 2, 0x00020000);
+      rsC2 = __builtin_amdgcn_make_buffer_rsrc(g.C2, (short)0, M * N * 2, 0x00020000);
+    }
+    if constexpr (EPI == EPI_GATE) {
+      // 32 rows x 64 columns (128 B) of a, b and h per pass, staged one after
+      // the other (row r's 16-byte chunk c at c ^ (r % 8), its 8-byte halves
+      // swapped where r % 16 >= 8); rowwise reciprocals come from the table
+      // that the last k-tile left: 128 rows, 64 columns of B, 64 of B2
+      const float inv_b20 = RW ? 0.f : 1.0f / scalar_load(g.sb2);
+      const float *rtab = reinterpret_cast<const float *>(epi);
+      const int scol = n0 + wn * (WN / 2) + (lane_e & 7) * 8;
+      const bool col_ok = scol < N;
+      rsGA = __builtin_amdgcn_make_buffer_rsrc(g.a, (short)0, g.a ? M * N * 2 : 0, 0x00020000);
+      rsGB = __builtin_amdgcn_make_buffer_rsrc(g.b, (short)0, g.a ? M * N * 2 : 0, 0x00020000);
+      const int slice_r = (n0 / TN) * 2 + wn;     // this wave's partial maxima
+      uint32_t cm[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        uint2 pa[2][4], pb[2][4];
+#pragma unroll
+        for (int ii = 0; ii < 2; ++ii) {
+          const int i = 2 * p + ii;
+          const float ia = RW ? rtab[i * FR + ml16] : inv_a0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const v4f ib = RW ? *reinterpret_cast<const v4f *>(rtab + WM + j * FR + nq) : inv_br[0];
+            const v4f ib2 = RW ? *reinterpret_cast<const v4f *>(rtab + WM + 64 + j * FR + nq)
+                               : (v4f){inv_b20, inv_b20, inv_b20, inv_b20};
+            const v4f x = acc[j][i], y = acc[j + 4][i];
+            pa[ii][j] = make_uint2(bf16x2_bits((x[0] * ia) * ib[0], (x[1] * ia) * ib[1]),
+                                   bf16x2_bits((x[2] * ia) * ib[2], (x[3] * ia) * ib[3]));
+            pb[ii][j] = make_uint2(bf16x2_bits((y[0] * ia) * ib2[0], (y[1] * ia) * ib2[1]),
+                                   bf16x2_bits((y[2] * ia) * ib2[2], (y[3] * ia) * ib2[3]));
+          }
+        }
+        const int srow = m0 + wm * WM + p * 32 + (lane_e >> 3);
+        uint32_t off[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          off[u] = col_ok && srow + u * 8 < M ? (uint32_t)(((srow + u * 8) * N + scol) * 2) : OOB_C;
+        // one staged matrix: 8 writes, then 4 whole 16-byte chunks per lane
+        auto staged = [&](const uint2 (&w)[2][4], v4u (&v)[4]) {
+#pragma unroll
+          for (int ii = 0; ii < 2; ++ii)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int ch = (2 * j + (nq >> 3)) ^ (ml16 & 7);
+              *reinterpret_cast<uint2 *>(stg + (ii * FR + ml16) * 128 + ch * 16 +
+                                         (((nq & 7) * 2) ^ ((ml16 >> 3) << 3))) = w[ii][j];
+            }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int r = u * 8 + (lane_e >> 3);
+            v[u] = *reinterpret_cast<const v4u *>(stg + r * 128 + (((lane_e & 7) ^ (r & 7)) * 16));
+            if (u & 1) v[u] = (v4u){v[u].z, v[u].w, v[u].x, v[u].y};
+          }
+        };
+        v4u v[4];
+        if (g.a) {
+          staged(pa, v);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            __builtin_amdgcn_raw_buffer_store_b128(v[u], rsGA, off[u], 0, C_STORE_AUX);
+          staged(pb, v);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            __builtin_amdgcn_raw_buffer_store_b128(v[u], rsGB, off[u], 0, C_STORE_AUX);
+        }
+#pragma unroll
+        for (int ii = 0; ii < 2; ++ii)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            pa[ii][j] = make_uint2(gate_fwd2(pa[ii][j].x, pb[ii][j].x),
+                                   gate_fwd2(pa[ii][j].y, pb[ii][j].y));
+        staged(pa, v);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          __builtin_amdgcn_raw_buffer_store_b128(v[u], rsC, off[u], 0, GATE_STORE_AUX);
+        if (g.maxima) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint32_t keep = off[u] != OOB_C ? 0x7FFF7FFFu : 0u;
+            uint32_t rm = 0;
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+              const uint32_t x = v[u][d] & keep;
+              rm = pk_max(rm, x);
+              if (RW) cm[d] = pk_max(cm[d], x);
+            }
+            if (RW) {
+              rm = lanes_max<8>(hmax16(rm));
+              if ((lane_e & 7) == 0 && srow + u * 8 < M)
+                g.rowpart[0][(size_t)slice_r * M + srow + u * 8] = (uint16_t)rm;
+            } else {
+              tmax0 = pk_max(tmax0, rm);
+            }
+          }
+        }
+      }
+      if (RW && g.maxima)
+        store_colmax<8>(cm, lane_e, col_ok,
+                        g.colpart[0] + (size_t)((m0 / BM) * 2 + wm) * N + scol);
+    } else if (RW && F32) {
       // rowwise fp32: the tile's columns in two halves of 64, one 16-row
       // block per pass: 16 rows x 256 B (row r's 16-byte chunk c at
       // c ^ (r % 16)); the reciprocals are read from the table where they
@@ -799,6 +1046,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(GemmGroup g) {
       for (int jh = 0; jh < 2; ++jh) {
         const int scol = n0 + wn * WN + jh * 64 + (lane_e & 7) * 8;
         const bool col_ok = scol < N;
+        uint32_t cm[2][4] = {};                   // EPI_DGATE: column maxima of da, db
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           const float ia0 = tab[wm * WM + 2 * p * FR + ml16];
@@ -836,6 +1084,40 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(GemmGroup g) {
             const bool ok = col_ok && srow + u * 8 < M;
             off[u] = ok ? (uint32_t)(((srow + u * 8) * N + scol) * 2) : OOB_C;
           }
+          if constexpr (EPI == EPI_DGATE) {
+            v4u ga[4], gb[4], w[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              ga[u] = __builtin_amdgcn_raw_buffer_load_b128(rsGA, off[u], 0, 0);
+              gb[u] = __builtin_amdgcn_raw_buffer_load_b128(rsGB, off[u], 0, 0);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              uint32_t rm0 = 0, rm1 = 0;
+              const uint32_t keep = off[u] != OOB_C ? 0x7FFF7FFFu : 0u;
+#pragma unroll
+              for (int d = 0; d < 4; ++d) {
+                uint32_t da, db;
+                gate_bwd2(v[u][d], ga[u][d], gb[u][d], da, db);
+                v[u][d] = da;
+                w[u][d] = db;
+                rm0 = pk_max(rm0, da & keep);
+                rm1 = pk_max(rm1, db & keep);
+                cm[0][d] = pk_max(cm[0][d], da & keep);
+                cm[1][d] = pk_max(cm[1][d], db & keep);
+              }
+              __builtin_amdgcn_raw_buffer_store_b128(w[u], rsC2, off[u], 0, GATE_STORE_AUX);
+              if (g.maxima) {
+                rm0 = lanes_max<8>(hmax16(rm0));
+                rm1 = lanes_max<8>(hmax16(rm1));
+                const size_t at = (size_t)((n0 / BN) * 4 + wn * 2 + jh) * M + srow + u * 8;
+                if ((lane_e & 7) == 0 && srow + u * 8 < M) {
+                  g.rowpart[0][at] = (uint16_t)rm0;
+                  g.rowpart[1][at] = (uint16_t)rm1;
+                }
+              }
+            }
+          }
           if (ACC) {
             v4u cin[4];
 #pragma unroll
@@ -853,7 +1135,15 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(GemmGroup g) {
           }
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            __builtin_amdgcn_raw_buffer_store_b128(v[u], rsC, off[u], 0, C_STORE_AUX);
+            __builtin_amdgcn_raw_buffer_store_b128(v[u], rsC, off[u], 0,
+                                                   EPI == EPI_NONE ? C_STORE_AUX : GATE_STORE_AUX);
+        }
+        if constexpr (EPI == EPI_DGATE) {
+          if (g.maxima) {
+            const size_t at = (size_t)((m0 / BM) * 2 + wm) * N + scol;
+            store_colmax<8>(cm[0], lane_e, col_ok, g.colpart[0] + at);
+            store_colmax<8>(cm[1], lane_e, col_ok, g.colpart[1] + at);
+          }
         }
       }
     } else {
@@ -861,6 +1151,17 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(GemmGroup g) {
       const bool col_ok = scol < N;
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
+        // EPI_DGATE: a and b of the pass, on their way while dh is staged
+        v4u ga[8], gb[8];
+        if constexpr (EPI == EPI_DGATE) {
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int row = m0 + wm * WM + p * 32 + u * 4 + (lane_e >> 4);
+            const uint32_t o = col_ok && row < M ? (uint32_t)((row * N + scol) * 2) : OOB_C;
+            ga[u] = __builtin_amdgcn_raw_buffer_load_b128(rsGA, o, 0, 0);
+            gb[u] = __builtin_amdgcn_raw_buffer_load_b128(rsGB, o, 0, 0);
+          }
+        }
 #pragma unroll
         for (int ii = 0; ii < 2; ++ii) {
           const int i = 2 * p + ii;
@@ -895,6 +1196,23 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(GemmGroup g) {
           const bool ok = col_ok && srow + u * 4 < M;
           off[u] = ok ? (uint32_t)(((srow + u * 4) * N + scol) * 2) : OOB_C;
         }
+        if constexpr (EPI == EPI_DGATE) {
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            v4u w;
+            const uint32_t keep = off[u] != OOB_C ? 0x7FFF7FFFu : 0u;
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+              uint32_t da, db;
+              gate_bwd2(v[u][d], ga[u][d], gb[u][d], da, db);
+              v[u][d] = da;
+              w[d] = db;
+              tmax0 = pk_max(tmax0, da & keep);
+              tmax1 = pk_max(tmax1, db & keep);
+            }
+            __builtin_amdgcn_raw_buffer_store_b128(w, rsC2, off[u], 0, GATE_STORE_AUX);
+          }
+        }
         if (ACC) {
           v4u cin[8];
 #pragma unroll
@@ -911,7 +1229,9 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(GemmGroup g) {
           }
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) __builtin_amdgcn_raw_buffer_store_b128(v[u], rsC, off[u], 0, C_STORE_AUX);
+        for (int u = 0; u < 8; ++u)
+          __builtin_amdgcn_raw_buffer_store_b128(v[u], rsC, off[u], 0,
+                                                 EPI == EPI_NONE ? C_STORE_AUX : GATE_STORE_AUX);
       }
     }
 #ifdef FP8L_PHASE_TIMING
@@ -929,7 +1249,16 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(GemmGroup g) {
     // both run on).  A wave stages and keeps its scales only in its own part
     // of the epilogue region, and the next tile's operands were made visible
     // by the barrier of this tile's last k-tile: no barrier here.
-    if (RW) FP8P_SCALES(b_ok, b_pi, b_m0, b_n0, tile & 1);
+    if (RWT) FP8P_SCALES(b_ok, b_pi, b_m0, b_n0, tile & 1);
+  }
+  if constexpr (EPI != EPI_NONE && !RW) {
+    if (g.maxima) {
+      const uint32_t m0_ = wave_max(hmax16(tmax0)), m1_ = wave_max(hmax16(tmax1));
+      if (hw_lane() == 0) {
+        g.part[0][blockIdx.x * 4 + wave] = m0_;
+        if (EPI == EPI_DGATE) g.part[1][blockIdx.x * 4 + wave] = m1_;
+      }
+    }
   }
 #undef FP8P_H2D
 #undef FP8P_H2
@@ -1094,6 +1423,8 @@ hipError_t gemm_f32_launch(const uint8_t *A, const float *sa, const uint8_t *B,
 }
 
 }  // namespace fp8l
+
+#include "gated.h"
 
 #ifdef FP8L_PHASE_TIMING
 // Copies the first `bytes` of the timestamp array (8 u64 per workgroup:

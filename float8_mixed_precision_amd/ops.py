@@ -26,6 +26,7 @@ EXPORTS = ("fp8_linear_workspace_bytes", "fp8_linear_quantize",
            "fp8_linear_quantize_noalloc", "fp8_linear_amax",
            "fp8_linear_quantize_scaled", "fp8_linear_fwd", "fp8_linear_bwd",
            "fp8_linear_bwd_w_f32", "fp8_linear_bwd_x_acc", "fp8_linear_gemm_grouped",
+           "fp8_gated_workspace_bytes", "fp8_gated_fwd", "fp8_gated_bwd",
            "fp8_layernorm_workspace_bytes", "fp8_layernorm_fwd", "fp8_layernorm_quantize",
            "fp8_layernorm_bwd", "fp8_linear_encode_e4m3",
            "fp8_linear_encode_e5m2", "fp8_swiglu_workspace_bytes", "fp8_swiglu_fwd",
@@ -91,6 +92,14 @@ def lib() -> ctypes.CDLL:
     L.fp8_swiglu_bwd.restype = I
     L.fp8_swiglu_bwd.argtypes = ([P, P, P, i64, i64, I, P, P] + [P] * 10
                                  + [P, ctypes.c_size_t, P])
+    L.fp8_gated_workspace_bytes.restype = ctypes.c_size_t
+    L.fp8_gated_workspace_bytes.argtypes = [i64, i64, I]
+    L.fp8_gated_fwd.restype = I
+    L.fp8_gated_fwd.argtypes = ([P] * 6 + [i64, i64, i64, I] + [P] * 8
+                                + [P, ctypes.c_size_t, P])
+    L.fp8_gated_bwd.restype = I
+    L.fp8_gated_bwd.argtypes = ([P] * 6 + [i64, i64, i64, I] + [P] * 12
+                                + [P, ctypes.c_size_t, P])
     F = ctypes.c_float
     L.fp8_layernorm_workspace_bytes.restype = ctypes.c_size_t
     L.fp8_layernorm_workspace_bytes.argtypes = [i64, i64, I]
@@ -522,6 +531,100 @@ def fp8_layernorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.
             workspace.numel() if workspace is not None else 0, _stream(stream)),
             "fp8_layernorm_bwd")
     return dx, dweight, dbias
+
+
+# ---------------------------------------------------- gated feed-forward --
+
+def fp8_gated_workspace_bytes(M: int, H: int, rowwise: bool = False) -> int:
+    return int(lib().fp8_gated_workspace_bytes(M, H, _scaling(rowwise)))
+
+
+def alloc_gated_workspace(M: int, H: int, rowwise: bool, device) -> torch.Tensor:
+    """Workspace of fp8_gated_fwd (with a quantized h) and fp8_gated_bwd for
+    [M, H] outputs; needs no clearing."""
+    return torch.empty(max(fp8_gated_workspace_bytes(M, H, rowwise), 256), dtype=torch.uint8,
+                       device=device)
+
+
+def _operands(prefix, q, s, rows, k, rowwise):
+    """_on_device's checks of an fp8 operand: codes [rows, k] and scales."""
+    return {prefix + "q": (q, torch.uint8, (rows, k)),
+            prefix + " scale": (s, torch.float32, (rows if rowwise else 1,))}
+
+
+def _quantized(prefix, z, M, H, rowwise):
+    """_on_device's checks of the quantize outputs of an [M, H] matrix."""
+    u8, f32 = torch.uint8, torch.float32
+    ns, nst, na = (M, H, M + H) if rowwise else (1, 1, 1)
+    return {prefix + "q": (z.q, u8, (M, H)), prefix + "qt": (z.qt, u8, (H, M)),
+            prefix + "scale": (z.scale, f32, (ns,)), prefix + "scale_t": (z.scale_t, f32, (nst,)),
+            prefix + "amax": (z.amax, f32, (na,))}
+
+
+def fp8_gated_fwd(xq: torch.Tensor, sx: torch.Tensor, w1q: torch.Tensor, sw1: torch.Tensor,
+                  w3q: torch.Tensor, sw3: torch.Tensor, rowwise: bool = False,
+                  h: Optional[torch.Tensor] = None, a: Optional[torch.Tensor] = None,
+                  b: Optional[torch.Tensor] = None, out: Optional[Quantized] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """h [M, H] bf16 = silu(x W1^T) * (x W3^T) in one kernel, from the fp8
+    copies of x [M, K] (any M) and of W1, W3 [H, K].  With tensors a and b
+    given, the two projections are stored there for fp8_gated_bwd; with
+    ``out`` given (M a multiple of 16), h is quantized into it."""
+    (M, K), H = xq.shape, w1q.shape[0]
+    bf = torch.bfloat16
+    checks = {}
+    checks.update(_operands("x", xq, sx, M, K, rowwise))
+    checks.update(_operands("w1", w1q, sw1, H, K, rowwise))
+    checks.update(_operands("w3", w3q, sw3, H, K, rowwise))
+    if out is not None:
+        checks.update(_quantized("h", out, M, H, rowwise))
+    with _on_device(xq, a=(a, bf, (M, H)), b=(b, bf, (M, H)), h=(h, bf, (M, H)), **checks):
+        if h is None:
+            h = torch.empty((M, H), dtype=bf, device=xq.device)
+        if out is not None and workspace is None:
+            workspace = alloc_gated_workspace(M, H, rowwise, xq.device)
+        z = out if out is not None else _NO_CODES
+        _check(lib().fp8_gated_fwd(
+            _p(xq), _p(sx), _p(w1q), _p(sw1), _p(w3q), _p(sw3), M, H, K, _scaling(rowwise),
+            _p(a), _p(b), _p(h), _p(z.q), _p(z.qt), _p(z.scale), _p(z.scale_t), _p(z.amax),
+            _p(workspace), workspace.numel() if workspace is not None else 0, _stream(stream)),
+            "fp8_gated_fwd")
+    return h
+
+
+_NO_CODES = Quantized(None, None, None, None, None)
+
+
+def fp8_gated_bwd(dyq: torch.Tensor, sdy: torch.Tensor, w2tq: torch.Tensor, sw2t: torch.Tensor,
+                  a: torch.Tensor, b: torch.Tensor, rowwise: bool = False, e5m2: bool = False,
+                  da: Optional[torch.Tensor] = None, db: Optional[torch.Tensor] = None,
+                  qa: Optional[Quantized] = None, qb: Optional[Quantized] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None):
+    """(da, db, quantize of da, quantize of db) of the gate h = silu(a) * b for
+    dh = dY . W2, from the fp8 copies of dY [M, D] and of W2^T [H, D], in one
+    kernel and the two casts; dY's and the outputs' codes E5M2 when e5m2."""
+    (M, D), H = dyq.shape, w2tq.shape[0]
+    bf, dev = torch.bfloat16, dyq.device
+    checks = {}
+    checks.update(_operands("dy", dyq, sdy, M, D, rowwise))
+    checks.update(_operands("w2t", w2tq, sw2t, H, D, rowwise))
+    for name, z in (("da ", qa), ("db ", qb)):
+        if z is not None:
+            checks.update(_quantized(name, z, M, H, rowwise))
+    with _on_device(dyq, a=(a, bf, (M, H)), b=(b, bf, (M, H)), da=(da, bf, (M, H)),
+                    db=(db, bf, (M, H)), **checks):
+        da = torch.empty((M, H), dtype=bf, device=dev) if da is None else da
+        db = torch.empty((M, H), dtype=bf, device=dev) if db is None else db
+        qa = alloc_quantized(M, H, rowwise, dev) if qa is None else qa
+        qb = alloc_quantized(M, H, rowwise, dev) if qb is None else qb
+        if workspace is None:
+            workspace = alloc_gated_workspace(M, H, rowwise, dev)
+        _check(lib().fp8_gated_bwd(
+            _p(dyq), _p(sdy), _p(w2tq), _p(sw2t), _p(a), _p(b), M, H, D, _scaling(rowwise, e5m2),
+            _p(da), _p(db), _p(qa.q), _p(qa.qt), _p(qa.scale), _p(qa.scale_t), _p(qa.amax),
+            _p(qb.q), _p(qb.qt), _p(qb.scale), _p(qb.scale_t), _p(qb.amax), _p(workspace),
+            workspace.numel(), _stream(stream)), "fp8_gated_bwd")
+    return da, db, qa, qb
 
 
 def fp8_linear_encode_e4m3(x: torch.Tensor, out: Optional[torch.Tensor] = None,

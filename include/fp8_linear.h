@@ -354,6 +354,63 @@ FP8L_API int fp8_swiglu_bwd(const void *dh, const void *a, const void *b, int64_
                             void *stream);
 
 /*
+ * Gated feed-forward: the two projections and the gate in one kernel, and the
+ * gradient through the gate in one kernel (the block's launches above with
+ * fewer passes over its [M, H] tensors).
+ *
+ *   a[m][j] = fp8_linear_fwd's out for (xq, w1q),  b[m][j] for (xq, w3q)
+ *   h       = bf16( fl32( silu(a) * b ) )
+ *
+ * from the bf16 a and b.  silu and silu' are computed in fp32 here (relative
+ * error at most (|a| + 4) 2^-23; where the exact silu is below 2^-119 it may
+ * be 0), so that h, da and db can differ from fp8_swiglu_fwd / _bwd's by one
+ * bf16 step where the value lies next to a rounding border.
+ *
+ *   xq [M, K], sx;  w1q, w3q [H, K], sw1, sw3   as fp8_linear_fwd's operands
+ *   a, b    [M, H] bf16 (written), both or neither NULL: what fp8_gated_bwd
+ *           needs
+ *   h       [M, H] bf16 (written)
+ *   hq, hqt, scale, scale_t, amax_out  the E4M3 quantize of h, as
+ *           fp8_linear_quantize's outputs for x = h; all NULL: h is not
+ *           quantized, the workspace is not used (it may be NULL) and M is
+ *           any number of tokens >= 0
+ *   scaling FP8L_TENSORWISE or FP8L_ROWWISE, of the operands and of hq
+ *   workspace / workspace_bytes: >= fp8_gated_workspace_bytes(M, H, scaling)
+ * H and K are multiples of 16, and M where h is quantized; sizes as for
+ * fp8_linear_fwd.  The order of the fp32 additions depends on M (up to 64
+ * tokens split the contraction over the waves of a workgroup); equal calls
+ * give equal bits.  The workspace's contents are undefined on entry and exit,
+ * not shared by calls in flight together.
+ */
+FP8L_API size_t fp8_gated_workspace_bytes(int64_t M, int64_t H, int scaling);
+FP8L_API int fp8_gated_fwd(const void *xq, const float *sx, const void *w1q, const float *sw1,
+                           const void *w3q, const float *sw3, int64_t M, int64_t H, int64_t K,
+                           int scaling, void *a, void *b, void *h, void *hq, void *hqt,
+                           float *scale, float *scale_t, float *amax_out, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/*
+ * With dh[m][j] = fp8_linear_bwd's grad_x for (dyq, w2tq) (bf16; not stored):
+ *
+ *   da = bf16( fl32( fl32(dh * b) * silu'(a) ) ),  db = bf16( fl32(dh * silu(a)) )
+ *
+ *   dyq  [M, D] (q of the block's output gradient), sdy
+ *   w2tq [H, D] (qt of W2 [D, H]), sw2t
+ *   a, b [M, H] bf16 (read): fp8_gated_fwd's
+ *   da, db [M, H] bf16 (written); daq ... db_amax their quantizes, as for
+ *           fp8_swiglu_bwd
+ *   scaling FP8L_TENSORWISE or FP8L_ROWWISE, optionally | FP8L_E5M2 (dyq and
+ *           the codes of da and db)
+ * M, H and D are multiples of 16.
+ */
+FP8L_API int fp8_gated_bwd(const void *dyq, const float *sdy, const void *w2tq,
+                           const float *sw2t, const void *a, const void *b, int64_t M, int64_t H,
+                           int64_t D, int scaling, void *da, void *db, void *daq, void *daqt,
+                           float *da_scale, float *da_scale_t, float *da_amax, void *dbq,
+                           void *dbqt, float *db_scale, float *db_scale_t, float *db_amax,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Layer norm, and its RMS form: the norm in front of the feed-forward block,
  * as the producer of the fp8 operand that the block's first linears read.
  *
