@@ -887,10 +887,29 @@ class SwiGLUFFNStep:
       grad_x += db.w3                              (fp8_linear_bwd_x_acc)
 
     With ``e5m2_grad`` the gradient operands (d_out, da, db) are E5M2.
+
+    With ``fused`` the gate runs in the GEMMs' own kernels, in place of the
+    launches of the same effect above (dh is then not stored, and grad_w2 joins
+    the last grouped launch):
+
+      a, b, h and the quantize of h                (fp8_gated_fwd)
+      da, db and their quantizes                   (fp8_gated_bwd)
+
+    With ``norm`` = (weight, bias) (each a tensor or None) x is normalized
+    first (the layer norm with ``eps``, its RMS form with ``rms``); the block
+    then starts and ends with
+
+      normalize x and quantize the result          (fp8_layernorm_quantize)
+      grad_x -> grad_in, grad_norm_w, grad_norm_b  (fp8_layernorm_bwd)
+
+    grad_x being the gradient of the normalized x, grad_in that of x (the
+    norm's branch alone, without the residual's).
     """
 
-    def __init__(self, x, w1, w3, w2, d_out, rowwise: bool = False, e5m2_grad: bool = False):
+    def __init__(self, x, w1, w3, w2, d_out, rowwise: bool = False, e5m2_grad: bool = False,
+                 fused: bool = False, norm=None, eps: float = 1e-5, rms: bool = False):
         self.x, self.w1, self.w3, self.w2, self.d_out = x, w1, w3, w2, d_out
+        self.fused, self.norm, self.eps, self.rms = fused, norm, eps, rms
         self.rowwise, self.e5m2_grad = rowwise, e5m2_grad
         self.M, self.D = x.shape
         self.H = w1.shape[0]
@@ -910,17 +929,26 @@ class SwiGLUFFNStep:
                  ((M, D), (H, D), (D, H)))
         self.ws = torch.zeros(max(ws, 256), dtype=torch.uint8, device=dev)
         self.ws_side = torch.zeros_like(self.ws)     # quantizes on a second stream
-        self.ws_sw = alloc_swiglu_workspace(M, H, rowwise, dev)
+        self.ws_sw = (alloc_gated_workspace if fused else alloc_swiglu_workspace)(M, H, rowwise,
+                                                                                  dev)
         self._start = torch.cuda.Event()
         self._side_events = {n: torch.cuda.Event() for n in ("qw1", "qw3", "qw2", "qdy")}
         self.a = torch.empty((M, H), **bf)
         self.b = torch.empty((M, H), **bf)
         self.h = torch.empty((M, H), **bf)
         self.out = torch.empty((M, D), **bf)
-        self.dh = torch.empty((M, H), **bf)
+        self.dh = None if fused else torch.empty((M, H), **bf)
         self.da = torch.empty((M, H), **bf)
         self.db = torch.empty((M, H), **bf)
         self.grad_x = torch.empty((M, D), **bf)
+        if norm is not None:
+            f32 = dict(dtype=torch.float32, device=dev)
+            self.mean = None if rms else torch.empty(M, **f32)
+            self.rstd = torch.empty(M, **f32)
+            self.ws_norm = alloc_layernorm_workspace(M, D, dev, rowwise)
+            self.grad_in = torch.empty((M, D), **bf)
+            self.grad_norm_w = torch.empty(D, **f32) if norm[0] is not None else None
+            self.grad_norm_b = torch.empty(D, **f32) if norm[1] is not None else None
         self.grad_w1 = torch.empty((H, D), **bf)
         self.grad_w3 = torch.empty((H, D), **bf)
         self.grad_w2 = torch.empty((D, H), **bf)
@@ -932,14 +960,15 @@ class SwiGLUFFNStep:
 
     def ops(self):
         """The launches of one step, in order: (name, kind, work, side,
-        needs, fn) with kind one of "quantize", "swiglu", "gemm"; work the
-        algorithmic bytes (quantize / swiglu) or flops (gemm) of the launch;
+        needs, fn) with kind one of "quantize", "swiglu", "gemm", "norm"; work
+        the algorithmic bytes (quantize, swiglu, norm) or the GEMMs' flops
+        (gemm) of the launch;
         side True for the launches that depend on no other launch of the
         step (the quantizes of the weights and of d_out); needs the names
         of the side launches this one reads; fn(stream) the call."""
         M, D, H, rw, e5 = self.M, self.D, self.H, self.rowwise, self.e5m2_grad
         g = 2 * M * D * H
-        return (
+        head = (
             ("qw1", "quantize", 6 * H * D, True, (),
              lambda st: fp8_linear_quantize(self.w1, rw, self.qw1, self.ws_side, st)),
             ("qw3", "quantize", 6 * H * D, True, (),
@@ -949,8 +978,49 @@ class SwiGLUFFNStep:
             ("qdy", "quantize", 6 * M * D, True, (),
              lambda st: fp8_linear_quantize(self.d_out, rw, self.qdy, self.ws_side, st,
                                             e5m2=e5)),
-            ("qx", "quantize", 6 * M * D, False, (),
-             lambda st: fp8_linear_quantize(self.x, rw, self.qx, self.ws, st)),
+        )
+        qx = ("qx", "quantize", 6 * M * D, False, (),
+              lambda st: fp8_linear_quantize(self.x, rw, self.qx, self.ws, st))
+        tail = ()
+        if self.norm is not None:
+            w, b = self.norm
+            # x read twice (statistics, then the cast), q and qt written
+            qx = ("norm_qx", "norm", 6 * M * D, False, (), lambda st: fp8_layernorm_quantize(
+                self.x, w, b, self.eps, self.rms, rw, mean=self.mean, rstd=self.rstd,
+                out=self.qx, workspace=self.ws_norm, stream=st))
+            tail = (("norm_bwd", "norm", 6 * M * D, False, (), lambda st: fp8_layernorm_bwd(
+                self.grad_x, self.x, w, self.mean, self.rstd, self.rms, self.grad_in,
+                self.grad_norm_w, self.grad_norm_b, want_w=w is not None, want_b=b is not None,
+                workspace=self.ws_norm, stream=st)),)
+        out = ("out", "gemm", g, False, ("qw2",),
+               lambda st: fp8_linear_fwd(self.qh.q, self.qh.scale, self.qw2.q, self.qw2.scale, rw,
+                                         self.out, st))
+        grad_w2 = (self.qdy.qt, self.qdy.scale_t, self.qh.qt, self.qh.scale_t, self.grad_w2)
+        grad_x_w13 = [
+            (self.qda.q, self.qda.scale, self.qw1.qt, self.qw1.scale_t, self.grad_x),
+            (self.qda.qt, self.qda.scale_t, self.qx.qt, self.qx.scale_t, self.grad_w1),
+            (self.qdb.qt, self.qdb.scale_t, self.qx.qt, self.qx.scale_t, self.grad_w3)]
+        grad_x_acc = ("grad_x_acc", "gemm", g, False, ("qw3",), lambda st: fp8_linear_bwd_x_acc(
+            self.qdb.q, self.qdb.scale, self.qw3.qt, self.qw3.scale_t, M, H, D, self.grad_x, rw,
+            st, e5m2=e5))
+        if self.fused:
+            return head + (
+                qx,
+                # both projections and the gate; the cast of h follows
+                ("gated_fwd", "gemm", 2 * g, False, ("qw1", "qw3"), lambda st: fp8_gated_fwd(
+                    self.qx.q, self.qx.scale, self.qw1.q, self.qw1.scale, self.qw3.q,
+                    self.qw3.scale, rw, self.h, self.a, self.b, self.qh, self.ws_sw, st)),
+                out,
+                # dh and the gate's backward; the casts of da and db follow
+                ("gated_bwd", "gemm", g, False, ("qw2", "qdy"), lambda st: fp8_gated_bwd(
+                    self.qdy.q, self.qdy.scale, self.qw2.qt, self.qw2.scale_t, self.a, self.b,
+                    rw, e5, self.da, self.db, self.qda, self.qdb, self.ws_sw, st)),
+                # grad_x (contraction H) and the three grad_W (contraction M)
+                ("grad_x_w123", "gemm", 4 * g, False, (),
+                 lambda st: fp8_linear_gemm_grouped(grad_x_w13 + [grad_w2], rw, st, e5m2=e5)),
+                grad_x_acc) + tail
+        return head + (
+            qx,
             # a and b in one launch
             ("ab", "gemm", 2 * g, False, ("qw1", "qw3"), lambda st: fp8_linear_gemm_grouped(
                 [(self.qx.q, self.qx.scale, self.qw1.q, self.qw1.scale, self.a),
@@ -959,14 +1029,12 @@ class SwiGLUFFNStep:
             # h written once; q and qt written
             ("swiglu_fwd", "swiglu", 10 * M * H, False, (),
              lambda st: fp8_swiglu_fwd(self.a, self.b, rw, self.h, self.qh, self.ws_sw, st)),
-            ("out", "gemm", g, False, ("qw2",),
-             lambda st: fp8_linear_fwd(self.qh.q, self.qh.scale, self.qw2.q, self.qw2.scale, rw,
-                                       self.out, st)),
+            out,
             # grad_W2 (896 tiles, contraction M) and dh (1792 tiles,
             # contraction D) in one launch, the longer tiles first
             ("grad_w2_dh", "gemm", 2 * g, False, ("qw2", "qdy"),
              lambda st: fp8_linear_gemm_grouped(
-                 [(self.qdy.qt, self.qdy.scale_t, self.qh.qt, self.qh.scale_t, self.grad_w2),
+                 [grad_w2,
                   (self.qdy.q, self.qdy.scale, self.qw2.qt, self.qw2.scale_t, self.dh)],
                  rw, st, e5m2=e5)),
             # dh, a, b read; da, db written; each read again by its cast,
@@ -977,15 +1045,10 @@ class SwiGLUFFNStep:
             # grad_x = da.w1 (512 tiles, contraction H) with the grad_W of w1
             # and w3 (2 x 896 tiles, contraction M) in one launch; then
             # grad_x += db.w3
-            ("grad_x_w13", "gemm", 3 * g, False, ("qw1",), lambda st: fp8_linear_gemm_grouped(
-                [(self.qda.q, self.qda.scale, self.qw1.qt, self.qw1.scale_t, self.grad_x),
-                 (self.qda.qt, self.qda.scale_t, self.qx.qt, self.qx.scale_t, self.grad_w1),
-                 (self.qdb.qt, self.qdb.scale_t, self.qx.qt, self.qx.scale_t, self.grad_w3)],
-                rw, st, e5m2=e5)),
-            ("grad_x_acc", "gemm", g, False, ("qw3",), lambda st: fp8_linear_bwd_x_acc(
-                self.qdb.q, self.qdb.scale, self.qw3.qt, self.qw3.scale_t, M, H, D,
-                self.grad_x, rw, st, e5m2=e5)),
-        )
+            ("grad_x_w13", "gemm", 3 * g, False, ("qw1",),
+             lambda st: fp8_linear_gemm_grouped(grad_x_w13, rw, st, e5m2=e5)),
+            grad_x_acc,
+        ) + tail
 
     def run(self, side=None, record: bool = False):
         """Enqueue one step on the current stream.  With ``side`` (a second
