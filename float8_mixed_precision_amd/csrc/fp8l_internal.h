@@ -84,6 +84,13 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   return lo | (hi << 16);
 }
 
+// per-half maxima of two u16 pairs, in one instruction
+__device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                                __builtin_bit_cast(u16x2, b)));
+}
+
 // max over the two u16 halves of a dword
 __device__ __forceinline__ uint32_t hmax16(uint32_t a) {
   return max(a & 0xFFFFu, a >> 16);

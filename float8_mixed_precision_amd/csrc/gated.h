@@ -16,10 +16,10 @@
 //
 // Few tokens (M <= SKINNY_M): the time is that of reading W1 and W3 once, and
 // a tile of 256 rows would leave most compute units without a tile and most
-// of each tile's work on padding.  k_gated_skinny: a workgroup owns 16 columns
-// of h, its 8 waves split the contraction and join through LDS.  Weights go
-// straight from memory to the MFMA operands (no byte of them is used twice);
-// x comes from L2.
+// of each tile's work on padding.  k_gated_skinny: a workgroup owns 16 to 64
+// columns of h, its 8 waves split the contraction and join through LDS.
+// Weights go straight from memory to the MFMA operands (no byte of them is
+// used twice); x comes from L2.
 //
 // Part of gemm.hip (included at its end).
 #pragma once
@@ -33,7 +33,6 @@ namespace {
 
 constexpr int SKINNY_M = 64;
 constexpr int SK_WAVES = 8;
-constexpr int SK_COLS = 16;
 
 struct SkinnyArgs {
   const uint8_t *x, *w1, *w3;
@@ -56,111 +55,136 @@ __device__ __forceinline__ v8i frag(v4u lo, v4u hi) {
                (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
 
-// MB blocks of 16 tokens.  Lane l of a wave holds row l % 16 of an operand and
-// the chunks of 16 bytes at l / 16 and l / 16 + 4 of the 128-byte k-tile (the
-// same for both operands), so that one load instruction reads 64 contiguous
-// bytes of each of 16 weight rows.  Rows past M read row M - 1 (not stored).
-// UN k-tiles of a wave load together; a k-tile past the end is all zeros.
-template <int MB, bool KFULL>
+// MB blocks of 16 tokens, CB blocks of 16 columns of h.  Lane l of a wave
+// holds row l % 16 of an operand and the chunks of 16 bytes at l / 16 and l / 16
+// + 4 of the 128-byte k-tile (the same for both operands), so that one load
+// instruction reads 64 contiguous bytes of each of 16 weight rows.  Rows past
+// M or H read the last row (not stored).  UN k-tiles of a wave load together.
+// The waves join per block of tokens, so the LDS does not grow with M.
+template <int MB, int CB, int UN, bool KFULL>
 __global__ __launch_bounds__(64 * SK_WAVES) void k_gated_skinny(SkinnyArgs p) {
-  constexpr int UN = MB == 1 ? 4 : 2;
-  __shared__ v4f red[SK_WAVES][2 * MB][64];
+  static_assert(CB <= SK_WAVES, "one wave finishes each block of columns");
+  __shared__ v4f red[SK_WAVES][2 * CB][64];
   const int lane = threadIdx.x & 63;
   const int wave = threadIdx.x >> 6;
-  const int n0 = blockIdx.x * SK_COLS;
+  const int n0 = blockIdx.x * (16 * CB);
   const int K = p.K;
   const int nk = (K + BK - 1) / BK;
   const int kl = (lane >> 4) * 16;
-  const uint8_t *r1 = p.w1 + (size_t)(n0 + (lane & 15)) * K;
-  const uint8_t *r3 = p.w3 + (size_t)(n0 + (lane & 15)) * K;
-  const uint8_t *rx[MB];
+  const uint8_t *r1[CB], *r3[CB], *rx[MB];
+#pragma unroll
+  for (int c = 0; c < CB; ++c) {
+    const size_t row = (size_t)min(n0 + c * 16 + (lane & 15), p.H - 1) * K;
+    r1[c] = p.w1 + row;
+    r3[c] = p.w3 + row;
+  }
 #pragma unroll
   for (int i = 0; i < MB; ++i)
     rx[i] = p.x + (size_t)min(i * 16 + (lane & 15), p.M - 1) * K;
-  v4f acc[2][MB];
+  v4f acc[2][CB][MB];
 #pragma unroll
-  for (int i = 0; i < MB; ++i) acc[0][i] = acc[1][i] = (v4f){0.f, 0.f, 0.f, 0.f};
+  for (int c = 0; c < CB; ++c)
+#pragma unroll
+    for (int i = 0; i < MB; ++i) acc[0][c][i] = acc[1][c][i] = (v4f){0.f, 0.f, 0.f, 0.f};
   for (int t0 = wave; t0 < nk; t0 += SK_WAVES * UN) {
-    v4u f1[UN][2], f3[UN][2], fx[UN][MB][2];
+    v4u f1[UN][CB][2], f3[UN][CB][2], fx[UN][MB][2];
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
-      const int t = t0 + u * SK_WAVES;
-      const bool in = t < nk;
-      const int k = (in ? t : t0) * BK + kl;
+      const int t = t0 + u * SK_WAVES;            // past the end: loaded again, not used
+      const int k = (t < nk ? t : t0) * BK + kl;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        f1[u][c] = row_chunk<KFULL>(r1, k + c * 64, K);
-        f3[u][c] = row_chunk<KFULL>(r3, k + c * 64, K);
+      for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int i = 0; i < MB; ++i) fx[u][i][c] = row_chunk<KFULL>(rx[i], k + c * 64, K);
+        for (int c = 0; c < CB; ++c) {
+          f1[u][c][e] = row_chunk<KFULL>(r1[c], k + e * 64, K);
+          f3[u][c][e] = row_chunk<KFULL>(r3[c], k + e * 64, K);
+        }
+#pragma unroll
+        for (int i = 0; i < MB; ++i) fx[u][i][e] = row_chunk<KFULL>(rx[i], k + e * 64, K);
       }
     }
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
       if (t0 + u * SK_WAVES < nk) {               // wave-uniform
-        const v8i b1 = frag(f1[u][0], f1[u][1]), b3 = frag(f3[u][0], f3[u][1]);
 #pragma unroll
-        for (int i = 0; i < MB; ++i) {
-          const v8i ax = frag(fx[u][i][0], fx[u][i][1]);
-          acc[0][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b1, ax, acc[0][i], 0, 0, 0,
-                                                                       0, 0, 0);
-          acc[1][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b3, ax, acc[1][i], 0, 0, 0,
-                                                                       0, 0, 0);
+        for (int c = 0; c < CB; ++c) {
+          const v8i b1 = frag(f1[u][c][0], f1[u][c][1]), b3 = frag(f3[u][c][0], f3[u][c][1]);
+#pragma unroll
+          for (int i = 0; i < MB; ++i) {
+            const v8i ax = frag(fx[u][i][0], fx[u][i][1]);
+            acc[0][c][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                b1, ax, acc[0][c][i], 0, 0, 0, 0, 0, 0);
+            acc[1][c][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                b3, ax, acc[1][c][i], 0, 0, 0, 0, 0, 0);
+          }
         }
       }
     }
   }
 #pragma unroll
   for (int i = 0; i < MB; ++i) {
-    red[wave][2 * i][lane] = acc[0][i];
-    red[wave][2 * i + 1][lane] = acc[1][i];
-  }
-  __syncthreads();
-  // thread (block i, lane l): token i 16 + l % 16, columns n0 + 4 (l / 16) ...
-  const int i = wave;
-  if (i >= MB) return;
-  const int m = i * 16 + (lane & 15);
-  if (m >= p.M) return;
-  v4f a = red[0][2 * i][lane], b = red[0][2 * i + 1][lane];
+    if (i) __syncthreads();                       // the round before has been read
 #pragma unroll
-  for (int w = 1; w < SK_WAVES; ++w) {
-    a += red[w][2 * i][lane];
-    b += red[w][2 * i + 1][lane];
-  }
-  const int n = n0 + (lane >> 4) * 4;
-  const float ia = 1.0f / p.sx[p.rowwise ? m : 0];
-  float i1[4], i3[4];
+    for (int c = 0; c < CB; ++c) {
+      red[wave][2 * c][lane] = acc[0][c][i];
+      red[wave][2 * c + 1][lane] = acc[1][c][i];
+    }
+    __syncthreads();
+    // wave c, lane l: token i 16 + l % 16, columns n0 + 16 c + 4 (l / 16) ...
+    const int c = wave;
+    const int m = i * 16 + (lane & 15);
+    const int n = n0 + c * 16 + (lane >> 4) * 4;
+    if (c < CB && m < p.M && n < p.H) {
+      v4f a = red[0][2 * c][lane], b = red[0][2 * c + 1][lane];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    i1[j] = 1.0f / p.s1[p.rowwise ? n + j : 0];
-    i3[j] = 1.0f / p.s3[p.rowwise ? n + j : 0];
+      for (int w = 1; w < SK_WAVES; ++w) {
+        a += red[w][2 * c][lane];
+        b += red[w][2 * c + 1][lane];
+      }
+      const float ia = 1.0f / p.sx[p.rowwise ? m : 0];
+      float i1[4], i3[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        i1[j] = 1.0f / p.s1[p.rowwise ? n + j : 0];
+        i3[j] = 1.0f / p.s3[p.rowwise ? n + j : 0];
+      }
+      const uint2 pa = make_uint2(bf16x2_bits((a[0] * ia) * i1[0], (a[1] * ia) * i1[1]),
+                                  bf16x2_bits((a[2] * ia) * i1[2], (a[3] * ia) * i1[3]));
+      const uint2 pb = make_uint2(bf16x2_bits((b[0] * ia) * i3[0], (b[1] * ia) * i3[1]),
+                                  bf16x2_bits((b[2] * ia) * i3[2], (b[3] * ia) * i3[3]));
+      const size_t at = (size_t)m * p.H + n;
+      if (p.a) {
+        *reinterpret_cast<uint2 *>(p.a + at) = pa;
+        *reinterpret_cast<uint2 *>(p.b + at) = pb;
+      }
+      *reinterpret_cast<uint2 *>(p.h + at) =
+          make_uint2(gate_fwd2(pa.x, pb.x), gate_fwd2(pa.y, pb.y));
+    }
   }
-  const uint2 pa = make_uint2(bf16x2_bits((a[0] * ia) * i1[0], (a[1] * ia) * i1[1]),
-                              bf16x2_bits((a[2] * ia) * i1[2], (a[3] * ia) * i1[3]));
-  const uint2 pb = make_uint2(bf16x2_bits((b[0] * ia) * i3[0], (b[1] * ia) * i3[1]),
-                              bf16x2_bits((b[2] * ia) * i3[2], (b[3] * ia) * i3[3]));
-  const size_t at = (size_t)m * p.H + n;
-  if (p.a) {
-    *reinterpret_cast<uint2 *>(p.a + at) = pa;
-    *reinterpret_cast<uint2 *>(p.b + at) = pb;
-  }
-  *reinterpret_cast<uint2 *>(p.h + at) = make_uint2(gate_fwd2(pa.x, pb.x), gate_fwd2(pa.y, pb.y));
 }
 
+template <int MB, int CB, int UN>
+hipError_t skinny_shape(const SkinnyArgs &p, hipStream_t stream) {
+  const dim3 grid((unsigned)((p.H + 16 * CB - 1) / (16 * CB))), block(64 * SK_WAVES);
+  if (p.K % BK == 0)
+    hipLaunchKernelGGL((k_gated_skinny<MB, CB, UN, true>), grid, block, 0, stream, p);
+  else
+    hipLaunchKernelGGL((k_gated_skinny<MB, CB, UN, false>), grid, block, 0, stream, p);
+  return hipGetLastError();
+}
+
+// Columns per workgroup: x is read by every workgroup, so with more than 16
+// tokens a workgroup takes as many columns as still leave nearly every compute
+// unit one (14336 columns, K = 4096: 64 tokens 52 us with 16 columns, 40 with
+// 32, 33 with 64; 32 tokens 37, 30, 28; one token 24, 25).
 hipError_t skinny_launch(const SkinnyArgs &p, hipStream_t stream) {
-  const dim3 grid((unsigned)(p.H / SK_COLS)), block(64 * SK_WAVES);
-  const bool kfull = p.K % BK == 0;
-#define FP8L_SKINNY(MB)                                                              \
-  if (p.M <= 16 * (MB)) {                                                            \
-    if (kfull) hipLaunchKernelGGL((k_gated_skinny<MB, true>), grid, block, 0, stream, p);  \
-    else hipLaunchKernelGGL((k_gated_skinny<MB, false>), grid, block, 0, stream, p);       \
-    return hipGetLastError();                                                        \
-  }
-  FP8L_SKINNY(1)
-  FP8L_SKINNY(2)
-  FP8L_SKINNY(4)
-#undef FP8L_SKINNY
-  return hipErrorInvalidValue;
+  if (p.M <= 16) return skinny_shape<1, 1, 4>(p, stream);
+  const bool c4 = p.H >= 64 * 192, c2 = p.H >= 32 * 192;
+  if (p.M <= 32)
+    return c4 ? skinny_shape<2, 4, 1>(p, stream)
+              : c2 ? skinny_shape<2, 2, 2>(p, stream) : skinny_shape<2, 1, 2>(p, stream);
+  return c4 ? skinny_shape<4, 4, 1>(p, stream)
+            : c2 ? skinny_shape<4, 2, 2>(p, stream) : skinny_shape<4, 1, 2>(p, stream);
 }
 
 // ------------------------------------------------------------- launches --

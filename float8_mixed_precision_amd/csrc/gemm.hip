@@ -261,13 +261,6 @@ __device__ __forceinline__ void gate_bwd2(uint32_t dh, uint32_t a, uint32_t b, u
   db = bf16x2_bits(g0 * u0, g1 * u1);
 }
 
-// per-half maxima of two u16 pairs, in one instruction
-__device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
-  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
-                                                                __builtin_bit_cast(u16x2, b)));
-}
-
 // Maximum over each 8 (LANES = 8) or 16 neighbouring lanes, in all of them
 // (DPP: quad permutations, then a mirror within 8 and within 16 lanes).
 template <int LANES>

@@ -107,6 +107,18 @@ __device__ __forceinline__ bool owned(int k, int j, int t, int cols) {
   return c < cols && min(c, cols - 8) + j >= c;
 }
 
+// Sum of f(j) over the elements of chunk k that are this thread's to count.
+template <int LAY, int TPR, class F>
+__device__ __forceinline__ float chunk_sum(int k, int t, int cols, F f) {
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (LAY == LAY_ALIGNED) s += f(j);            // all eight or none
+    else s += owned<LAY, TPR>(k, j, t, cols) ? f(j) : 0.f;
+  }
+  return LAY != LAY_ALIGNED || chunk_start<TPR>(k, t) < cols ? s : 0.f;
+}
+
 // 16 bytes at any element's address
 template <class T>
 struct __attribute__((packed, aligned(sizeof(T)))) Any16 {
@@ -249,7 +261,7 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
                  (uint32_t)__builtin_amdgcn_readlane((int)v, 48)));
 }
 
-// Sum over a row's TPR threads, in each of them.  red: one float per wave of
+// Sum over a row's TPR threads, in each of them.  red2: one float per wave of
 // the workgroup, in two copies that successive calls take in turn (slot):
 // the barrier of the call between orders a write behind the reads of the
 // call before that, so one barrier per sum is enough.
@@ -287,19 +299,29 @@ __device__ __forceinline__ uint32_t row_umax(uint32_t v, uint32_t *red) {
 
 // --------------------------------------------------------------- forward --
 
-template <int TPR>
+// Threads of a workgroup: NORM_RW leaves one partial row per workgroup, so it
+// takes the largest; the others 256 where that holds a row.
+template <int TPR, int MODE>
 constexpr int block_threads() {
-  return TPR > 256 ? TPR : 256;
+  return MODE == NORM_RW ? 1024 : TPR > 256 ? TPR : 256;
 }
 
-// Workgroups of rows [blockIdx.x G + g, + gridDim.x G, ...), G row groups of
-// TPR threads each; every thread of a workgroup makes the same number of
-// rounds (a row past the end is computed on row rows - 1 and not stored).
+// Workgroup b takes rows b G + g, G row groups g of TPR threads each, then
+// those gridDim.x G further on, and so on; every thread of a workgroup makes
+// the same number of rounds (a row past the end is computed on row rows - 1
+// and not stored).
+//
+// Measured, statistics and maxima of 8192 x 4096 bf16 (tensorwise): 16.6 us,
+// 4.0 TB/s, the rate at which this card reads a large array, with 256 threads a
+// row and 2048 workgroups; with a wave a row 30 us (its w and b take 128
+// registers, or twice the traffic of x when read per row: 29 us), 512 threads
+// 19 us, two rows a round 17-21 us.
 template <class T, int LAY, int TPR, int CH, int MODE>
-__global__ __launch_bounds__(block_threads<TPR>()) void k_norm(NormArgs p) {
-  constexpr int G = block_threads<TPR>() / TPR;
+__global__ __launch_bounds__((block_threads<TPR, MODE>())) void k_norm(NormArgs p) {
+  constexpr int G = block_threads<TPR, MODE>() / TPR;
   constexpr bool BF = sizeof(T) == 2;
-  static_assert(MODE == NORM_Y || (BF && LAY == LAY_ALIGNED), "codes come from bf16 rows of whole chunks");
+  static_assert(MODE == NORM_Y || (BF && LAY == LAY_ALIGNED),
+                "codes come from bf16 rows of whole chunks");
   __shared__ float red[2][16];
   __shared__ uint32_t redu[16];
   const int t = threadIdx.x % TPR;
@@ -313,32 +335,47 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_norm(NormArgs p) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) cm[k][j] = 0;
 
+  // a round's row is loaded a round ahead of its use
+  Pack<T> vn[CH];
+  auto load_row = [&](int64_t r0) {
+    const T *xr = static_cast<const T *>(p.x) + min(r0 + g, p.rows - 1) * cols;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) load_chunk<LAY, TPR>(vn[k], xr, k, t, cols);
+  };
+  const int64_t step = (int64_t)gridDim.x * G;
+  const int64_t first = (int64_t)blockIdx.x * G;
+  load_row(first);
+  // the columns of a thread are the same in every round: w and b stay in its
+  // registers
+  float w[CH][8], b[CH][8];
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    load_param<LAY, TPR>(w[k], p.w, p.wf32, 1.f, k, t, cols);
+    load_param<LAY, TPR>(b[k], p.b, p.wf32, 0.f, k, t, cols);
+  }
   int slot = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * G; r0 < p.rows; r0 += (int64_t)gridDim.x * G) {
-    const bool ok = r0 + g < p.rows;
-    const int64_t r = ok ? r0 + g : p.rows - 1;
-    const T *xr = static_cast<const T *>(p.x) + r * cols;
+  for (int64_t r0 = first; r0 < p.rows; r0 += step) {
+    const int64_t r = r0 + g;
+    const bool ok = r < p.rows;
     Pack<T> v[CH];
 #pragma unroll
-    for (int k = 0; k < CH; ++k) load_chunk<LAY, TPR>(v[k], xr, k, t, cols);
+    for (int k = 0; k < CH; ++k) v[k] = vn[k];
+    if (r0 + step < p.rows) load_row(r0 + step);
     float mean = 0.f;
     if (!p.rms) {
       float s = 0.f;
 #pragma unroll
       for (int k = 0; k < CH; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          s += owned<LAY, TPR>(k, j, t, cols) ? v[k].get(j) : 0.f;
+        s += chunk_sum<LAY, TPR>(k, t, cols, [&](int j) { return v[k].get(j); });
       mean = row_sum<TPR>(s, red, slot) / (float)cols;
     }
     float s2 = 0.f;
 #pragma unroll
     for (int k = 0; k < CH; ++k)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      s2 += chunk_sum<LAY, TPR>(k, t, cols, [&](int j) {
         const float d = v[k].get(j) - mean;
-        s2 += owned<LAY, TPR>(k, j, t, cols) ? d * d : 0.f;
-      }
+        return d * d;
+      });
     const float rstd = 1.0f / sqrtf(row_sum<TPR>(s2, red, slot) * inv_n + p.eps);
     if (t == 0 && ok) {
       if (p.mean && !p.rms) p.mean[r] = mean;
@@ -348,32 +385,31 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_norm(NormArgs p) {
     uint32_t yb[CH][4];
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      float w[8], b[8], f[8];
-      load_param<LAY, TPR>(w, p.w, p.wf32, 1.f, k, t, cols);
-      load_param<LAY, TPR>(b, p.b, p.wf32, 0.f, k, t, cols);
+      float f[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = norm_value(v[k].get(j), mean, rstd, w[j], b[j]);
+      for (int j = 0; j < 8; ++j) f[j] = norm_value(v[k].get(j), mean, rstd, w[k][j], b[k][j]);
       if constexpr (BF) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) yb[k][j] = bf16x2_bits(f[2 * j], f[2 * j + 1]);
         if (p.y && ok)
           store_chunk<LAY, TPR>(static_cast<uint16_t *>(p.y) + r * cols, yb[k], k, t, cols);
         if (MODE != NORM_Y) {
-          const uint32_t keep =
-              ok && chunk_start<TPR>(k, t) < cols ? 0x7FFF7FFFu : 0u;
+          const uint32_t keep = ok && chunk_start<TPR>(k, t) < cols ? 0x7FFF7FFFu : 0u;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint32_t m = yb[k][j] & keep;
-            rm = max_u16x2(rm, m);
-            if (MODE == NORM_RW) cm[k][j] = max_u16x2(cm[k][j], m);
+            rm = pk_max(rm, m);
+            if (MODE == NORM_RW) cm[k][j] = pk_max(cm[k][j], m);
           }
         }
       } else {
         if (ok) store_chunk<LAY, TPR>(static_cast<float *>(p.y) + r * cols, f, k, t, cols);
       }
     }
-    if (MODE == NORM_TW) tw_max = max_u16x2(tw_max, rm);
+    if (MODE == NORM_TW) tw_max = pk_max(tw_max, rm);
     if (MODE == NORM_RW || MODE == NORM_ROWS) {
+      // (the next round's row_sum puts a barrier between these reads of redu
+      // and the next writes)
       const uint32_t am = row_umax<TPR>(hmax16(rm), redu);
       if (MODE == NORM_RW && t == 0 && ok) p.rowpart[r] = (uint16_t)am;
       if (MODE == NORM_ROWS) {
@@ -387,14 +423,14 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_norm(NormArgs p) {
         for (int k = 0; k < CH; ++k) {
           const int c = chunk_start<TPR>(k, t);
           const uint32_t *d = yb[k];
-          const uint32_t q0 = fp8x4<0>(bf16_to_f32(d[0] & 0xFFFFu) * s, bf16_to_f32(d[0] >> 16) * s,
-                                       bf16_to_f32(d[1] & 0xFFFFu) * s, bf16_to_f32(d[1] >> 16) * s);
-          const uint32_t q1 = fp8x4<0>(bf16_to_f32(d[2] & 0xFFFFu) * s, bf16_to_f32(d[2] >> 16) * s,
-                                       bf16_to_f32(d[3] & 0xFFFFu) * s, bf16_to_f32(d[3] >> 16) * s);
+          const uint32_t q0 =
+              fp8x4<0>(bf16_to_f32(d[0] & 0xFFFFu) * s, bf16_to_f32(d[0] >> 16) * s,
+                       bf16_to_f32(d[1] & 0xFFFFu) * s, bf16_to_f32(d[1] >> 16) * s);
+          const uint32_t q1 =
+              fp8x4<0>(bf16_to_f32(d[2] & 0xFFFFu) * s, bf16_to_f32(d[2] >> 16) * s,
+                       bf16_to_f32(d[3] & 0xFFFFu) * s, bf16_to_f32(d[3] >> 16) * s);
           if (c < cols && ok) *reinterpret_cast<uint2 *>(p.q + r * cols + c) = make_uint2(q0, q1);
         }
-        // the next round's row_sum puts a barrier between these reads of
-        // redu and the next writes
       }
     }
   }
@@ -406,7 +442,7 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_norm(NormArgs p) {
     if (threadIdx.x == 0) {
       uint32_t a = tw[0];
 #pragma unroll
-      for (int i = 1; i < block_threads<TPR>() / 64; ++i) a = max(a, tw[i]);
+      for (int i = 1; i < block_threads<TPR, MODE>() / 64; ++i) a = max(a, tw[i]);
       p.part[blockIdx.x] = a;
     }
   }
@@ -417,7 +453,7 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_norm(NormArgs p) {
     __shared__ uint32_t cred[G > 1 ? SPAN : 1];
     uint16_t *dst = p.colpart + (size_t)blockIdx.x * cols;
     if constexpr (G > 1) {
-      for (int c = threadIdx.x; c < SPAN; c += block_threads<TPR>()) cred[c] = 0;
+      for (int c = threadIdx.x; c < SPAN; c += block_threads<TPR, MODE>()) cred[c] = 0;
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < CH; ++k)
@@ -428,7 +464,7 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_norm(NormArgs p) {
           atomicMax(&cred[c + 1], cm[k][j] >> 16);
         }
       __syncthreads();
-      for (int c = threadIdx.x; c < cols; c += block_threads<TPR>()) dst[c] = (uint16_t)cred[c];
+      for (int c = threadIdx.x; c < cols; c += block_threads<TPR, MODE>()) dst[c] = (uint16_t)cred[c];
     } else {
 #pragma unroll
       for (int k = 0; k < CH; ++k) store_chunk<LAY, TPR>(dst, cm[k], k, t, cols);
@@ -485,17 +521,35 @@ __global__ __launch_bounds__(BWD_THREADS) void k_norm_bwd(NormBwdArgs p) {
   }
   __syncthreads();
   int slot = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * G; r0 < p.rows; r0 += (int64_t)gridDim.x * G) {
+  // a round's rows are loaded a round ahead, while the sums of the one before
+  // wait at their barrier (16 columns a thread leave no registers for it)
+  constexpr bool AHEAD = CH == 1;
+  Pack<T> xn[CH], dyn[CH];
+  float rstd_n = 0.f, mean_n = 0.f;
+  auto load_row = [&](int64_t r0) {
+    const int64_t r = min(r0 + g, p.rows - 1);
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      load_chunk<LAY, TPR>(xn[k], static_cast<const T *>(p.x) + r * cols, k, t, cols);
+      load_chunk<LAY, TPR>(dyn[k], static_cast<const T *>(p.dy) + r * cols, k, t, cols);
+    }
+    rstd_n = p.rstd[r];
+    mean_n = p.rms ? 0.f : p.mean[r];
+  };
+  const int64_t step = (int64_t)gridDim.x * G;
+  if (AHEAD) load_row((int64_t)blockIdx.x * G);
+  for (int64_t r0 = (int64_t)blockIdx.x * G; r0 < p.rows; r0 += step) {
     const bool ok = r0 + g < p.rows;
     const int64_t r = ok ? r0 + g : p.rows - 1;
+    if (!AHEAD) load_row(r0);
     Pack<T> x[CH], dy[CH];
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      load_chunk<LAY, TPR>(x[k], static_cast<const T *>(p.x) + r * cols, k, t, cols);
-      load_chunk<LAY, TPR>(dy[k], static_cast<const T *>(p.dy) + r * cols, k, t, cols);
+      x[k] = xn[k];
+      dy[k] = dyn[k];
     }
-    const float rstd = p.rstd[r];
-    const float mean = p.rms ? 0.f : p.mean[r];
+    const float rstd = rstd_n, mean = mean_n;
+    if (AHEAD && r0 + step < p.rows) load_row(r0 + step);
     float s1 = 0.f, s2 = 0.f;                     // sums of g xh and of g
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
@@ -631,37 +685,45 @@ __global__ __launch_bounds__(64 * FIN_SLICES) void k_norm_bwd_finish(
 
 constexpr int kComputeUnits = 256;
 // most workgroups of a pass that leaves one partial row each
-constexpr int kMaxSlices = 512;
+constexpr int kMaxSlices = kComputeUnits;
 
-// Calls f with the pass's kernel shape (TPR, CH) for `cols` columns; `wide`
-// prefers more threads per row.
+// Calls f with a pass's kernel shape (TPR, CH) for `cols` columns: 8 columns a
+// thread, or 16 (`wide`; and always for the widest rows).
 template <class F>
 hipError_t with_shape(int cols, bool wide, F f) {
 #define FP8L_SHAPE(TPR, CH)                                                  \
   if (cols <= (TPR) * 8 * (CH))                                              \
     return f(std::integral_constant<int, TPR>(), std::integral_constant<int, CH>());
-  if (!wide) {
-    FP8L_SHAPE(64, 1)
+  FP8L_SHAPE(64, 1)
+  if (wide) {
     FP8L_SHAPE(64, 2)
-    FP8L_SHAPE(64, 4)
-    FP8L_SHAPE(64, 8)
+    FP8L_SHAPE(128, 2)
+    FP8L_SHAPE(256, 2)
+    FP8L_SHAPE(512, 2)
+  } else {
+    FP8L_SHAPE(128, 1)
+    FP8L_SHAPE(256, 1)
+    FP8L_SHAPE(512, 1)
+    FP8L_SHAPE(1024, 1)
   }
-  FP8L_SHAPE(256, 1)
-  FP8L_SHAPE(256, 2)
-  FP8L_SHAPE(256, 4)
   FP8L_SHAPE(1024, 2)
 #undef FP8L_SHAPE
   return hipErrorInvalidValue;
 }
 
-// A row by one wave once every SIMD has one (4 per compute unit).
-bool few_rows(int64_t rows) { return rows < 4 * kComputeUnits; }
+// The forward takes 16 columns a thread where there are at least 4 rows for
+// every compute unit: one row of 4096 takes 3.9 us with 256 threads, 3.0 with
+// 512; 8192 rows 16.6 against 19.
+bool many_rows(int64_t rows) { return rows >= 4 * kComputeUnits; }
 
 template <class T, int LAY, int MODE>
 hipError_t launch_norm(const NormArgs &a, int64_t max_blocks, int *blocks, hipStream_t stream) {
+  static_assert(TW_MAX_BLOCKS >= kComputeUnits * 8, "one maximum per workgroup");
   auto launch = [&](auto tpr, auto ch) {
     constexpr int TPR = decltype(tpr)::value, CH = decltype(ch)::value;
-    constexpr int BLK = block_threads<TPR>();
+    constexpr int BLK = block_threads<TPR, MODE>();
+    // as many waves as a compute unit holds, each walking its rows
+    if (max_blocks > kComputeUnits * (2048 / BLK)) max_blocks = kComputeUnits * (2048 / BLK);
     int64_t nb = cdiv(a.rows, BLK / TPR);
     if (nb > max_blocks) nb = max_blocks;
     *blocks = (int)nb;
@@ -672,21 +734,7 @@ hipError_t launch_norm(const NormArgs &a, int64_t max_blocks, int *blocks, hipSt
   if constexpr (LAY == LAY_SCALAR)
     return launch(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
   else
-    return with_shape(a.cols, few_rows(a.rows), launch);
-}
-
-template <class F>
-hipError_t with_bwd_shape(int cols, F f) {
-#define FP8L_SHAPE(TPR, CH)                                                  \
-  if (cols <= (TPR) * 8 * (CH))                                              \
-    return f(std::integral_constant<int, TPR>(), std::integral_constant<int, CH>());
-  FP8L_SHAPE(64, 1)
-  FP8L_SHAPE(256, 1)
-  FP8L_SHAPE(256, 2)
-  FP8L_SHAPE(1024, 1)
-  FP8L_SHAPE(1024, 2)
-#undef FP8L_SHAPE
-  return hipErrorInvalidValue;
+    return with_shape(a.cols, many_rows(a.rows), launch);
 }
 
 template <class T, int LAY>
@@ -703,7 +751,7 @@ hipError_t launch_bwd(const NormBwdArgs &a, int *blocks, hipStream_t stream) {
   if constexpr (LAY == LAY_SCALAR)
     return launch(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
   else
-    return with_bwd_shape(a.cols, launch);
+    return with_shape(a.cols, false, launch);
 }
 
 // f(LAY) for a width
@@ -736,9 +784,8 @@ NormArgs make_args(const NormIn &in, void *y, float *mean, float *rstd) {
   return a;
 }
 
-// Workgroups of a pass without partials: enough rounds that a launch of any
-// size stays within a 32-bit grid.
-constexpr int64_t kMaxBlocks = 1 << 20;
+// Workgroups of a pass without partials (as many as the chip holds).
+constexpr int64_t kMaxBlocks = 8 * kComputeUnits;
 
 }  // namespace
 

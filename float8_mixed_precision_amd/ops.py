@@ -11,6 +11,7 @@ dtypes (bf16 for x / outputs, uint8 for the fp8 codes, float32 for scales).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -376,43 +377,50 @@ def fp8_swiglu_bwd(dh: torch.Tensor, a: torch.Tensor, b: torch.Tensor, rowwise: 
 _DTYPES = {torch.bfloat16: FP8L_BF16, torch.float32: FP8L_F32}
 
 
-class _on_device:
-    """Makes the device of tensor t current around a call (a default stream
-    is that of the current device) and checks that the other tensors given
-    (None allowed) are on it, dense, and of the stated type and shape."""
+def _checked(device, *tensors) -> None:
+    """Each (name, tensor or None, dtype, shape) on `device`, of that type
+    and shape, and dense."""
+    index = -1 if device.type == "cpu" else device.index
+    for name, t, dtype, shape in tensors:
+        if t is not None and (t.dtype is not dtype or t.shape != shape
+                              or t.get_device() != index or not t.is_contiguous()):
+            raise ValueError("%s must be a dense %s %s on %s, not a %s%s %s on %s" % (
+                name, dtype, tuple(shape), device, "" if t.is_contiguous() else "strided ",
+                t.dtype, tuple(t.shape), t.device))
 
-    def __init__(self, t, **tensors):
-        for name, (u, dtype, shape) in tensors.items():
-            if u is None:
-                continue
-            if u.device != t.device:
-                raise ValueError("%s is on %s, not on %s" % (name, u.device, t.device))
-            if u.dtype != dtype or tuple(u.shape) != tuple(shape):
-                raise ValueError("%s must be %s %s, not %s %s" % (
-                    name, dtype, tuple(shape), u.dtype, tuple(u.shape)))
-            if not u.is_contiguous():
-                raise ValueError("%s must be contiguous" % name)
-        self.guard = (torch.cuda.device(t.device)
-                      if t.device.type == "cuda"
-                      and t.device.index != torch.cuda.current_device() else None)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
+_NO_GUARD = contextlib.nullcontext()
 
-    def __exit__(self, *a):
-        if self.guard is not None:
-            self.guard.__exit__(*a)
+
+def _on_device(device):
+    """Makes `device` current around a call: a default stream belongs to the
+    current device."""
+    if device.type != "cuda" or device.index == torch.cuda.current_device():
+        return _NO_GUARD
+    return torch.cuda.device(device)
+
+
+def _ws(workspace, device):
+    """(address, bytes) of a workspace tensor or None."""
+    if workspace is None:
+        return None, 0
+    _checked(device, ("workspace", workspace, torch.uint8, workspace.shape))
+    return workspace.data_ptr(), workspace.numel()
+
+
+def _a(t):
+    return None if t is None else t.data_ptr()
 
 
 def _norm_params(x, weight, bias):
     """Checked dtypes of a norm call: (type of x, type of weight and bias)."""
-    if x.dim() != 2 or x.dtype not in _DTYPES:
+    xd = x.dtype
+    if xd not in _DTYPES or x.dim() != 2:
         raise ValueError("x must be a [rows, cols] bf16 or fp32 matrix")
-    ps = [p for p in (weight, bias) if p is not None]
-    if any(p.dtype != ps[0].dtype or p.dtype not in _DTYPES for p in ps):
+    pd = weight.dtype if weight is not None else bias.dtype if bias is not None else xd
+    if pd not in _DTYPES or (weight is not None and bias is not None and bias.dtype is not pd):
         raise ValueError("weight and bias must be both bf16 or both fp32")
-    return x.dtype, ps[0].dtype if ps else torch.float32
+    return xd, pd
 
 
 def fp8_layernorm_workspace_bytes(rows: int, cols: int, rowwise: bool = False) -> int:
@@ -435,18 +443,20 @@ def fp8_layernorm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     statistics fp32 [rows], kept for fp8_layernorm_bwd."""
     xd, pd = _norm_params(x, weight, bias)
     rows, cols = x.shape
-    f32 = torch.float32
-    with _on_device(x, x=(x, xd, x.shape), weight=(weight, pd, (cols,)), bias=(bias, pd, (cols,)),
-                    y=(y, xd, x.shape), mean=(mean, f32, (rows,)), rstd=(rstd, f32, (rows,))):
+    f32, dev = torch.float32, x.device
+    _checked(dev, ("x", x, xd, x.shape), ("weight", weight, pd, (cols,)),
+             ("bias", bias, pd, (cols,)), ("y", y, xd, x.shape), ("mean", mean, f32, (rows,)),
+             ("rstd", rstd, f32, (rows,)))
+    with _on_device(dev):
         if y is None:
             y = torch.empty_like(x)
         if mean is None and not rms:
-            mean = torch.empty(rows, dtype=f32, device=x.device)
+            mean = torch.empty(rows, dtype=f32, device=dev)
         if rstd is None:
-            rstd = torch.empty(rows, dtype=f32, device=x.device)
+            rstd = torch.empty(rows, dtype=f32, device=dev)
         _check(lib().fp8_layernorm_fwd(
-            _p(x), rows, cols, int(rms), _DTYPES[xd], _p(weight), _p(bias), _DTYPES[pd], eps,
-            _p(y), None if rms else _p(mean), _p(rstd), _stream(stream)), "fp8_layernorm_fwd")
+            _a(x), rows, cols, int(rms), _DTYPES[xd], _a(weight), _a(bias), _DTYPES[pd], eps,
+            _a(y), None if rms else _a(mean), _a(rstd), _stream(stream)), "fp8_layernorm_fwd")
     return y, None if rms else mean, rstd
 
 
@@ -482,22 +492,21 @@ def fp8_layernorm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = Non
             mean = torch.empty(rows, dtype=f32, device=dev)
         if rstd is None:
             rstd = torch.empty(rows, dtype=f32, device=dev)
-    with _on_device(x, x=(x, bf, x.shape), weight=(weight, pd, (cols,)), bias=(bias, pd, (cols,)),
-                    y=(y, bf, x.shape), mean=(mean, f32, (rows,)), rstd=(rstd, f32, (rows,)),
-                    q=(out.q, u8, (rows, cols)),
-                    qt=(out.qt if transposed else None, u8, (cols, rows)),
-                    scale=(out.scale, f32, (ns,)),
-                    scale_t=(out.scale_t if transposed else None, f32, (nst,)),
-                    amax=(out.amax, f32, (na,))):
+    _checked(dev, ("x", x, bf, x.shape), ("weight", weight, pd, (cols,)),
+             ("bias", bias, pd, (cols,)), ("y", y, bf, x.shape), ("mean", mean, f32, (rows,)),
+             ("rstd", rstd, f32, (rows,)), ("q", out.q, u8, (rows, cols)),
+             ("scale", out.scale, f32, (ns,)), ("amax", out.amax, f32, (na,)))
+    if transposed:
+        _checked(dev, ("qt", out.qt, u8, (cols, rows)), ("scale_t", out.scale_t, f32, (nst,)))
+    with _on_device(dev):
         if transposed and workspace is None:
             workspace = alloc_layernorm_workspace(rows, cols, dev, rowwise)
         _check(lib().fp8_layernorm_quantize(
-            _p(x), rows, cols, int(rms), _p(weight), _p(bias), _DTYPES[pd], eps,
-            _scaling(rowwise), _p(y), None if rms else _p(mean), _p(rstd), _p(out.q),
-            _p(out.qt) if transposed else None, _p(out.scale),
-            _p(out.scale_t) if transposed else None, _p(out.amax), _p(workspace),
-            workspace.numel() if workspace is not None else 0, _stream(stream)),
-            "fp8_layernorm_quantize")
+            _a(x), rows, cols, int(rms), _a(weight), _a(bias), _DTYPES[pd], eps,
+            _scaling(rowwise), _a(y), None if rms else _a(mean), _a(rstd), _a(out.q),
+            _a(out.qt) if transposed else None, _a(out.scale),
+            _a(out.scale_t) if transposed else None, _a(out.amax), *_ws(workspace, dev),
+            _stream(stream)), "fp8_layernorm_quantize")
     return out, None if rms else mean, rstd
 
 
@@ -512,9 +521,10 @@ def fp8_layernorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.
     xd, pd = _norm_params(x, weight, None)
     rows, cols = x.shape
     f32, dev = torch.float32, x.device
-    with _on_device(x, x=(x, xd, x.shape), dy=(dy, xd, x.shape), weight=(weight, pd, (cols,)),
-                    mean=(mean, f32, (rows,)), rstd=(rstd, f32, (rows,)), dx=(dx, xd, x.shape),
-                    dweight=(dweight, f32, (cols,)), dbias=(dbias, f32, (cols,))):
+    _checked(dev, ("x", x, xd, x.shape), ("dy", dy, xd, x.shape), ("weight", weight, pd, (cols,)),
+             ("mean", mean, f32, (rows,)), ("rstd", rstd, f32, (rows,)), ("dx", dx, xd, x.shape),
+             ("dweight", dweight, f32, (cols,)), ("dbias", dbias, f32, (cols,)))
+    with _on_device(dev):
         if want_x and dx is None:
             dx = torch.empty_like(x)
         if want_w and dweight is None:
@@ -526,10 +536,9 @@ def fp8_layernorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.
         if workspace is None and (want_w or want_b):
             workspace = alloc_layernorm_workspace(rows, cols, dev)
         _check(lib().fp8_layernorm_bwd(
-            _p(dy), _p(x), _p(weight), None if rms else _p(mean), _p(rstd), rows, cols, int(rms),
-            _DTYPES[xd], _DTYPES[pd], _p(dx), _p(dweight), _p(dbias), _p(workspace),
-            workspace.numel() if workspace is not None else 0, _stream(stream)),
-            "fp8_layernorm_bwd")
+            _a(dy), _a(x), _a(weight), None if rms else _a(mean), _a(rstd), rows, cols, int(rms),
+            _DTYPES[xd], _DTYPES[pd], _a(dx), _a(dweight), _a(dbias), *_ws(workspace, dev),
+            _stream(stream)), "fp8_layernorm_bwd")
     return dx, dweight, dbias
 
 
@@ -546,19 +555,22 @@ def alloc_gated_workspace(M: int, H: int, rowwise: bool, device) -> torch.Tensor
                        device=device)
 
 
-def _operands(prefix, q, s, rows, k, rowwise):
-    """_on_device's checks of an fp8 operand: codes [rows, k] and scales."""
-    return {prefix + "q": (q, torch.uint8, (rows, k)),
-            prefix + " scale": (s, torch.float32, (rows if rowwise else 1,))}
+def _operand(name, q, s, rows, k, rowwise):
+    """_checked's entries of an fp8 operand: codes [rows, k] and scales."""
+    return ((name, q, torch.uint8, (rows, k)),
+            (name + " scale", s, torch.float32, (rows if rowwise else 1,)))
 
 
-def _quantized(prefix, z, M, H, rowwise):
-    """_on_device's checks of the quantize outputs of an [M, H] matrix."""
+def _quantized(name, z, M, H, rowwise):
+    """_checked's entries of the quantize outputs of an [M, H] matrix."""
     u8, f32 = torch.uint8, torch.float32
     ns, nst, na = (M, H, M + H) if rowwise else (1, 1, 1)
-    return {prefix + "q": (z.q, u8, (M, H)), prefix + "qt": (z.qt, u8, (H, M)),
-            prefix + "scale": (z.scale, f32, (ns,)), prefix + "scale_t": (z.scale_t, f32, (nst,)),
-            prefix + "amax": (z.amax, f32, (na,))}
+    return ((name + "q", z.q, u8, (M, H)), (name + "qt", z.qt, u8, (H, M)),
+            (name + " scale", z.scale, f32, (ns,)), (name + " scale_t", z.scale_t, f32, (nst,)),
+            (name + " amax", z.amax, f32, (na,)))
+
+
+_NO_CODES = Quantized(None, None, None, None, None)
 
 
 def fp8_gated_fwd(xq: torch.Tensor, sx: torch.Tensor, w1q: torch.Tensor, sw1: torch.Tensor,
@@ -571,28 +583,23 @@ def fp8_gated_fwd(xq: torch.Tensor, sx: torch.Tensor, w1q: torch.Tensor, sw1: to
     given, the two projections are stored there for fp8_gated_bwd; with
     ``out`` given (M a multiple of 16), h is quantized into it."""
     (M, K), H = xq.shape, w1q.shape[0]
-    bf = torch.bfloat16
-    checks = {}
-    checks.update(_operands("x", xq, sx, M, K, rowwise))
-    checks.update(_operands("w1", w1q, sw1, H, K, rowwise))
-    checks.update(_operands("w3", w3q, sw3, H, K, rowwise))
+    bf, dev = torch.bfloat16, xq.device
+    z = out if out is not None else _NO_CODES
+    _checked(dev, *_operand("xq", xq, sx, M, K, rowwise), *_operand("w1q", w1q, sw1, H, K, rowwise),
+             *_operand("w3q", w3q, sw3, H, K, rowwise), ("a", a, bf, (M, H)), ("b", b, bf, (M, H)),
+             ("h", h, bf, (M, H)))
     if out is not None:
-        checks.update(_quantized("h", out, M, H, rowwise))
-    with _on_device(xq, a=(a, bf, (M, H)), b=(b, bf, (M, H)), h=(h, bf, (M, H)), **checks):
+        _checked(dev, *_quantized("h", out, M, H, rowwise))
+    with _on_device(dev):
         if h is None:
-            h = torch.empty((M, H), dtype=bf, device=xq.device)
+            h = torch.empty((M, H), dtype=bf, device=dev)
         if out is not None and workspace is None:
-            workspace = alloc_gated_workspace(M, H, rowwise, xq.device)
-        z = out if out is not None else _NO_CODES
+            workspace = alloc_gated_workspace(M, H, rowwise, dev)
         _check(lib().fp8_gated_fwd(
-            _p(xq), _p(sx), _p(w1q), _p(sw1), _p(w3q), _p(sw3), M, H, K, _scaling(rowwise),
-            _p(a), _p(b), _p(h), _p(z.q), _p(z.qt), _p(z.scale), _p(z.scale_t), _p(z.amax),
-            _p(workspace), workspace.numel() if workspace is not None else 0, _stream(stream)),
-            "fp8_gated_fwd")
+            _a(xq), _a(sx), _a(w1q), _a(sw1), _a(w3q), _a(sw3), M, H, K, _scaling(rowwise),
+            _a(a), _a(b), _a(h), _a(z.q), _a(z.qt), _a(z.scale), _a(z.scale_t), _a(z.amax),
+            *_ws(workspace, dev), _stream(stream)), "fp8_gated_fwd")
     return h
-
-
-_NO_CODES = Quantized(None, None, None, None, None)
 
 
 def fp8_gated_bwd(dyq: torch.Tensor, sdy: torch.Tensor, w2tq: torch.Tensor, sw2t: torch.Tensor,
@@ -605,14 +612,13 @@ def fp8_gated_bwd(dyq: torch.Tensor, sdy: torch.Tensor, w2tq: torch.Tensor, sw2t
     kernel and the two casts; dY's and the outputs' codes E5M2 when e5m2."""
     (M, D), H = dyq.shape, w2tq.shape[0]
     bf, dev = torch.bfloat16, dyq.device
-    checks = {}
-    checks.update(_operands("dy", dyq, sdy, M, D, rowwise))
-    checks.update(_operands("w2t", w2tq, sw2t, H, D, rowwise))
-    for name, z in (("da ", qa), ("db ", qb)):
+    _checked(dev, *_operand("dyq", dyq, sdy, M, D, rowwise),
+             *_operand("w2tq", w2tq, sw2t, H, D, rowwise), ("a", a, bf, (M, H)),
+             ("b", b, bf, (M, H)), ("da", da, bf, (M, H)), ("db", db, bf, (M, H)))
+    for name, z in (("da", qa), ("db", qb)):
         if z is not None:
-            checks.update(_quantized(name, z, M, H, rowwise))
-    with _on_device(dyq, a=(a, bf, (M, H)), b=(b, bf, (M, H)), da=(da, bf, (M, H)),
-                    db=(db, bf, (M, H)), **checks):
+            _checked(dev, *_quantized(name, z, M, H, rowwise))
+    with _on_device(dev):
         da = torch.empty((M, H), dtype=bf, device=dev) if da is None else da
         db = torch.empty((M, H), dtype=bf, device=dev) if db is None else db
         qa = alloc_quantized(M, H, rowwise, dev) if qa is None else qa
@@ -620,10 +626,10 @@ def fp8_gated_bwd(dyq: torch.Tensor, sdy: torch.Tensor, w2tq: torch.Tensor, sw2t
         if workspace is None:
             workspace = alloc_gated_workspace(M, H, rowwise, dev)
         _check(lib().fp8_gated_bwd(
-            _p(dyq), _p(sdy), _p(w2tq), _p(sw2t), _p(a), _p(b), M, H, D, _scaling(rowwise, e5m2),
-            _p(da), _p(db), _p(qa.q), _p(qa.qt), _p(qa.scale), _p(qa.scale_t), _p(qa.amax),
-            _p(qb.q), _p(qb.qt), _p(qb.scale), _p(qb.scale_t), _p(qb.amax), _p(workspace),
-            workspace.numel(), _stream(stream)), "fp8_gated_bwd")
+            _a(dyq), _a(sdy), _a(w2tq), _a(sw2t), _a(a), _a(b), M, H, D, _scaling(rowwise, e5m2),
+            _a(da), _a(db), _a(qa.q), _a(qa.qt), _a(qa.scale), _a(qa.scale_t), _a(qa.amax),
+            _a(qb.q), _a(qb.qt), _a(qb.scale), _a(qb.scale_t), _a(qb.amax),
+            *_ws(workspace, dev), _stream(stream)), "fp8_gated_bwd")
     return da, db, qa, qb
 
 
