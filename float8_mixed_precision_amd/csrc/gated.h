@@ -193,7 +193,7 @@ hipError_t skinny_launch(const SkinnyArgs &p, hipStream_t stream) {
 // the gate's own fields set; tile counts and the grid follow here.
 template <int EPI, int FA>
 hipError_t launch_gate(GateArgs &g, bool rowwise, int *blocks, hipStream_t stream) {
-  constexpr int TN = EPI == EPI_GATE ? BN / 2 : BN;
+  constexpr int TN = is_gate(EPI) ? BN / 2 : BN;
   g.count = 1;
   g.tiles_m[0] = (g.M[0] + BM - 1) / BM;
   g.tiles_n[0] = (g.N[0] + TN - 1) / TN;
@@ -210,12 +210,13 @@ hipError_t launch_gate(GateArgs &g, bool rowwise, int *blocks, hipStream_t strea
 }
 
 // Partial maxima of one output in its share of the workspace: rowwise the
-// row maxima per 64 columns, then (256-byte aligned) the column maxima per 128
-// rows; tensorwise one u32 per wave of at most 256 workgroups.
-int64_t row_slices(int64_t H) { return (H + BN - 1) / BN * 4; }
+// row maxima per wave of a tile (64 columns of h, 128 of da and db), then
+// (256-byte aligned) the column maxima per 128 rows; tensorwise one u32 per wave
+// of at most 256 workgroups.
+int64_t row_slices(int64_t H, int tile) { return (H + tile - 1) / tile * 2; }
 int64_t col_slices(int64_t M) { return (M + BM - 1) / BM * 2; }
 size_t colpart_at(int64_t M, int64_t H) {
-  return ((size_t)(row_slices(H) * M) * sizeof(uint16_t) + 255) & ~(size_t)255;
+  return ((size_t)(row_slices(H, BN / 2) * M) * sizeof(uint16_t) + 255) & ~(size_t)255;
 }
 size_t gate_share_bytes(int64_t M, int64_t H, bool rowwise) {
   const size_t b = rowwise ? colpart_at(M, H) + (size_t)(col_slices(M) * H) * sizeof(uint16_t)
@@ -225,14 +226,14 @@ size_t gate_share_bytes(int64_t M, int64_t H, bool rowwise) {
 
 // The partial maxima of output o: where the kernel writes them (g) and where
 // the cast reads them (src).
-void set_partials(GateArgs &g, int o, CastSource &src, void *share, bool rowwise, int tile_slices) {
+void set_partials(GateArgs &g, int o, CastSource &src, void *share, bool rowwise, int tile) {
   if (rowwise) {
     g.rowpart[o] = static_cast<uint16_t *>(share);
     g.colpart[o] = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(share) +
                                                 colpart_at(g.M[0], g.N[0]));
     src.rowpart = g.rowpart[o];
     src.colpart = g.colpart[o];
-    src.row_slices = tile_slices;
+    src.row_slices = (int)row_slices(g.N[0], tile);
     src.col_slices = (int)col_slices(g.M[0]);
   } else {
     g.part[o] = static_cast<uint32_t *>(share);
@@ -280,9 +281,10 @@ hipError_t gated_fwd_launch(const uint8_t *xq, const float *sx, const uint8_t *w
     g.maxima = o != nullptr;
     CastSource src = {};
     src.x = h;
-    if (o) set_partials(g, 0, src, workspace, rw, (int)((H + BN / 2 - 1) / (BN / 2) * 2));
+    if (o) set_partials(g, 0, src, workspace, rw, BN / 2);
     int blocks = 0;
-    const hipError_t e = launch_gate<EPI_GATE, 0>(g, rw, &blocks, stream);
+    const hipError_t e = a ? launch_gate<EPI_GATE_AB, 0>(g, rw, &blocks, stream)
+                           : launch_gate<EPI_GATE, 0>(g, rw, &blocks, stream);
     if (e != hipSuccess || !o) return e;
     src.nparts = blocks * 4;
     return quantize_cast_launch(src, M, H, scaling, *o, stream);
@@ -334,9 +336,8 @@ hipError_t gated_bwd_launch(const uint8_t *dyq, const float *sdy, const uint8_t 
   CastSource sa = {}, sb = {};
   sa.x = da;
   sb.x = db;
-  const int slices = (int)row_slices(H);
-  set_partials(g, 0, sa, workspace, rw, slices);
-  set_partials(g, 1, sb, static_cast<uint8_t *>(workspace) + gate_share_bytes(M, H, rw), rw, slices);
+  set_partials(g, 0, sa, workspace, rw, BN);
+  set_partials(g, 1, sb, static_cast<uint8_t *>(workspace) + gate_share_bytes(M, H, rw), rw, BN);
   int blocks = 0;
   hipError_t e = (scaling & FP8L_E5M2) ? launch_gate<EPI_DGATE, 1>(g, rw, &blocks, stream)
                                        : launch_gate<EPI_DGATE, 0>(g, rw, &blocks, stream);

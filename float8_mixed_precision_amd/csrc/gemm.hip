@@ -198,7 +198,7 @@ static_assert(sizeof(GemmGroup) <= 4096, "kernel arguments");
 //             128 rows of B2, dealt so that every wave's 128 slab rows are 64
 //             of each, for the same columns.  A wave's accumulators j and
 //             j + 4 are then a and b of the same elements and the gate needs
-//             no exchange.  C receives h; a and b are stored where wanted.
+//             no exchange.  C receives h.
 //  EPI_DGATE  the gradient through the gate: with dh = A B^T (rounded to
 //             bf16, as the plain GEMM writes it) and the forward pass's a and
 //             b read where the tile is finished, C receives
@@ -207,12 +207,15 @@ static_assert(sizeof(GemmGroup) <= 4096, "kernel arguments");
 // and db) where `maxima` is set: tensorwise one u32 per wave of the launch in
 // part[o], rowwise the row maxima over each wave's columns in
 // rowpart[o][slice][M] and the column maxima over its rows in
-// colpart[o][slice][N], one slice per wave column / wave row of the tiles.
-constexpr int EPI_NONE = 0, EPI_GATE = 1, EPI_DGATE = 2;
+// colpart[o][slice][N], one slice per wave column / wave row of the tiles
+// (EPI_DGATE takes them always).
+//  EPI_GATE_AB is EPI_GATE with a and b stored.
+constexpr int EPI_NONE = 0, EPI_GATE = 1, EPI_GATE_AB = 2, EPI_DGATE = 3;
+constexpr bool is_gate(int epi) { return epi == EPI_GATE || epi == EPI_GATE_AB; }
 struct GateArgs : GemmGroup {
-  const uint8_t *B2;           // EPI_GATE
+  const uint8_t *B2;           // is_gate(EPI)
   const float *sb2;
-  uint16_t *a, *b;             // EPI_GATE: stored unless NULL; EPI_DGATE: read
+  uint16_t *a, *b;             // EPI_GATE_AB: written; EPI_DGATE: read
   uint16_t *C2;                // EPI_DGATE
   int maxima;
   uint32_t *part[2];
@@ -412,7 +415,7 @@ __device__ __forceinline__ TileCoord decode_tile(const GemmGroup &g, int b, int 
   return {0, 0, 0, false};
 }
 
-// EPI_GATE, rowwise: the 4 scales of lane l of a wave whose rows start at m
+// is_gate(EPI), rowwise: the 4 scales of lane l of a wave whose rows start at m
 // and whose columns start at n: lanes 0-31 the wave's 128 rows, lanes 32-47
 // its 64 columns of B, lanes 48-63 of B2.  Indices are clamped into the
 // arrays (the outputs past them are not stored).
@@ -455,13 +458,13 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
   static_assert(EPI == EPI_NONE || (!F32 && !ACC), "gate forms write bf16");
   // rowwise scales two tiles ahead by DMA; EPI_GATE, whose columns come from
   // two tensors, loads each tile's scales beside its last k-tile instead
-  constexpr bool RWT = RW && EPI != EPI_GATE;
-  // stores every lane has certainly issued after an epilogue began (EPI_GATE
-  // without a and b: h's alone), which the next tile's first wait may leave
-  // in flight; 48 of EPI_DGATE's 64 (the counter has 6 bits)
-  constexpr int IN_FLIGHT = EPI == EPI_GATE ? 16 : EPI == EPI_DGATE ? 48 : EPI_STORES;
-  // column of the matrix per tile column of the operand slab
-  constexpr int TN = EPI == EPI_GATE ? BN / 2 : BN;
+  constexpr bool RWT = RW && !is_gate(EPI);
+  // stores every lane has certainly issued after an epilogue began, which the
+  // next tile's first wait may leave in flight; 48 of EPI_DGATE's 64 (the
+  // counter has 6 bits)
+  constexpr int IN_FLIGHT = EPI == EPI_GATE ? 16 : EPI == EPI_NONE ? EPI_STORES : 48;
+  // columns of the output per tile
+  constexpr int TN = is_gate(EPI) ? BN / 2 : BN;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[EPI_OFF + EPI_BYTES];
   const int G = gridDim.x;
   const int tid = threadIdx.x;
@@ -518,7 +521,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
     const int lr_v = lane_v >> 3;                                               \
     const int ce_v = (lane_v & 7) ^ lr_v;                                       \
     _Pragma("unroll") for (int q = 0; q < 16; ++q) {                            \
-      const int row = (EPI == EPI_GATE && q >= 8 ? wave >> 1 : wave) * 64 +     \
+      const int row = (is_gate(EPI) && q >= 8 ? wave >> 1 : wave) * 64 +        \
                       (q & 7) * 8 + lr_v;                                       \
       voff[q] = (uint32_t)(row * d_K + ((q & 1) ? ce_v ^ 1 : ce_v) * 16);       \
     }                                                                           \
@@ -542,7 +545,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
         (void *)(pick(g.A, pi_) + (size_t)m0_ * K_), (short)0,                  \
         d_valid ? (M_ - m0_) * K_ : 0, 0x00020000);                             \
     const uint8_t *B_ = pick(g.B, pi_);                                         \
-    if constexpr (EPI == EPI_GATE) B_ = (wave & 1) ? g.B2 : B_;                 \
+    if constexpr (is_gate(EPI)) B_ = (wave & 1) ? g.B2 : B_;                    \
     d_rsB = __builtin_amdgcn_make_buffer_rsrc(                                  \
         (void *)(B_ + (size_t)n0_ * K_), (short)0,                              \
         d_valid ? (N_ - n0_) * K_ : 0, 0x00020000);                             \
@@ -724,8 +727,11 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
     v4f *r_ = FP8P_RCP_AT(0);
     *r_ = recip4(*r_);
   }
-  // EPI_GATE, EPI_DGATE: tensorwise maxima of this wave's outputs so far (u16 pairs)
-  uint32_t tmax0 = 0, tmax1 = 0;
+  // the gate's forms, tensorwise: the maxima of this wave's outputs so far (u16
+  // pairs per lane) wait in its staging, which frees their registers for the
+  // main loop
+#define FP8P_TMAX() (reinterpret_cast<uint2 *>(epi) + hw_lane())
+  if (EPI != EPI_NONE && !RW) *FP8P_TMAX() = make_uint2(0u, 0u);
   int st = 0;          // stage of the current unit
   for (int tile = 0;; ++tile) {
     const TileCoord tc = {a_pi, a_m0, a_n0, a_ok};
@@ -783,7 +789,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
   do {                                                                            \
     v4f *rn_ = nullptr;                                                           \
     v4f sn_ = {};                                                                 \
-    if constexpr (EPI == EPI_GATE && RW) {                                        \
+    if constexpr (is_gate(EPI) && RW) {                                           \
       sn_ = gate_scales(g, hw_lane(), m0 + wm * WM, n0 + wn * (WN / 2));          \
       rn_ = reinterpret_cast<v4f *>(epi) + hw_lane();                             \
     }                                                                             \
@@ -865,112 +871,234 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
     // rowwise: the tile's reciprocal scales
     const float *tab = reinterpret_cast<const float *>(epi + (tile & 1) * SCALE_BYTES);
     uint8_t *stg = epi + RW_STAGE_OFF;            // rowwise staging
-    // EPI_DGATE: a and b read, db written at the offsets of da in C
-    __amdgpu_buffer_rsrc_t rsGA = rsC, rsGB = rsC, rsC2 = rsC;
-    if constexpr (EPI == EPI_DGATE) {
-      rsGA = __builtin_amdgcn_make_buffer_rsrc(g.a, (short)0, M * N * 2, 0x00020000);
-      rsGB = __builtin_amdgcn_make_buffer_rsrc(g.b, (short)0, M * N * 2, 0x00020000);
-      rsC2 = __builtin_amdgcn_make_buffer_rsrc(g.C2, (short)0, M * N * 2, 0x00020000);
-    }
-    if constexpr (EPI == EPI_GATE) {
-      // 32 rows x 64 columns (128 B) of a, b and h per pass, staged one after
-      // the other (row r's 16-byte chunk c at c ^ (r % 8), its 8-byte halves
-      // swapped where r % 16 >= 8); rowwise reciprocals come from the table
-      // that the last k-tile left: 128 rows, 64 columns of B, 64 of B2
+    if constexpr (is_gate(EPI)) {
+      // 16 rows x 64 columns (128 B) per pass of a, b and h, each staged in
+      // 2 KB of its own (row r's 16-byte chunk c at c ^ (r % 8), its 8-byte
+      // halves swapped where r >= 8).  The order of a pass lets arithmetic
+      // cover each trip through LDS (a lone wave per SIMD waits for all it
+      // does not cover): a and b are written, the gate is computed, a and b are
+      // read back, the next pass's a and b are scaled, and h, written after
+      // the gate, is read back then.  Rowwise reciprocals come from the table
+      // that the last k-tile left in the first KB: 128 rows, 64 columns of B,
+      // 64 of B2.
       const float inv_b20 = RW ? 0.f : 1.0f / scalar_load(g.sb2);
       const float *rtab = reinterpret_cast<const float *>(epi);
+      uint8_t *sa_ = epi + 2048, *sb_ = epi + 4096, *sh_ = epi + 6144;
       const int scol = n0 + wn * (WN / 2) + (lane_e & 7) * 8;
       const bool col_ok = scol < N;
-      rsGA = __builtin_amdgcn_make_buffer_rsrc(g.a, (short)0, g.a ? M * N * 2 : 0, 0x00020000);
-      rsGB = __builtin_amdgcn_make_buffer_rsrc(g.b, (short)0, g.a ? M * N * 2 : 0, 0x00020000);
-      const int slice_r = (n0 / TN) * 2 + wn;     // this wave's partial maxima
+      const __amdgpu_buffer_rsrc_t rsGA =
+          __builtin_amdgcn_make_buffer_rsrc(g.a, (short)0, M * N * 2, 0x00020000);
+      const __amdgpu_buffer_rsrc_t rsGB =
+          __builtin_amdgcn_make_buffer_rsrc(g.b, (short)0, M * N * 2, 0x00020000);
+      // a lane's place in a staged matrix: block j's 8 bytes, then chunk u
+      const int wr = ml16 * 128 + (((nq & 7) * 2) ^ ((ml16 >> 3) << 3));
+      const int rd = (lane_e >> 3) * 128 + (((lane_e & 7) ^ (lane_e >> 3)) * 16);
+      uint2 pa[4], pb[4];
+      v4u vh[2];
+      uint32_t tmax = RW ? 0u : FP8P_TMAX()->x;
       uint32_t cm[4] = {0, 0, 0, 0};
+      auto scale = [&](int i) {
+        const float ia = RW ? rtab[i * FR + ml16] : inv_a0;
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        uint2 pa[2][4], pb[2][4];
+        for (int j = 0; j < 4; ++j) {
+          const v4f ib = RW ? *reinterpret_cast<const v4f *>(rtab + WM + j * FR + nq) : inv_br[0];
+          const v4f ib2 = RW ? *reinterpret_cast<const v4f *>(rtab + WM + 64 + j * FR + nq)
+                             : (v4f){inv_b20, inv_b20, inv_b20, inv_b20};
+          const v4f x = acc[j][i], y = acc[j + 4][i];
+          pa[j] = make_uint2(bf16x2_bits((x[0] * ia) * ib[0], (x[1] * ia) * ib[1]),
+                             bf16x2_bits((x[2] * ia) * ib[2], (x[3] * ia) * ib[3]));
+          pb[j] = make_uint2(bf16x2_bits((y[0] * ia) * ib2[0], (y[1] * ia) * ib2[1]),
+                             bf16x2_bits((y[2] * ia) * ib2[2], (y[3] * ia) * ib2[3]));
+        }
+      };
+      auto put = [&](uint8_t *st_, const uint2 (&w)[4]) {
 #pragma unroll
-        for (int ii = 0; ii < 2; ++ii) {
-          const int i = 2 * p + ii;
-          const float ia = RW ? rtab[i * FR + ml16] : inv_a0;
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint2 *>(st_ + wr + ((2 * j + (nq >> 3)) ^ (ml16 & 7)) * 16) = w[j];
+      };
+      auto get = [&](const uint8_t *st_, v4u (&v)[2]) {
+        v[0] = *reinterpret_cast<const v4u *>(st_ + rd);
+        const v4u w = *reinterpret_cast<const v4u *>(st_ + rd + 8 * 128);
+        v[1] = (v4u){w.z, w.w, w.x, w.y};
+      };
+      // row u * 8 + lane / 8 of pass i: the lane's offset in row 0, and what the
+      // row adds to it (in the instruction's scalar offset)
+      const int row0 = m0 + wm * WM + (lane_e >> 3);
+      const uint32_t off0 = (uint32_t)((row0 * N + scol) * 2);
+      const int rows_left = col_ok ? M - row0 : 0;
+      auto offset = [&](int i, int u) { return i * FR + u * 8 < rows_left ? off0 : OOB_C; };
+      auto row_off = [&](int i, int u) { return (i * FR + u * 8) * N * 2; };
+      // the row maxima of the wave's columns (nothing is stored where no maxima
+      // are wanted)
+      const __amdgpu_buffer_rsrc_t rsRow = __builtin_amdgcn_make_buffer_rsrc(
+          RW ? g.rowpart[0] + (size_t)((n0 / TN) * 2 + wn) * M : nullptr, (short)0,
+          RW && g.maxima ? M * 2 : 0, 0x00020000);
+      // h of pass i: stored, its maxima taken
+      auto finish = [&](int i) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const v4f ib = RW ? *reinterpret_cast<const v4f *>(rtab + WM + j * FR + nq) : inv_br[0];
-            const v4f ib2 = RW ? *reinterpret_cast<const v4f *>(rtab + WM + 64 + j * FR + nq)
-                               : (v4f){inv_b20, inv_b20, inv_b20, inv_b20};
-            const v4f x = acc[j][i], y = acc[j + 4][i];
-            pa[ii][j] = make_uint2(bf16x2_bits((x[0] * ia) * ib[0], (x[1] * ia) * ib[1]),
-                                   bf16x2_bits((x[2] * ia) * ib[2], (x[3] * ia) * ib[3]));
-            pb[ii][j] = make_uint2(bf16x2_bits((y[0] * ia) * ib2[0], (y[1] * ia) * ib2[1]),
-                                   bf16x2_bits((y[2] * ia) * ib2[2], (y[3] * ia) * ib2[3]));
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t off = offset(i, u);
+          __builtin_amdgcn_raw_buffer_store_b128(vh[u], rsC, off, row_off(i, u), GATE_STORE_AUX);
+          const uint32_t keep = off != OOB_C ? 0x7FFF7FFFu : 0u;
+          uint32_t rm = 0;
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            const uint32_t x = vh[u][d] & keep;
+            rm = pk_max(rm, x);
+            if (RW) cm[d] = pk_max(cm[d], x);
+          }
+          if (!RW) tmax = pk_max(tmax, rm);
+          if (RW) {
+            rm = lanes_max<8>(hmax16(rm));
+            __builtin_amdgcn_raw_buffer_store_b16(
+                (unsigned short)rm, rsRow,
+                (lane_e & 7) == 0 && i * FR + u * 8 < M - row0 ? (uint32_t)row0 * 2 : OOB_C,
+                (i * FR + u * 8) * 2, 0);
           }
         }
-        const int srow = m0 + wm * WM + p * 32 + (lane_e >> 3);
-        uint32_t off[4];
+      };
+      scale(0);
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          off[u] = col_ok && srow + u * 8 < M ? (uint32_t)(((srow + u * 8) * N + scol) * 2) : OOB_C;
-        // one staged matrix: 8 writes, then 4 whole 16-byte chunks per lane
-        auto staged = [&](const uint2 (&w)[2][4], v4u (&v)[4]) {
-#pragma unroll
-          for (int ii = 0; ii < 2; ++ii)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int ch = (2 * j + (nq >> 3)) ^ (ml16 & 7);
-              *reinterpret_cast<uint2 *>(stg + (ii * FR + ml16) * 128 + ch * 16 +
-                                         (((nq & 7) * 2) ^ ((ml16 >> 3) << 3))) = w[ii][j];
-            }
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int r = u * 8 + (lane_e >> 3);
-            v[u] = *reinterpret_cast<const v4u *>(stg + r * 128 + (((lane_e & 7) ^ (r & 7)) * 16));
-            if (u & 1) v[u] = (v4u){v[u].z, v[u].w, v[u].x, v[u].y};
-          }
-        };
-        v4u v[4];
-        if (g.a) {
-          staged(pa, v);
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            __builtin_amdgcn_raw_buffer_store_b128(v[u], rsGA, off[u], 0, C_STORE_AUX);
-          staged(pb, v);
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            __builtin_amdgcn_raw_buffer_store_b128(v[u], rsGB, off[u], 0, C_STORE_AUX);
+      for (int i = 0; i < NF; ++i) {
+        if (EPI == EPI_GATE_AB) {
+          put(sa_, pa);
+          put(sb_, pb);
         }
+        uint2 ph[4];
 #pragma unroll
-        for (int ii = 0; ii < 2; ++ii)
+        for (int j = 0; j < 4; ++j)
+          ph[j] = make_uint2(gate_fwd2(pa[j].x, pb[j].x), gate_fwd2(pa[j].y, pb[j].y));
+        if (i > 0) finish(i - 1);
+        put(sh_, ph);
+        v4u va[2], vb[2];
+        if (EPI == EPI_GATE_AB) {
+          get(sa_, va);
+          get(sb_, vb);
+        }
+        if (i + 1 < NF) scale(i + 1);
+        if (EPI == EPI_GATE_AB) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            pa[ii][j] = make_uint2(gate_fwd2(pa[ii][j].x, pb[ii][j].x),
-                                   gate_fwd2(pa[ii][j].y, pb[ii][j].y));
-        staged(pa, v);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          __builtin_amdgcn_raw_buffer_store_b128(v[u], rsC, off[u], 0, GATE_STORE_AUX);
-        if (g.maxima) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const uint32_t keep = off[u] != OOB_C ? 0x7FFF7FFFu : 0u;
-            uint32_t rm = 0;
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-              const uint32_t x = v[u][d] & keep;
-              rm = pk_max(rm, x);
-              if (RW) cm[d] = pk_max(cm[d], x);
-            }
-            if (RW) {
-              rm = lanes_max<8>(hmax16(rm));
-              if ((lane_e & 7) == 0 && srow + u * 8 < M)
-                g.rowpart[0][(size_t)slice_r * M + srow + u * 8] = (uint16_t)rm;
-            } else {
-              tmax0 = pk_max(tmax0, rm);
-            }
+          for (int u = 0; u < 2; ++u) {
+            __builtin_amdgcn_raw_buffer_store_b128(va[u], rsGA, offset(i, u), row_off(i, u),
+                                                   C_STORE_AUX);
+            __builtin_amdgcn_raw_buffer_store_b128(vb[u], rsGB, offset(i, u), row_off(i, u),
+                                                   C_STORE_AUX);
           }
         }
+        get(sh_, vh);
       }
+      finish(NF - 1);
+      if (!RW) FP8P_TMAX()->x = tmax;
       if (RW && g.maxima)
         store_colmax<8>(cm, lane_e, col_ok,
                         g.colpart[0] + (size_t)((m0 / BM) * 2 + wm) * N + scol);
+    } else if constexpr (EPI == EPI_DGATE) {
+      // 16 rows x 128 columns (256 B) per pass: dh staged in 4 KB (row r's
+      // 16-byte chunk c at c ^ r, its 8-byte halves swapped where r >= 8), a and
+      // b of the next pass on their way while this one is computed.
+      const __amdgpu_buffer_rsrc_t rsGA =
+          __builtin_amdgcn_make_buffer_rsrc(g.a, (short)0, M * N * 2, 0x00020000);
+      const __amdgpu_buffer_rsrc_t rsGB =
+          __builtin_amdgcn_make_buffer_rsrc(g.b, (short)0, M * N * 2, 0x00020000);
+      const __amdgpu_buffer_rsrc_t rsC2 =
+          __builtin_amdgcn_make_buffer_rsrc(g.C2, (short)0, M * N * 2, 0x00020000);
+      const int scol = n0 + wn * WN + (lane_e & 15) * 8;
+      const bool col_ok = scol < N;
+      const size_t slice = RW ? (size_t)((n0 / BN) * 2 + wn) * M : 0;
+      const __amdgpu_buffer_rsrc_t rsRow0 = __builtin_amdgcn_make_buffer_rsrc(
+          RW ? g.rowpart[0] + slice : nullptr, (short)0, RW ? M * 2 : 0, 0x00020000);
+      const __amdgpu_buffer_rsrc_t rsRow1 = __builtin_amdgcn_make_buffer_rsrc(
+          RW ? g.rowpart[1] + slice : nullptr, (short)0, RW ? M * 2 : 0, 0x00020000);
+      uint32_t cm[2][4] = {};
+      uint2 tmax = RW ? make_uint2(0u, 0u) : *FP8P_TMAX();
+      v4u ga[2][4], gb[2][4], v[4];
+      // row u * 4 + lane / 16 of pass i: the lane's offset in row 0, and what the
+      // row adds to it (in the instruction's scalar offset)
+      const int row0 = m0 + wm * WM + (lane_e >> 4);
+      const uint32_t off0 = (uint32_t)((row0 * N + scol) * 2);
+      const int rows_left = col_ok ? M - row0 : 0;
+      auto offset = [&](int i, int u) { return i * FR + u * 4 < rows_left ? off0 : OOB_C; };
+      auto row_off = [&](int i, int u) { return (i * FR + u * 4) * N * 2; };
+      auto load_ab = [&](int i) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          ga[i & 1][u] = __builtin_amdgcn_raw_buffer_load_b128(rsGA, offset(i, u), row_off(i, u), 0);
+          gb[i & 1][u] = __builtin_amdgcn_raw_buffer_load_b128(rsGB, offset(i, u), row_off(i, u), 0);
+        }
+      };
+      auto put = [&](int i) {
+        const float ia = RW ? tab[wm * WM + i * FR + ml16] : inv_ar[i];
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+          const v4f ib = RW ? *reinterpret_cast<const v4f *>(tab + BM + wn * WN + j * FR + nq)
+                            : inv_br[j];
+          const int ch = (2 * j + (nq >> 3)) ^ ml16;
+          *reinterpret_cast<uint2 *>(stg + ml16 * 256 + ch * 16 +
+                                     (((nq & 7) * 2) ^ ((ml16 >> 3) << 3))) =
+              make_uint2(bf16x2_bits((acc[j][i][0] * ia) * ib[0], (acc[j][i][1] * ia) * ib[1]),
+                         bf16x2_bits((acc[j][i][2] * ia) * ib[2], (acc[j][i][3] * ia) * ib[3]));
+        }
+      };
+      auto get = [&]() {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = u * 4 + (lane_e >> 4);
+          v[u] = *reinterpret_cast<const v4u *>(stg + r * 256 + (((lane_e & 15) ^ r) * 16));
+          if (u & 2) v[u] = (v4u){v[u].z, v[u].w, v[u].x, v[u].y};
+        }
+      };
+      load_ab(0);
+      put(0);
+      get();
+#pragma unroll
+      for (int i = 0; i < NF; ++i) {
+        if (i + 1 < NF) {
+          load_ab(i + 1);
+          put(i + 1);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t off = offset(i, u);
+          const uint32_t keep = off != OOB_C ? 0x7FFF7FFFu : 0u;
+          v4u x, y;
+          uint32_t rm0 = 0, rm1 = 0;
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            uint32_t da, db;
+            gate_bwd2(v[u][d], ga[i & 1][u][d], gb[i & 1][u][d], da, db);
+            x[d] = da;
+            y[d] = db;
+            rm0 = pk_max(rm0, da & keep);
+            rm1 = pk_max(rm1, db & keep);
+            if (RW) {
+              cm[0][d] = pk_max(cm[0][d], da & keep);
+              cm[1][d] = pk_max(cm[1][d], db & keep);
+            }
+          }
+          __builtin_amdgcn_raw_buffer_store_b128(x, rsC, off, row_off(i, u), GATE_STORE_AUX);
+          __builtin_amdgcn_raw_buffer_store_b128(y, rsC2, off, row_off(i, u), GATE_STORE_AUX);
+          if (RW) {
+            rm0 = lanes_max<16>(hmax16(rm0));
+            rm1 = lanes_max<16>(hmax16(rm1));
+            const uint32_t at = (lane_e & 15) == 0 && i * FR + u * 4 < M - row0
+                                    ? (uint32_t)row0 * 2 : OOB_C;
+            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)rm0, rsRow0, at,
+                                                  (i * FR + u * 4) * 2, 0);
+            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)rm1, rsRow1, at,
+                                                  (i * FR + u * 4) * 2, 0);
+          } else {
+            tmax.x = pk_max(tmax.x, rm0);
+            tmax.y = pk_max(tmax.y, rm1);
+          }
+        }
+        if (i + 1 < NF) get();
+      }
+      if (!RW) *FP8P_TMAX() = tmax;
+      if (RW) {
+        const size_t at = (size_t)((m0 / BM) * 2 + wm) * N + scol;
+        store_colmax<16>(cm[0], lane_e, col_ok, g.colpart[0] + at);
+        store_colmax<16>(cm[1], lane_e, col_ok, g.colpart[1] + at);
+      }
     } else if (RW && F32) {
       // rowwise fp32: the tile's columns in two halves of 64, one 16-row
       // block per pass: 16 rows x 256 B (row r's 16-byte chunk c at
@@ -1039,7 +1167,6 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
       for (int jh = 0; jh < 2; ++jh) {
         const int scol = n0 + wn * WN + jh * 64 + (lane_e & 7) * 8;
         const bool col_ok = scol < N;
-        uint32_t cm[2][4] = {};                   // EPI_DGATE: column maxima of da, db
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           const float ia0 = tab[wm * WM + 2 * p * FR + ml16];
@@ -1077,40 +1204,6 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
             const bool ok = col_ok && srow + u * 8 < M;
             off[u] = ok ? (uint32_t)(((srow + u * 8) * N + scol) * 2) : OOB_C;
           }
-          if constexpr (EPI == EPI_DGATE) {
-            v4u ga[4], gb[4], w[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              ga[u] = __builtin_amdgcn_raw_buffer_load_b128(rsGA, off[u], 0, 0);
-              gb[u] = __builtin_amdgcn_raw_buffer_load_b128(rsGB, off[u], 0, 0);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              uint32_t rm0 = 0, rm1 = 0;
-              const uint32_t keep = off[u] != OOB_C ? 0x7FFF7FFFu : 0u;
-#pragma unroll
-              for (int d = 0; d < 4; ++d) {
-                uint32_t da, db;
-                gate_bwd2(v[u][d], ga[u][d], gb[u][d], da, db);
-                v[u][d] = da;
-                w[u][d] = db;
-                rm0 = pk_max(rm0, da & keep);
-                rm1 = pk_max(rm1, db & keep);
-                cm[0][d] = pk_max(cm[0][d], da & keep);
-                cm[1][d] = pk_max(cm[1][d], db & keep);
-              }
-              __builtin_amdgcn_raw_buffer_store_b128(w[u], rsC2, off[u], 0, GATE_STORE_AUX);
-              if (g.maxima) {
-                rm0 = lanes_max<8>(hmax16(rm0));
-                rm1 = lanes_max<8>(hmax16(rm1));
-                const size_t at = (size_t)((n0 / BN) * 4 + wn * 2 + jh) * M + srow + u * 8;
-                if ((lane_e & 7) == 0 && srow + u * 8 < M) {
-                  g.rowpart[0][at] = (uint16_t)rm0;
-                  g.rowpart[1][at] = (uint16_t)rm1;
-                }
-              }
-            }
-          }
           if (ACC) {
             v4u cin[4];
 #pragma unroll
@@ -1128,15 +1221,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
           }
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            __builtin_amdgcn_raw_buffer_store_b128(v[u], rsC, off[u], 0,
-                                                   EPI == EPI_NONE ? C_STORE_AUX : GATE_STORE_AUX);
-        }
-        if constexpr (EPI == EPI_DGATE) {
-          if (g.maxima) {
-            const size_t at = (size_t)((m0 / BM) * 2 + wm) * N + scol;
-            store_colmax<8>(cm[0], lane_e, col_ok, g.colpart[0] + at);
-            store_colmax<8>(cm[1], lane_e, col_ok, g.colpart[1] + at);
-          }
+            __builtin_amdgcn_raw_buffer_store_b128(v[u], rsC, off[u], 0, C_STORE_AUX);
         }
       }
     } else {
@@ -1144,17 +1229,6 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
       const bool col_ok = scol < N;
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        // EPI_DGATE: a and b of the pass, on their way while dh is staged
-        v4u ga[8], gb[8];
-        if constexpr (EPI == EPI_DGATE) {
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int row = m0 + wm * WM + p * 32 + u * 4 + (lane_e >> 4);
-            const uint32_t o = col_ok && row < M ? (uint32_t)((row * N + scol) * 2) : OOB_C;
-            ga[u] = __builtin_amdgcn_raw_buffer_load_b128(rsGA, o, 0, 0);
-            gb[u] = __builtin_amdgcn_raw_buffer_load_b128(rsGB, o, 0, 0);
-          }
-        }
 #pragma unroll
         for (int ii = 0; ii < 2; ++ii) {
           const int i = 2 * p + ii;
@@ -1189,23 +1263,6 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
           const bool ok = col_ok && srow + u * 4 < M;
           off[u] = ok ? (uint32_t)(((srow + u * 4) * N + scol) * 2) : OOB_C;
         }
-        if constexpr (EPI == EPI_DGATE) {
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            v4u w;
-            const uint32_t keep = off[u] != OOB_C ? 0x7FFF7FFFu : 0u;
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-              uint32_t da, db;
-              gate_bwd2(v[u][d], ga[u][d], gb[u][d], da, db);
-              v[u][d] = da;
-              w[d] = db;
-              tmax0 = pk_max(tmax0, da & keep);
-              tmax1 = pk_max(tmax1, db & keep);
-            }
-            __builtin_amdgcn_raw_buffer_store_b128(w, rsC2, off[u], 0, GATE_STORE_AUX);
-          }
-        }
         if (ACC) {
           v4u cin[8];
 #pragma unroll
@@ -1222,9 +1279,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
           }
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-          __builtin_amdgcn_raw_buffer_store_b128(v[u], rsC, off[u], 0,
-                                                 EPI == EPI_NONE ? C_STORE_AUX : GATE_STORE_AUX);
+        for (int u = 0; u < 8; ++u) __builtin_amdgcn_raw_buffer_store_b128(v[u], rsC, off[u], 0, C_STORE_AUX);
       }
     }
 #ifdef FP8L_PHASE_TIMING
@@ -1246,13 +1301,16 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
   }
   if constexpr (EPI != EPI_NONE && !RW) {
     if (g.maxima) {
-      const uint32_t m0_ = wave_max(hmax16(tmax0)), m1_ = wave_max(hmax16(tmax1));
+      const uint2 tmax = *FP8P_TMAX();
+      const uint32_t m0_ = wave_max(hmax16(tmax.x)), m1_ = wave_max(hmax16(tmax.y));
       if (hw_lane() == 0) {
+        // (a wave without a tile leaves 0)
         g.part[0][blockIdx.x * 4 + wave] = m0_;
         if (EPI == EPI_DGATE) g.part[1][blockIdx.x * 4 + wave] = m1_;
       }
     }
   }
+#undef FP8P_TMAX
 #undef FP8P_H2D
 #undef FP8P_H2
 #undef FP8P_H1
