@@ -14,12 +14,14 @@
 // against the separate passes: a and b are not read back to form h, dh is
 // neither written nor read, and the amax of h, da, db costs no pass.
 //
-// Few tokens (M <= SKINNY_M): the time is that of reading W1 and W3 once, and
-// a tile of 256 rows would leave most compute units without a tile and most
-// of each tile's work on padding.  k_gated_skinny: a workgroup owns 16 to 64
-// columns of h, its 8 waves split the contraction and join through LDS.
-// Weights go straight from memory to the MFMA operands (no byte of them is
-// used twice); x comes from L2.
+// In between, where those tiles are too few for the compute units:
+// k_gate_tile, one tile of 64 rows x 64 columns of h (128 of da and db) per
+// workgroup.
+//
+// Few tokens (M <= SKINNY_M = 16, one MFMA block): k_gated_skinny.  The time is
+// that of reading W1 and W3 once.  A workgroup owns 16 columns of h, its 8 waves
+// split the contraction and join through LDS; weights go straight from memory
+// to the MFMA operands (no byte of them is used twice), x comes from L2.
 //
 // Part of gemm.hip (included at its end).
 #pragma once
@@ -31,8 +33,9 @@ namespace {
 
 // ---------------------------------------------------------- few tokens --
 
-constexpr int SKINNY_M = 64;
+constexpr int SKINNY_M = 16;
 constexpr int SK_WAVES = 8;
+constexpr int SK_UNROLL = 4;   // k-tiles of a wave that load together
 
 struct SkinnyArgs {
   const uint8_t *x, *w1, *w3;
@@ -55,186 +58,387 @@ __device__ __forceinline__ v8i frag(v4u lo, v4u hi) {
                (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
 
-// MB blocks of 16 tokens, CB blocks of 16 columns of h.  Lane l of a wave
-// holds row l % 16 of an operand and the chunks of 16 bytes at l / 16 and l / 16
-// + 4 of the 128-byte k-tile (the same for both operands), so that one load
-// instruction reads 64 contiguous bytes of each of 16 weight rows.  Rows past
-// M or H read the last row (not stored).  UN k-tiles of a wave load together.
-// The waves join per block of tokens, so the LDS does not grow with M.
-template <int MB, int CB, int UN, bool KFULL>
+// Lane l of a wave holds row l % 16 of an operand and the chunks of 16 bytes at
+// l / 16 and l / 16 + 4 of the 128-byte k-tile (the same for both operands), so
+// that one load instruction reads 64 contiguous bytes of each of 16 weight
+// rows.  Rows past M read row M - 1 (not stored).
+//
+// One token, 14336 columns, K = 4096: 23.8 us, 4.9 TB/s of weights, the rate of a
+// large copy; with 4 waves and the same loads in flight 26, with 2 k-tiles
+// together 28, with non-temporal loads 27.  More tokens go to the small tiles:
+// a form of this kernel with 4 token blocks took 33 us at 64 tokens, where every
+// workgroup reads all of x.
+template <bool KFULL>
 __global__ __launch_bounds__(64 * SK_WAVES) void k_gated_skinny(SkinnyArgs p) {
-  static_assert(CB <= SK_WAVES, "one wave finishes each block of columns");
-  __shared__ v4f red[SK_WAVES][2 * CB][64];
+  __shared__ v4f red[SK_WAVES][2][64];
   const int lane = threadIdx.x & 63;
   const int wave = threadIdx.x >> 6;
-  const int n0 = blockIdx.x * (16 * CB);
+  const int n0 = blockIdx.x * 16;
   const int K = p.K;
   const int nk = (K + BK - 1) / BK;
   const int kl = (lane >> 4) * 16;
-  const uint8_t *r1[CB], *r3[CB], *rx[MB];
+  const uint8_t *r1 = p.w1 + (size_t)(n0 + (lane & 15)) * K;
+  const uint8_t *r3 = p.w3 + (size_t)(n0 + (lane & 15)) * K;
+  const uint8_t *rx = p.x + (size_t)min(lane & 15, p.M - 1) * K;
+  v4f acc1 = {0.f, 0.f, 0.f, 0.f}, acc3 = acc1;
+  for (int t0 = wave; t0 < nk; t0 += SK_WAVES * SK_UNROLL) {
+    v4u f1[SK_UNROLL][2], f3[SK_UNROLL][2], fx[SK_UNROLL][2];
 #pragma unroll
-  for (int c = 0; c < CB; ++c) {
-    const size_t row = (size_t)min(n0 + c * 16 + (lane & 15), p.H - 1) * K;
-    r1[c] = p.w1 + row;
-    r3[c] = p.w3 + row;
-  }
-#pragma unroll
-  for (int i = 0; i < MB; ++i)
-    rx[i] = p.x + (size_t)min(i * 16 + (lane & 15), p.M - 1) * K;
-  v4f acc[2][CB][MB];
-#pragma unroll
-  for (int c = 0; c < CB; ++c)
-#pragma unroll
-    for (int i = 0; i < MB; ++i) acc[0][c][i] = acc[1][c][i] = (v4f){0.f, 0.f, 0.f, 0.f};
-  for (int t0 = wave; t0 < nk; t0 += SK_WAVES * UN) {
-    v4u f1[UN][CB][2], f3[UN][CB][2], fx[UN][MB][2];
-#pragma unroll
-    for (int u = 0; u < UN; ++u) {
+    for (int u = 0; u < SK_UNROLL; ++u) {
       const int t = t0 + u * SK_WAVES;            // past the end: loaded again, not used
       const int k = (t < nk ? t : t0) * BK + kl;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int c = 0; c < CB; ++c) {
-          f1[u][c][e] = row_chunk<KFULL>(r1[c], k + e * 64, K);
-          f3[u][c][e] = row_chunk<KFULL>(r3[c], k + e * 64, K);
-        }
-#pragma unroll
-        for (int i = 0; i < MB; ++i) fx[u][i][e] = row_chunk<KFULL>(rx[i], k + e * 64, K);
+        f1[u][e] = row_chunk<KFULL>(r1, k + e * 64, K);
+        f3[u][e] = row_chunk<KFULL>(r3, k + e * 64, K);
+        fx[u][e] = row_chunk<KFULL>(rx, k + e * 64, K);
       }
     }
 #pragma unroll
-    for (int u = 0; u < UN; ++u) {
+    for (int u = 0; u < SK_UNROLL; ++u) {
       if (t0 + u * SK_WAVES < nk) {               // wave-uniform
-#pragma unroll
-        for (int c = 0; c < CB; ++c) {
-          const v8i b1 = frag(f1[u][c][0], f1[u][c][1]), b3 = frag(f3[u][c][0], f3[u][c][1]);
-#pragma unroll
-          for (int i = 0; i < MB; ++i) {
-            const v8i ax = frag(fx[u][i][0], fx[u][i][1]);
-            acc[0][c][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                b1, ax, acc[0][c][i], 0, 0, 0, 0, 0, 0);
-            acc[1][c][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                b3, ax, acc[1][c][i], 0, 0, 0, 0, 0, 0);
-          }
-        }
+        const v8i ax = frag(fx[u][0], fx[u][1]);
+        acc1 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(f1[u][0], f1[u][1]), ax, acc1,
+                                                                0, 0, 0, 0, 0, 0);
+        acc3 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(f3[u][0], f3[u][1]), ax, acc3,
+                                                                0, 0, 0, 0, 0, 0);
       }
     }
   }
+  red[wave][0][lane] = acc1;
+  red[wave][1][lane] = acc3;
+  __syncthreads();
+  // lane l of the first wave: token l % 16, columns n0 + 4 (l / 16) ...
+  const int m = lane & 15;
+  const int n = n0 + (lane >> 4) * 4;
+  if (wave > 0 || m >= p.M) return;
+  v4f a = red[0][0][lane], b = red[0][1][lane];
 #pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    if (i) __syncthreads();                       // the round before has been read
-#pragma unroll
-    for (int c = 0; c < CB; ++c) {
-      red[wave][2 * c][lane] = acc[0][c][i];
-      red[wave][2 * c + 1][lane] = acc[1][c][i];
-    }
-    __syncthreads();
-    // wave c, lane l: token i 16 + l % 16, columns n0 + 16 c + 4 (l / 16) ...
-    const int c = wave;
-    const int m = i * 16 + (lane & 15);
-    const int n = n0 + c * 16 + (lane >> 4) * 4;
-    if (c < CB && m < p.M && n < p.H) {
-      v4f a = red[0][2 * c][lane], b = red[0][2 * c + 1][lane];
-#pragma unroll
-      for (int w = 1; w < SK_WAVES; ++w) {
-        a += red[w][2 * c][lane];
-        b += red[w][2 * c + 1][lane];
-      }
-      const float ia = 1.0f / p.sx[p.rowwise ? m : 0];
-      float i1[4], i3[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        i1[j] = 1.0f / p.s1[p.rowwise ? n + j : 0];
-        i3[j] = 1.0f / p.s3[p.rowwise ? n + j : 0];
-      }
-      const uint2 pa = make_uint2(bf16x2_bits((a[0] * ia) * i1[0], (a[1] * ia) * i1[1]),
-                                  bf16x2_bits((a[2] * ia) * i1[2], (a[3] * ia) * i1[3]));
-      const uint2 pb = make_uint2(bf16x2_bits((b[0] * ia) * i3[0], (b[1] * ia) * i3[1]),
-                                  bf16x2_bits((b[2] * ia) * i3[2], (b[3] * ia) * i3[3]));
-      const size_t at = (size_t)m * p.H + n;
-      if (p.a) {
-        *reinterpret_cast<uint2 *>(p.a + at) = pa;
-        *reinterpret_cast<uint2 *>(p.b + at) = pb;
-      }
-      *reinterpret_cast<uint2 *>(p.h + at) =
-          make_uint2(gate_fwd2(pa.x, pb.x), gate_fwd2(pa.y, pb.y));
-    }
+  for (int w = 1; w < SK_WAVES; ++w) {
+    a += red[w][0][lane];
+    b += red[w][1][lane];
   }
+  const float ia = 1.0f / p.sx[p.rowwise ? m : 0];
+  float i1[4], i3[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    i1[j] = 1.0f / p.s1[p.rowwise ? n + j : 0];
+    i3[j] = 1.0f / p.s3[p.rowwise ? n + j : 0];
+  }
+  const uint2 pa = make_uint2(bf16x2_bits((a[0] * ia) * i1[0], (a[1] * ia) * i1[1]),
+                              bf16x2_bits((a[2] * ia) * i1[2], (a[3] * ia) * i1[3]));
+  const uint2 pb = make_uint2(bf16x2_bits((b[0] * ia) * i3[0], (b[1] * ia) * i3[1]),
+                              bf16x2_bits((b[2] * ia) * i3[2], (b[3] * ia) * i3[3]));
+  const size_t at = (size_t)m * p.H + n;
+  if (p.a) {
+    *reinterpret_cast<uint2 *>(p.a + at) = pa;
+    *reinterpret_cast<uint2 *>(p.b + at) = pb;
+  }
+  *reinterpret_cast<uint2 *>(p.h + at) = make_uint2(gate_fwd2(pa.x, pb.x), gate_fwd2(pa.y, pb.y));
 }
 
-template <int MB, int CB, int UN>
-hipError_t skinny_shape(const SkinnyArgs &p, hipStream_t stream) {
-  const dim3 grid((unsigned)((p.H + 16 * CB - 1) / (16 * CB))), block(64 * SK_WAVES);
+hipError_t skinny_launch(const SkinnyArgs &p, hipStream_t stream) {
+  const dim3 grid((unsigned)(p.H / 16)), block(64 * SK_WAVES);
   if (p.K % BK == 0)
-    hipLaunchKernelGGL((k_gated_skinny<MB, CB, UN, true>), grid, block, 0, stream, p);
+    hipLaunchKernelGGL((k_gated_skinny<true>), grid, block, 0, stream, p);
   else
-    hipLaunchKernelGGL((k_gated_skinny<MB, CB, UN, false>), grid, block, 0, stream, p);
+    hipLaunchKernelGGL((k_gated_skinny<false>), grid, block, 0, stream, p);
   return hipGetLastError();
 }
 
-// Columns per workgroup: x is read by every workgroup, so with more than 16
-// tokens a workgroup takes as many columns as still leave nearly every compute
-// unit one (14336 columns, K = 4096: 64 tokens 52 us with 16 columns, 40 with
-// 32, 33 with 64; 32 tokens 37, 30, 28; one token 24, 25).
-hipError_t skinny_launch(const SkinnyArgs &p, hipStream_t stream) {
-  if (p.M <= 16) return skinny_shape<1, 1, 4>(p, stream);
-  const bool c4 = p.H >= 64 * 192, c2 = p.H >= 32 * 192;
-  if (p.M <= 32)
-    return c4 ? skinny_shape<2, 4, 1>(p, stream)
-              : c2 ? skinny_shape<2, 2, 2>(p, stream) : skinny_shape<2, 1, 2>(p, stream);
-  return c4 ? skinny_shape<4, 4, 1>(p, stream)
-            : c2 ? skinny_shape<4, 2, 2>(p, stream) : skinny_shape<4, 1, 2>(p, stream);
+// ---------------------------------------------------------- small tiles --
+//
+// Tile: 64 rows x 128 rows of the B slab (EPI_GATE: 64 of B and the same 64 of
+// B2, 32 + 32 per wave column).  4 waves in a 2 x 2 grid own 32 x 64 each, 2 x 4
+// blocks of the same MFMA.  Three 24 KB stages of one 128-byte k-tile, filled
+// by DMA two k-tiles ahead, in the layout of the large kernel (16-byte chunk c
+// of row r at c ^ h(r)); one barrier per k-tile.  Two workgroups live on a
+// compute unit and cover each other's epilogue, which therefore works in the
+// accumulators' own layout: 8-byte accesses of 4 columns, no staging.
+//
+// At 1040 x 1808 (K = 784, rowwise, a and b stored) TILE_FWD_US, at 528 x 4112
+// (K = 400) backward TILE_BWD_US: with 75 and 51 tiles of the large kernel the
+// same GEMMs take 26 and 32 us.
+constexpr int TM = 64;
+constexpr int TB = 128;                            // rows of the B slab
+constexpr int T_STAGE = (TM + TB) * BK;            // 24 KB
+constexpr int T_STAGES = 3;
+
+template <int EPI, int FA, bool RW>
+__global__ __launch_bounds__(256) void k_gate_tile(GateArgs g) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[T_STAGES * T_STAGE];
+  constexpr bool GATE = EPI != EPI_DGATE;
+  constexpr int TN = GATE ? TB / 2 : TB;           // output columns of the tile
+  constexpr int WC = TN / 2;                       // of a wave
+  constexpr int NJ = WC / FR;                      // output blocks of a wave along n
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int M = g.M[0], N = g.N[0], K = g.K[0];
+  const int nk = (K + BK - 1) / BK;
+  // workgroups are dealt to the XCDs round-robin; each XCD takes a contiguous
+  // share of the tiles, rows fastest, so that it reads its own rows of B
+  const int x = blockIdx.x % NUM_XCD, total = g.total;
+  int q = blockIdx.x / NUM_XCD;
+  for (int xx = 0; xx < x; ++xx) q += (total - xx + NUM_XCD - 1) / NUM_XCD;
+  const int m0 = q % g.tiles_m[0] * TM, n0 = q / g.tiles_m[0] * TN;
+
+  // DMA: wave w fills A rows w 16 + (0..15) and slab rows w 32 + (0..31) of B,
+  // 8 rows an instruction.  Rows past the matrix fail the bounds check of the
+  // vector offset and read as zero; so do chunks past K.
+  const uint8_t *B = g.B[0];
+  int nb0 = n0 + wave * 32;                        // first B row of this wave's part
+  if (GATE) {
+    B = (wave & 1) ? g.B2 : B;
+    nb0 = n0 + (wave >> 1) * 32;
+  }
+  const int ma0 = m0 + wave * 16;
+  const __amdgpu_buffer_rsrc_t rsA = __builtin_amdgcn_make_buffer_rsrc(
+      (void *)(g.A[0] + (size_t)min(ma0, M) * K), (short)0, max(M - ma0, 0) * K, 0x00020000);
+  const __amdgpu_buffer_rsrc_t rsB = __builtin_amdgcn_make_buffer_rsrc(
+      (void *)(B + (size_t)min(nb0, N) * K), (short)0, max(N - nb0, 0) * K, 0x00020000);
+  const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void *)lds;
+  const int lr = lane >> 3;
+  auto fill = [&](int t) {
+    const int k0 = t * BK;
+    const uint32_t st = base + (uint32_t)(t % T_STAGES * T_STAGE);
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+      const int r = (i < 2 ? i : i - 2) * 8 + lr;  // row of this wave's part
+      // h(r) of the slab row: parts start at multiples of 16 rows
+      const int c = (lane & 7) ^ (r & 7) ^ ((r >> 3) & 1);
+      const uint32_t off = k0 + c * 16 < K ? (uint32_t)(r * K + c * 16) : OOB;
+      if (i < 2) dma16(rsA, st + (uint32_t)((wave * 16 + i * 8) * BK), off, (uint32_t)k0);
+      else dma16(rsB, st + (uint32_t)((TM + wave * 32 + (i - 2) * 8) * BK), off, (uint32_t)k0);
+    }
+  };
+  v4f acc[4][2];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) acc[j][i] = (v4f){0.f, 0.f, 0.f, 0.f};
+  // fragment reads: lane l, row l % 16, chunks 2 (l / 16) and 2 (l / 16) + 1
+  const int l16 = lane & 15, g4 = lane >> 4;
+  const int hr = (lane & 7) ^ ((lane >> 3) & 1);
+  const int c0 = ((2 * g4) ^ hr) << 4, c1 = ((2 * g4 + 1) ^ hr) << 4;
+  const int ra = (wm * 32 + l16) * BK, rb = (TM + wn * 64 + l16) * BK;
+  // the places of the lane's outputs; EPI_DGATE reads its a and b first of all
+  const int mrow = m0 + wm * 32 + l16;
+  const int ncol = n0 + wn * WC + g4 * 4;
+  uint2 ga[GATE ? 1 : NJ][2], gb[GATE ? 1 : NJ][2];
+  if constexpr (!GATE) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const size_t at = (size_t)min(mrow + i * FR, M - 1) * N + min(ncol + j * FR, N - 4);
+        ga[j][i] = *reinterpret_cast<const uint2 *>(g.a + at);
+        gb[j][i] = *reinterpret_cast<const uint2 *>(g.b + at);
+      }
+  }
+  fill(0);
+  if (nk > 1) fill(1);
+  for (int t = 0; t < nk; ++t) {
+    // this wave's part of k-tile t has arrived (k-tile t + 1 may be on its way)
+    if (t + 1 < nk) wait_vmcnt<6>();
+    else wait_vmcnt0();
+    wait_lgkm0();
+    barrier_lds();                                 // all parts; k-tile t - 1 has been read
+    if (t + 2 < nk) fill(t + 2);
+    const uint8_t *st = lds + t % T_STAGES * T_STAGE;
+    v8i fa[2], fb[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      fa[i] = frag(*reinterpret_cast<const v4u *>(st + ra + i * FR * BK + c0),
+                   *reinterpret_cast<const v4u *>(st + ra + i * FR * BK + c1));
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      fb[j] = frag(*reinterpret_cast<const v4u *>(st + rb + j * FR * BK + c0),
+                   *reinterpret_cast<const v4u *>(st + rb + j * FR * BK + c1));
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], fa[i], acc[j][i], 0,
+                                                                     FA, 0, 0, 0, 0);
+  }
+
+  // ---- epilogue: lane l holds columns 4 (l / 16) .. + 3 of row l % 16 of its
+  // blocks
+  uint16_t *C = static_cast<uint16_t *>(g.C[0]);
+  uint32_t rm[2][2] = {};                          // [output][i]: row maxima (u16 pairs)
+  uint2 cm[2][NJ] = {};                            // [output][j]: column maxima
+  float ia[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) ia[i] = 1.0f / g.sa[0][RW ? min(mrow + i * FR, M - 1) : 0];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int n = ncol + j * FR;
+    float ib[4], ib2[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int at = RW ? min(n + e, N - 1) : 0;
+      ib[e] = 1.0f / g.sb[0][at];
+      ib2[e] = GATE ? 1.0f / g.sb2[at] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int m = mrow + i * FR;
+      const bool ok = m < M && n < N;
+      const size_t at = (size_t)m * N + n;
+      const v4f p = acc[j][i];
+      const uint2 pa = make_uint2(bf16x2_bits((p[0] * ia[i]) * ib[0], (p[1] * ia[i]) * ib[1]),
+                                  bf16x2_bits((p[2] * ia[i]) * ib[2], (p[3] * ia[i]) * ib[3]));
+      uint2 o[2];
+      if constexpr (GATE) {
+        const v4f r = acc[j + NJ][i];
+        const uint2 pb =
+            make_uint2(bf16x2_bits((r[0] * ia[i]) * ib2[0], (r[1] * ia[i]) * ib2[1]),
+                       bf16x2_bits((r[2] * ia[i]) * ib2[2], (r[3] * ia[i]) * ib2[3]));
+        if (EPI == EPI_GATE_AB && ok) {
+          *reinterpret_cast<uint2 *>(g.a + at) = pa;
+          *reinterpret_cast<uint2 *>(g.b + at) = pb;
+        }
+        o[0] = make_uint2(gate_fwd2(pa.x, pb.x), gate_fwd2(pa.y, pb.y));
+        if (ok) *reinterpret_cast<uint2 *>(C + at) = o[0];
+      } else {
+        gate_bwd2(pa.x, ga[j][i].x, gb[j][i].x, o[0].x, o[1].x);
+        gate_bwd2(pa.y, ga[j][i].y, gb[j][i].y, o[0].y, o[1].y);
+        if (ok) {
+          *reinterpret_cast<uint2 *>(C + at) = o[0];
+          *reinterpret_cast<uint2 *>(g.C2 + at) = o[1];
+        }
+      }
+      const uint32_t keep = ok ? 0x7FFF7FFFu : 0u;
+#pragma unroll
+      for (int k = 0; k < (GATE ? 1 : 2); ++k) {
+        const uint32_t v0 = o[k].x & keep, v1 = o[k].y & keep;
+        rm[k][i] = pk_max(rm[k][i], pk_max(v0, v1));
+        if (RW) cm[k][j] = make_uint2(pk_max(cm[k][j].x, v0), pk_max(cm[k][j].y, v1));
+      }
+    }
+  }
+  if (!g.maxima) return;                           // uniform
+#pragma unroll
+  for (int k = 0; k < (GATE ? 1 : 2); ++k) {
+    if (RW) {
+      const int tile_n = n0 / TN, tile_m = m0 / TM;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t v = hmax16(rm[k][i]);
+        v = max(v, (uint32_t)__shfl_xor((int)v, 16));
+        v = max(v, (uint32_t)__shfl_xor((int)v, 32));
+        if (lane < 16 && mrow + i * FR < M)
+          g.rowpart[k][(size_t)(tile_n * 2 + wn) * M + mrow + i * FR] = (uint16_t)v;
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        uint2 v = cm[k][j];
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) {
+          v.x = pk_max(v.x, (uint32_t)__shfl_xor((int)v.x, o));
+          v.y = pk_max(v.y, (uint32_t)__shfl_xor((int)v.y, o));
+        }
+        const int n = ncol + j * FR;
+        if (l16 == 0 && n < N)
+          *reinterpret_cast<uint2 *>(g.colpart[k] + (size_t)(tile_m * 2 + wm) * N + n) = v;
+      }
+    } else {
+      // one maximum per workgroup, through LDS that the main loop is done with
+      uint32_t *red = reinterpret_cast<uint32_t *>(lds) + k * 4;
+      const uint32_t v = wave_max(hmax16(pk_max(rm[k][0], rm[k][1])));
+      if (k == 0) __syncthreads();
+      if (lane == 0) red[wave] = v;
+      __syncthreads();
+      if (threadIdx.x == 0)
+        g.part[k][blockIdx.x] = max(max(red[0], red[1]), max(red[2], red[3]));
+    }
+  }
 }
 
 // ------------------------------------------------------------- launches --
 
-// The persistent kernel over one problem.  args: A, sa, B, sb, C, M, N, K and
-// the gate's own fields set; tile counts and the grid follow here.
+int64_t tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
+
+// Whether an [M, H] output takes the small tiles (a large tile is 256 rows x
+// bn columns): while the large ones leave about half the compute units
+// without any.  Measured, small against large, in us.  Forward with a, b and
+// the quantize of h: 112 large tiles 29 / 47 (80 x 14336), 48 / 49 (256 x 14336),
+// 120 tiles 26 / 28, 128 tiles 35 / 35 and 49 / 49, 224 tiles 60 / 52, 256 tiles 45 /
+// 34.  Backward: 51 tiles 23 / 33, 64 tiles 32 / 45 and 38 / 60, 85 tiles 44 / 40, 112
+// tiles 55 / 60, 128 tiles 47 / 43.
+constexpr int64_t SMALL_TILES = 128, SMALL_TILES_BWD = 80;
+bool small_tiles(int64_t M, int64_t H, int bn) {
+  return tiles(M, BM) * tiles(H, bn) <= (bn == BN ? SMALL_TILES_BWD : SMALL_TILES);
+}
+
+// One problem.  args: A, sa, B, sb, C, M, N, K and the gate's own fields set;
+// tile counts and the grid follow here.  nparts: tensorwise maxima written.
 template <int EPI, int FA>
-hipError_t launch_gate(GateArgs &g, bool rowwise, int *blocks, hipStream_t stream) {
+hipError_t launch_gate(GateArgs &g, bool rowwise, int *nparts, hipStream_t stream) {
   constexpr int TN = is_gate(EPI) ? BN / 2 : BN;
   g.count = 1;
-  g.tiles_m[0] = (g.M[0] + BM - 1) / BM;
-  g.tiles_n[0] = (g.N[0] + TN - 1) / TN;
+  if (small_tiles(g.M[0], g.N[0], TN)) {
+    g.tiles_m[0] = (int)tiles(g.M[0], TM);
+    g.tiles_n[0] = (int)tiles(g.N[0], TN / 2);
+    g.total = *nparts = g.tiles_m[0] * g.tiles_n[0];
+    if (rowwise)
+      hipLaunchKernelGGL((k_gate_tile<EPI, FA, true>), dim3((unsigned)g.total), dim3(256), 0,
+                         stream, g);
+    else
+      hipLaunchKernelGGL((k_gate_tile<EPI, FA, false>), dim3((unsigned)g.total), dim3(256), 0,
+                         stream, g);
+    return hipGetLastError();
+  }
+  g.tiles_m[0] = (int)tiles(g.M[0], BM);
+  g.tiles_n[0] = (int)tiles(g.N[0], TN);
   g.total = g.tiles_m[0] * g.tiles_n[0];
   constexpr int kComputeUnits = 256;
-  *blocks = g.total < kComputeUnits ? g.total : kComputeUnits;
+  const int blocks = g.total < kComputeUnits ? g.total : kComputeUnits;
+  *nparts = blocks * 4;                           // one per wave
   const bool kfull = g.K[0] % BK == 0;
   auto kern = rowwise ? (kfull ? k_gemm_fp8_pers<true, true, false, FA, false, EPI>
                                : k_gemm_fp8_pers<false, true, false, FA, false, EPI>)
                       : (kfull ? k_gemm_fp8_pers<true, false, false, FA, false, EPI>
                                : k_gemm_fp8_pers<false, false, false, FA, false, EPI>);
-  hipLaunchKernelGGL(kern, dim3((unsigned)*blocks), dim3(THREADS), 0, stream, g);
+  hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(THREADS), 0, stream, g);
   return hipGetLastError();
 }
 
 // Partial maxima of one output in its share of the workspace: rowwise the
-// row maxima per wave of a tile (64 columns of h, 128 of da and db), then
-// (256-byte aligned) the column maxima per 128 rows; tensorwise one u32 per wave
-// of at most 256 workgroups.
-int64_t row_slices(int64_t H, int tile) { return (H + tile - 1) / tile * 2; }
-int64_t col_slices(int64_t M) { return (M + BM - 1) / BM * 2; }
-size_t colpart_at(int64_t M, int64_t H) {
-  return ((size_t)(row_slices(H, BN / 2) * M) * sizeof(uint16_t) + 255) & ~(size_t)255;
+// row maxima per wave column of the tiles, then (256-byte aligned) the column
+// maxima per wave row; tensorwise one u32 per wave of at most 256 workgroups, or
+// per workgroup of at most 8 SMALL_TILES.  A large tile holds 8 small ones.
+// (Columns per large tile: bn; a small tile has half as many.)
+int64_t row_slices(int64_t M, int64_t H, int bn) {
+  return 2 * (small_tiles(M, H, bn) ? tiles(H, bn / 2) : tiles(H, bn));
 }
-size_t gate_share_bytes(int64_t M, int64_t H, bool rowwise) {
-  const size_t b = rowwise ? colpart_at(M, H) + (size_t)(col_slices(M) * H) * sizeof(uint16_t)
-                           : (size_t)256 * 4 * sizeof(uint32_t);
+int64_t col_slices(int64_t M, int64_t H, int bn) {
+  return 2 * (small_tiles(M, H, bn) ? tiles(M, TM) : tiles(M, BM));
+}
+size_t colpart_at(int64_t M, int64_t H, int bn) {
+  return ((size_t)(row_slices(M, H, bn) * M) * sizeof(uint16_t) + 255) & ~(size_t)255;
+}
+constexpr size_t TW_PARTS = 8 * SMALL_TILES > 4 * 256 ? 8 * SMALL_TILES : 4 * 256;
+static_assert(TW_PARTS <= TW_MAX_BLOCKS, "the cast reduces at most that many");
+size_t gate_share_bytes(int64_t M, int64_t H, bool rowwise, int bn) {
+  const size_t b = rowwise ? colpart_at(M, H, bn) +
+                                 (size_t)(col_slices(M, H, bn) * H) * sizeof(uint16_t)
+                           : TW_PARTS * sizeof(uint32_t);
   return (b + 255) & ~(size_t)255;
 }
 
 // The partial maxima of output o: where the kernel writes them (g) and where
 // the cast reads them (src).
-void set_partials(GateArgs &g, int o, CastSource &src, void *share, bool rowwise, int tile) {
+void set_partials(GateArgs &g, int o, CastSource &src, void *share, bool rowwise, int bn) {
   if (rowwise) {
     g.rowpart[o] = static_cast<uint16_t *>(share);
     g.colpart[o] = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(share) +
-                                                colpart_at(g.M[0], g.N[0]));
+                                                colpart_at(g.M[0], g.N[0], bn));
     src.rowpart = g.rowpart[o];
     src.colpart = g.colpart[o];
-    src.row_slices = (int)row_slices(g.N[0], tile);
-    src.col_slices = (int)col_slices(g.M[0]);
+    src.row_slices = (int)row_slices(g.M[0], g.N[0], bn);
+    src.col_slices = (int)col_slices(g.M[0], g.N[0], bn);
   } else {
     g.part[o] = static_cast<uint32_t *>(share);
     src.part = g.part[o];
@@ -252,7 +456,9 @@ hipError_t fill_zero(void *c, int64_t bytes, hipStream_t stream) {
 
 size_t gated_workspace_bytes(int64_t M, int64_t H, int scaling) {
   const bool rw = (scaling & FP8L_ROWWISE) != 0;
-  size_t b = 2 * gate_share_bytes(M, H, rw);
+  size_t b = gate_share_bytes(M, H, rw, BN / 2);            // h
+  const size_t d = 2 * gate_share_bytes(M, H, rw, BN);      // da and db
+  if (b < d) b = d;
   // the forms that leave the quantize or the gate to the separate passes
   const size_t q = quantize_workspace_bytes(M, H, scaling), s = swiglu_workspace_bytes(M, H, scaling);
   if (b < q) b = q;
@@ -282,11 +488,9 @@ hipError_t gated_fwd_launch(const uint8_t *xq, const float *sx, const uint8_t *w
     CastSource src = {};
     src.x = h;
     if (o) set_partials(g, 0, src, workspace, rw, BN / 2);
-    int blocks = 0;
-    const hipError_t e = a ? launch_gate<EPI_GATE_AB, 0>(g, rw, &blocks, stream)
-                           : launch_gate<EPI_GATE, 0>(g, rw, &blocks, stream);
+    const hipError_t e = a ? launch_gate<EPI_GATE_AB, 0>(g, rw, &src.nparts, stream)
+                           : launch_gate<EPI_GATE, 0>(g, rw, &src.nparts, stream);
     if (e != hipSuccess || !o) return e;
-    src.nparts = blocks * 4;
     return quantize_cast_launch(src, M, H, scaling, *o, stream);
   }
   if (M * H > 0) {
@@ -337,12 +541,12 @@ hipError_t gated_bwd_launch(const uint8_t *dyq, const float *sdy, const uint8_t 
   sa.x = da;
   sb.x = db;
   set_partials(g, 0, sa, workspace, rw, BN);
-  set_partials(g, 1, sb, static_cast<uint8_t *>(workspace) + gate_share_bytes(M, H, rw), rw, BN);
-  int blocks = 0;
-  hipError_t e = (scaling & FP8L_E5M2) ? launch_gate<EPI_DGATE, 1>(g, rw, &blocks, stream)
-                                       : launch_gate<EPI_DGATE, 0>(g, rw, &blocks, stream);
+  set_partials(g, 1, sb, static_cast<uint8_t *>(workspace) + gate_share_bytes(M, H, rw, BN), rw,
+               BN);
+  hipError_t e = (scaling & FP8L_E5M2) ? launch_gate<EPI_DGATE, 1>(g, rw, &sa.nparts, stream)
+                                       : launch_gate<EPI_DGATE, 0>(g, rw, &sa.nparts, stream);
   if (e != hipSuccess) return e;
-  sa.nparts = sb.nparts = blocks * 4;
+  sb.nparts = sa.nparts;
   e = quantize_cast_launch(sa, M, H, scaling, qa, stream);
   if (e != hipSuccess) return e;
   return quantize_cast_launch(sb, M, H, scaling, qb, stream);

@@ -116,8 +116,9 @@ constexpr uint32_t OOB_C = 0xFFFFFF00u;  // output offset that is dropped
 // that the next kernel would have to write back (measured: the GEMMs of the
 // FFN step 3% faster, the amax passes after them faster too).
 constexpr int C_STORE_AUX = 2;
-// h, da and db are read again right away, by the cast that follows.
-constexpr int GATE_STORE_AUX = 0;
+// (The same for h, da and db, although a cast reads them next: 8B block, h alone
+// 640 us against 676 with plain stores, with a, b and the cast 812 against 815,
+// rowwise 829 against 849; the backward 645 either way.)
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
@@ -938,7 +939,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const uint32_t off = offset(i, u);
-          __builtin_amdgcn_raw_buffer_store_b128(vh[u], rsC, off, row_off(i, u), GATE_STORE_AUX);
+          __builtin_amdgcn_raw_buffer_store_b128(vh[u], rsC, off, row_off(i, u), C_STORE_AUX);
           const uint32_t keep = off != OOB_C ? 0x7FFF7FFFu : 0u;
           uint32_t rm = 0;
 #pragma unroll
@@ -1075,8 +1076,8 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
               cm[1][d] = pk_max(cm[1][d], db & keep);
             }
           }
-          __builtin_amdgcn_raw_buffer_store_b128(x, rsC, off, row_off(i, u), GATE_STORE_AUX);
-          __builtin_amdgcn_raw_buffer_store_b128(y, rsC2, off, row_off(i, u), GATE_STORE_AUX);
+          __builtin_amdgcn_raw_buffer_store_b128(x, rsC, off, row_off(i, u), C_STORE_AUX);
+          __builtin_amdgcn_raw_buffer_store_b128(y, rsC2, off, row_off(i, u), C_STORE_AUX);
           if (RW) {
             rm0 = lanes_max<16>(hmax16(rm0));
             rm1 = lanes_max<16>(hmax16(rm1));

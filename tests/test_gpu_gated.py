@@ -1,7 +1,7 @@
 """GPU gated feed-forward kernels.
 
 * a, b and dh come from the plain GEMM's instructions in its order: for more
-  than 64 tokens they equal fp8_linear_fwd's / fp8_linear_bwd's outputs bit
+  than 16 tokens they equal fp8_linear_fwd's / fp8_linear_bwd's outputs bit
   for bit, and with fewer (the contraction split over 8 waves) they are
   within the instruction's accumulation bound (tests/mfma_model.py) plus 7
   fp32 additions, 7 2^-24 sum |p|, and two bf16 roundings.
@@ -89,8 +89,10 @@ def _x(M, K, rowwise, seed):
     return z.q, z.scale
 
 
-FWD = [(80, 16, 16), (272, 400, 528), (256, 128, 128), (528, 144, 1040), (1040, 784, 304),
-       (512, 2048, 256), (4112, 8208, 144), (4096, 8192, 128)]  # several tiles a workgroup
+FWD = [(32, 144, 400), (80, 16, 16), (272, 400, 528), (256, 128, 128), (528, 144, 1040), (1040, 784, 304),
+       (512, 2048, 256),
+       # more than 128 large tiles: those kernels, several tiles a workgroup
+       (2064, 4112, 384), (4112, 8208, 144), (4096, 8192, 128)]
 
 
 @pytest.mark.parametrize("rowwise", RW, ids=RW_IDS)
@@ -119,8 +121,8 @@ def test_forward(mhk, rowwise):
 
 
 @pytest.mark.parametrize("rowwise", RW, ids=RW_IDS)
-@pytest.mark.parametrize("mhk", [(65, 400, 528), (131, 256, 128), (257, 144, 272),
-                                 (769, 2048, 256)], ids=lambda s: "%dx%dx%d" % s)
+@pytest.mark.parametrize("mhk", [(17, 272, 4112), (50, 1040, 784), (65, 400, 528), (131, 256, 128), (257, 144, 272),
+                                 (769, 2048, 256), (2081, 4112, 144)], ids=lambda s: "%dx%dx%d" % s)
 def test_forward_any_number_of_tokens(mhk, rowwise):
     """M tokens give the first M rows of the padded call, and the rows behind
     them stay as they were."""
@@ -183,7 +185,9 @@ def test_few_tokens(mhk, rowwise):
 
 
 BWD = [(16, 16, 16), (80, 144, 48), (272, 400, 528), (256, 256, 128), (1040, 784, 304),
-       (528, 4112, 400), (4112, 16400, 272)]           # several tiles a workgroup
+       (528, 4112, 400),
+       # more than 128 large tiles: those kernels, several tiles a workgroup
+       (2064, 8208, 128), (2064, 4112, 512), (4112, 16400, 272)]
 
 
 @pytest.mark.parametrize("e5m2", [False, True], ids=["e4m3", "e5m2"])
