@@ -187,8 +187,10 @@ struct CastSource {
   const uint16_t *rowpart, *colpart;
   int row_slices, col_slices;
 };
-hipError_t quantize_cast_launch(const CastSource &src, int64_t rows, int64_t cols, int scaling,
-                                const Fp8Out &o, hipStream_t stream);
+// count (1, or 2 without rstd) tensors of one shape and one count of partials, in
+// the same launches.
+hipError_t quantize_cast_launch(const CastSource *src, int count, int64_t rows, int64_t cols,
+                                int scaling, const Fp8Out *o, hipStream_t stream);
 
 // Layer norm (norm.h).  w, b: bf16, or fp32 with wf32; NULL for 1 and 0.
 struct NormIn {

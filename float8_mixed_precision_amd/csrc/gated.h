@@ -18,8 +18,8 @@
 // k_gate_tile, one tile of 64 rows x 64 columns of h (128 of da and db) per
 // workgroup.
 //
-// Few tokens (M <= SKINNY_M = 16, one MFMA block): k_gated_skinny.  The time is
-// that of reading W1 and W3 once.  A workgroup owns 16 columns of h, its 8 waves
+// Few tokens (one MFMA block, 16) and H too small for the tiles to cover the
+// compute units: k_gated_skinny.  The time is that of reading W1 and W3 once.  A workgroup owns 16 columns of h, its 8 waves
 // split the contraction and join through LDS; weights go straight from memory
 // to the MFMA operands (no byte of them is used twice), x comes from L2.
 //
@@ -65,9 +65,7 @@ __device__ __forceinline__ v8i frag(v4u lo, v4u hi) {
 //
 // One token, 14336 columns, K = 4096: 23.8 us, 4.9 TB/s of weights, the rate of a
 // large copy; with 4 waves and the same loads in flight 26, with 2 k-tiles
-// together 28, with non-temporal loads 27.  More tokens go to the small tiles:
-// a form of this kernel with 4 token blocks took 33 us at 64 tokens, where every
-// workgroup reads all of x.
+// together 28, with non-temporal loads 27.
 template <bool KFULL>
 __global__ __launch_bounds__(64 * SK_WAVES) void k_gated_skinny(SkinnyArgs p) {
   __shared__ v4f red[SK_WAVES][2][64];
@@ -136,6 +134,16 @@ __global__ __launch_bounds__(64 * SK_WAVES) void k_gated_skinny(SkinnyArgs p) {
   }
   *reinterpret_cast<uint2 *>(p.h + at) = make_uint2(gate_fwd2(pa.x, pb.x), gate_fwd2(pa.y, pb.y));
 }
+
+// Which calls it takes: up to 4 tokens, and up to 16 where the small tiles
+// below, one per 64 columns, are fewer than three for every four compute
+// units.  Measured, this kernel against the tiles, K = 4096, us for one token
+// and for 16: H = 4096 7.5 / 15.1 and 8.3 / 15.3, 8192 13.5 / 15.4 and 15.0 / 16.3,
+// 10240 19.3 / 21.3 and 21.6 / 21.0, 14336 24.1 / 23.0 (rowwise 24.3 / 27.4) and
+// 29.5 / 24.3; 4 tokens 25.2 / 26.5, 8 tokens 26.7 / 23.4.  (With more tokens every
+// workgroup reads all of x: a form with 4 token blocks took 33 us at 64 tokens
+// and H = 14336, the tiles 28.)
+bool few_tokens(int64_t M, int64_t H) { return M <= 4 || (M <= SKINNY_M && H < 64 * 192); }
 
 hipError_t skinny_launch(const SkinnyArgs &p, hipStream_t stream) {
   const dim3 grid((unsigned)(p.H / 16)), block(64 * SK_WAVES);
@@ -222,7 +230,8 @@ __global__ __launch_bounds__(256) void k_gate_tile(GateArgs g) {
   const int hr = (lane & 7) ^ ((lane >> 3) & 1);
   const int c0 = ((2 * g4) ^ hr) << 4, c1 = ((2 * g4 + 1) ^ hr) << 4;
   const int ra = (wm * 32 + l16) * BK, rb = (TM + wn * 64 + l16) * BK;
-  // the places of the lane's outputs; EPI_DGATE reads its a and b first of all
+  // the places of the lane's outputs; their scales, and EPI_DGATE's a and b, are
+  // read first of all
   const int mrow = m0 + wm * 32 + l16;
   const int ncol = n0 + wn * WC + g4 * 4;
   uint2 ga[GATE ? 1 : NJ][2], gb[GATE ? 1 : NJ][2];
@@ -236,6 +245,17 @@ __global__ __launch_bounds__(256) void k_gate_tile(GateArgs g) {
         gb[j][i] = *reinterpret_cast<const uint2 *>(g.b + at);
       }
   }
+  float ia[2], ib[NJ][4], ib2[NJ][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) ia[i] = g.sa[0][RW ? min(mrow + i * FR, M - 1) : 0];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int at = RW ? min(ncol + j * FR + e, N - 1) : 0;
+      ib[j][e] = g.sb[0][at];
+      ib2[j][e] = GATE ? g.sb2[at] : 1.f;
+    }
   fill(0);
   if (nk > 1) fill(1);
   for (int t = 0; t < nk; ++t) {
@@ -268,18 +288,15 @@ __global__ __launch_bounds__(256) void k_gate_tile(GateArgs g) {
   uint16_t *C = static_cast<uint16_t *>(g.C[0]);
   uint32_t rm[2][2] = {};                          // [output][i]: row maxima (u16 pairs)
   uint2 cm[2][NJ] = {};                            // [output][j]: column maxima
-  float ia[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) ia[i] = 1.0f / g.sa[0][RW ? min(mrow + i * FR, M - 1) : 0];
+  for (int i = 0; i < 2; ++i) ia[i] = 1.0f / ia[i];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     const int n = ncol + j * FR;
-    float ib[4], ib2[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int at = RW ? min(n + e, N - 1) : 0;
-      ib[e] = 1.0f / g.sb[0][at];
-      ib2[e] = GATE ? 1.0f / g.sb2[at] : 0.f;
+      ib[j][e] = 1.0f / ib[j][e];
+      if (GATE) ib2[j][e] = 1.0f / ib2[j][e];
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -287,14 +304,15 @@ __global__ __launch_bounds__(256) void k_gate_tile(GateArgs g) {
       const bool ok = m < M && n < N;
       const size_t at = (size_t)m * N + n;
       const v4f p = acc[j][i];
-      const uint2 pa = make_uint2(bf16x2_bits((p[0] * ia[i]) * ib[0], (p[1] * ia[i]) * ib[1]),
-                                  bf16x2_bits((p[2] * ia[i]) * ib[2], (p[3] * ia[i]) * ib[3]));
+      const uint2 pa =
+          make_uint2(bf16x2_bits((p[0] * ia[i]) * ib[j][0], (p[1] * ia[i]) * ib[j][1]),
+                     bf16x2_bits((p[2] * ia[i]) * ib[j][2], (p[3] * ia[i]) * ib[j][3]));
       uint2 o[2];
       if constexpr (GATE) {
         const v4f r = acc[j + NJ][i];
         const uint2 pb =
-            make_uint2(bf16x2_bits((r[0] * ia[i]) * ib2[0], (r[1] * ia[i]) * ib2[1]),
-                       bf16x2_bits((r[2] * ia[i]) * ib2[2], (r[3] * ia[i]) * ib2[3]));
+            make_uint2(bf16x2_bits((r[0] * ia[i]) * ib2[j][0], (r[1] * ia[i]) * ib2[j][1]),
+                       bf16x2_bits((r[2] * ia[i]) * ib2[j][2], (r[3] * ia[i]) * ib2[j][3]));
         if (EPI == EPI_GATE_AB && ok) {
           *reinterpret_cast<uint2 *>(g.a + at) = pa;
           *reinterpret_cast<uint2 *>(g.b + at) = pb;
@@ -366,10 +384,14 @@ int64_t tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
 // the quantize of h: 112 large tiles 29 / 47 (80 x 14336), 48 / 49 (256 x 14336),
 // 120 tiles 26 / 28, 128 tiles 35 / 35 and 49 / 49, 224 tiles 60 / 52, 256 tiles 45 /
 // 34.  Backward: 51 tiles 23 / 33, 64 tiles 32 / 45 and 38 / 60, 85 tiles 44 / 40, 112
-// tiles 55 / 60, 128 tiles 47 / 43.
+// tiles 55 / 60, 128 tiles 47 / 43.  One row of small tiles is better than one of
+// large ones at any number: 64 x 28672, K = 8192, 224 tiles, 103 / 132; backward 112
+// tiles 51 / 90; at 128 rows 137 / 154 but rowwise 154 / 129.  (The tensorwise
+// maxima, one per small tile, bound that number.)
 constexpr int64_t SMALL_TILES = 128, SMALL_TILES_BWD = 80;
 bool small_tiles(int64_t M, int64_t H, int bn) {
-  return tiles(M, BM) * tiles(H, bn) <= (bn == BN ? SMALL_TILES_BWD : SMALL_TILES);
+  return tiles(M, BM) * tiles(H, bn) <= (bn == BN ? SMALL_TILES_BWD : SMALL_TILES) ||
+         (M <= TM && tiles(H, bn / 2) <= 8 * SMALL_TILES);
 }
 
 // One problem.  args: A, sa, B, sb, C, M, N, K and the gate's own fields set;
@@ -470,7 +492,7 @@ hipError_t gated_fwd_launch(const uint8_t *xq, const float *sx, const uint8_t *w
                             int64_t H, int64_t K, int scaling, uint16_t *a, uint16_t *b,
                             uint16_t *h, const Fp8Out *o, void *workspace, hipStream_t stream) {
   const bool rw = (scaling & FP8L_ROWWISE) != 0;
-  if (M * H > 0 && K > 0 && M > SKINNY_M) {
+  if (M * H > 0 && K > 0 && !few_tokens(M, H)) {
     GateArgs g = {};
     g.A[0] = xq;
     g.sa[0] = sx;
@@ -491,7 +513,7 @@ hipError_t gated_fwd_launch(const uint8_t *xq, const float *sx, const uint8_t *w
     const hipError_t e = a ? launch_gate<EPI_GATE_AB, 0>(g, rw, &src.nparts, stream)
                            : launch_gate<EPI_GATE, 0>(g, rw, &src.nparts, stream);
     if (e != hipSuccess || !o) return e;
-    return quantize_cast_launch(src, M, H, scaling, *o, stream);
+    return quantize_cast_launch(&src, 1, M, H, scaling, o, stream);
   }
   if (M * H > 0) {
     hipError_t e;
@@ -543,13 +565,14 @@ hipError_t gated_bwd_launch(const uint8_t *dyq, const float *sdy, const uint8_t 
   set_partials(g, 0, sa, workspace, rw, BN);
   set_partials(g, 1, sb, static_cast<uint8_t *>(workspace) + gate_share_bytes(M, H, rw, BN), rw,
                BN);
-  hipError_t e = (scaling & FP8L_E5M2) ? launch_gate<EPI_DGATE, 1>(g, rw, &sa.nparts, stream)
-                                       : launch_gate<EPI_DGATE, 0>(g, rw, &sa.nparts, stream);
+  const hipError_t e = (scaling & FP8L_E5M2)
+                           ? launch_gate<EPI_DGATE, 1>(g, rw, &sa.nparts, stream)
+                           : launch_gate<EPI_DGATE, 0>(g, rw, &sa.nparts, stream);
   if (e != hipSuccess) return e;
   sb.nparts = sa.nparts;
-  e = quantize_cast_launch(sa, M, H, scaling, qa, stream);
-  if (e != hipSuccess) return e;
-  return quantize_cast_launch(sb, M, H, scaling, qb, stream);
+  const CastSource src[2] = {sa, sb};
+  const Fp8Out out[2] = {qa, qb};
+  return quantize_cast_launch(src, 2, M, H, scaling, out, stream);
 }
 
 }  // namespace fp8l

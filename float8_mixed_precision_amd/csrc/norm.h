@@ -856,7 +856,7 @@ hipError_t norm_quantize_launch(const NormIn &in, int scaling, void *y, float *m
     src.mean = in.rms ? nullptr : mean;
     src.rstd = rstd;
   }
-  return quantize_cast_launch(src, in.rows, in.cols, scaling, o, stream);
+  return quantize_cast_launch(&src, 1, in.rows, in.cols, scaling, &o, stream);
 }
 
 hipError_t norm_bwd_launch(const void *dy, const NormIn &in, int f32, const float *mean,

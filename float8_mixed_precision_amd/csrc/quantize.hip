@@ -212,11 +212,21 @@ constexpr int FR_OUT = 64;
 constexpr int FR_SLICES = 4;
 constexpr int FR_UNROLL = 8;
 static_assert(FR_OUT * FR_SLICES == 256, "one finalize workgroup is 256 threads");
+// Grid row y finalizes tensor y of a pair (one shape, one count of partials).
+struct FinalizeJob {
+  const uint16_t *rowpart, *colpart;
+  float *scale, *scale_t, *amax_out;
+};
 template <int FMT>
-__global__ __launch_bounds__(256) void k_finalize_rowwise(
-    const uint16_t *__restrict__ rowpart, const uint16_t *__restrict__ colpart,
-    int rows, int cols, int tiles_c, int tiles_r, int nbr, float *scale, float *scale_t,
-    float *amax_out) {
+__global__ __launch_bounds__(256) void k_finalize_rowwise(FinalizeJob job0, FinalizeJob job1,
+                                                          int rows, int cols, int tiles_c,
+                                                          int tiles_r, int nbr) {
+  const bool second = blockIdx.y != 0;
+  const uint16_t *__restrict__ rowpart = second ? job1.rowpart : job0.rowpart;
+  const uint16_t *__restrict__ colpart = second ? job1.colpart : job0.colpart;
+  float *scale = second ? job1.scale : job0.scale;
+  float *scale_t = second ? job1.scale_t : job0.scale_t;
+  float *amax_out = second ? job1.amax_out : job0.amax_out;
   const int o = threadIdx.x % FR_OUT;
   const int sl = threadIdx.x / FR_OUT;
   const bool is_row = (int)blockIdx.x < nbr;
@@ -303,12 +313,12 @@ __device__ __forceinline__ void load_param8(float (&f)[8], const void *p, int wf
     f[6] = bf16_to_f32(v.w & 0xFFFFu); f[7] = bf16_to_f32(v.w >> 16);
   }
 }
-template <int MODE, int FMT, bool NORM = false>
-__global__ __launch_bounds__(CT_THREADS) void k_cast_transpose(
+template <int MODE, int FMT, bool NORM>
+__device__ __forceinline__ void cast_tile(
     const uint16_t *__restrict__ x, int rows, int cols, int tiles_c,
     float *__restrict__ scale, float *__restrict__ scale_t,
     const uint32_t *__restrict__ part, int nparts, float *__restrict__ amax_out,
-    uint8_t *__restrict__ q, uint8_t *__restrict__ qt, CastNorm nm) {
+    uint8_t *__restrict__ q, uint8_t *__restrict__ qt, const CastNorm &nm) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[CT_T * CT_T];
   const int tid = threadIdx.x;
   // block -> (tile_r, tile_c): groups of CT_GROUP row tiles (the last one
@@ -468,6 +478,37 @@ __global__ __launch_bounds__(CT_THREADS) void k_cast_transpose(
   }
 }
 
+template <int MODE, int FMT, bool NORM = false>
+__global__ __launch_bounds__(CT_THREADS) void k_cast_transpose(
+    const uint16_t *__restrict__ x, int rows, int cols, int tiles_c,
+    float *__restrict__ scale, float *__restrict__ scale_t,
+    const uint32_t *__restrict__ part, int nparts, float *__restrict__ amax_out,
+    uint8_t *__restrict__ q, uint8_t *__restrict__ qt, CastNorm nm) {
+  cast_tile<MODE, FMT, NORM>(x, rows, cols, tiles_c, scale, scale_t, part, nparts, amax_out, q,
+                             qt, nm);
+}
+
+// Two tensors of one shape (and one count of partials) in one launch: grid
+// row y casts tensor y.  (Each is a call of its own, not a choice of
+// pointers, which would lose that they do not alias.)
+struct CastJob {
+  const uint16_t *x;
+  float *scale, *scale_t;
+  const uint32_t *part;
+  float *amax_out;
+  uint8_t *q, *qt;
+};
+template <int MODE, int FMT>
+__global__ __launch_bounds__(CT_THREADS) void k_cast_pair(CastJob a, CastJob b, int rows, int cols,
+                                                          int tiles_c, int nparts) {
+  if (blockIdx.y == 0)
+    cast_tile<MODE, FMT, false>(a.x, rows, cols, tiles_c, a.scale, a.scale_t, a.part, nparts,
+                                a.amax_out, a.q, a.qt, CastNorm{});
+  else
+    cast_tile<MODE, FMT, false>(b.x, rows, cols, tiles_c, b.scale, b.scale_t, b.part, nparts,
+                                b.amax_out, b.q, b.qt, CastNorm{});
+}
+
 // --------------------------------------------------------------- encode --
 
 template <int FMT>
@@ -519,35 +560,50 @@ size_t quantize_workspace_bytes(int64_t rows, int64_t cols, int scaling) {
 namespace {
 
 template <int FMT, bool NORM>
-hipError_t cast_fmt(const CastSource &src, int64_t rows, int64_t cols, bool rowwise,
-                    const Fp8Out &o, hipStream_t stream) {
-  const uint16_t *xb = static_cast<const uint16_t *>(src.x);
-  const int R = (int)rows, C = (int)cols;
-  const CastNorm nm = {src.w, src.b, src.wf32, src.mean, src.rstd};
+hipError_t cast_fmt(const CastSource *src, int count, int64_t rows, int64_t cols, bool rowwise,
+                    const Fp8Out *o, hipStream_t stream) {
+  const int R = (int)rows, C = (int)cols, l = count - 1;   // l: the last tensor
+  const CastNorm nm = {src->w, src->b, src->wf32, src->mean, src->rstd};
   if (rowwise) {
     const int64_t nbr = cdiv(rows, FR_OUT), nbc = cdiv(cols, FR_OUT);
+    auto job = [&](int i) {
+      return FinalizeJob{src[i].rowpart, src[i].colpart, o[i].scale, o[i].scale_t, o[i].amax};
+    };
     if (nbr + nbc > 0)
-      hipLaunchKernelGGL(k_finalize_rowwise<FMT>, dim3((unsigned)(nbr + nbc)), dim3(256), 0,
-                         stream, src.rowpart, src.colpart, R, C, src.row_slices, src.col_slices,
-                         (int)nbr, o.scale, o.scale_t, o.amax);
-  } else if (src.nparts == 0) {
-    hipLaunchKernelGGL(k_finalize_tw_empty<FMT>, dim3(1), dim3(64), 0, stream, o.scale,
-                       o.scale_t, o.amax);
+      hipLaunchKernelGGL(k_finalize_rowwise<FMT>, dim3((unsigned)(nbr + nbc), (unsigned)count),
+                         dim3(256), 0, stream, job(0), job(l), R, C, src->row_slices,
+                         src->col_slices, (int)nbr);
+  } else if (src->nparts == 0) {
+    for (int i = 0; i < count; ++i)
+      hipLaunchKernelGGL(k_finalize_tw_empty<FMT>, dim3(1), dim3(64), 0, stream, o[i].scale,
+                         o[i].scale_t, o[i].amax);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t ct_r = cdiv(rows, CT_T), ct_c = cdiv(cols, CT_T);
   if (ct_r * ct_c > 0) {
-    if (!rowwise)
-      hipLaunchKernelGGL((k_cast_transpose<MODE_TW, FMT, NORM>), dim3((unsigned)(ct_r * ct_c)),
-                         dim3(CT_THREADS), 0, stream, xb, R, C, (int)ct_c, o.scale, o.scale_t,
-                         src.part, src.nparts, o.amax, static_cast<uint8_t *>(o.q),
-                         static_cast<uint8_t *>(o.qt), nm);
-    else
-      hipLaunchKernelGGL((k_cast_transpose<MODE_RW, FMT, NORM>), dim3((unsigned)(ct_r * ct_c)),
-                         dim3(CT_THREADS), 0, stream, xb, R, C, (int)ct_c, o.scale, o.scale_t,
-                         nullptr, 0, nullptr, static_cast<uint8_t *>(o.q),
-                         static_cast<uint8_t *>(o.qt), nm);
+    const unsigned nb = (unsigned)(ct_r * ct_c);
+    auto job = [&](int i) {
+      return CastJob{static_cast<const uint16_t *>(src[i].x), o[i].scale, o[i].scale_t, src[i].part,
+                     o[i].amax, static_cast<uint8_t *>(o[i].q), static_cast<uint8_t *>(o[i].qt)};
+    };
+    const CastJob j = job(0);
+    if (count == 2) {
+      if (rowwise)
+        hipLaunchKernelGGL((k_cast_pair<MODE_RW, FMT>), dim3(nb, 2), dim3(CT_THREADS), 0, stream,
+                           j, job(1), R, C, (int)ct_c, 0);
+      else
+        hipLaunchKernelGGL((k_cast_pair<MODE_TW, FMT>), dim3(nb, 2), dim3(CT_THREADS), 0, stream,
+                           j, job(1), R, C, (int)ct_c, src->nparts);
+    } else if (!rowwise) {
+      hipLaunchKernelGGL((k_cast_transpose<MODE_TW, FMT, NORM>), dim3(nb), dim3(CT_THREADS), 0,
+                         stream, j.x, R, C, (int)ct_c, j.scale, j.scale_t, j.part, src->nparts,
+                         j.amax_out, j.q, j.qt, nm);
+    } else {
+      hipLaunchKernelGGL((k_cast_transpose<MODE_RW, FMT, NORM>), dim3(nb), dim3(CT_THREADS), 0,
+                         stream, j.x, R, C, (int)ct_c, j.scale, j.scale_t, nullptr, 0, nullptr,
+                         j.q, j.qt, nm);
+    }
   }
   return hipGetLastError();
 }
@@ -572,7 +628,7 @@ hipError_t finish_fmt(const void *x, int64_t rows, int64_t cols, bool rowwise, i
     src.nparts = nparts;
   }
   const Fp8Out o = {q, qt, scale, scale_t, amax_out};
-  return cast_fmt<FMT, false>(src, rows, cols, rowwise, o, stream);
+  return cast_fmt<FMT, false>(&src, 1, rows, cols, rowwise, &o, stream);
 }
 
 // first pass (amax partial maxima of x), then the second half
@@ -660,12 +716,12 @@ hipError_t quantize_scaled_launch(const void *x, int64_t rows, int64_t cols,
   return hipGetLastError();
 }
 
-hipError_t quantize_cast_launch(const CastSource &src, int64_t rows, int64_t cols, int scaling,
-                                const Fp8Out &o, hipStream_t stream) {
+hipError_t quantize_cast_launch(const CastSource *src, int count, int64_t rows, int64_t cols,
+                                int scaling, const Fp8Out *o, hipStream_t stream) {
   const bool rw = (scaling & FP8L_ROWWISE) != 0;
-  if (src.rstd) return cast_fmt<0, true>(src, rows, cols, rw, o, stream);  // norms: E4M3 only
-  if (scaling & FP8L_E5M2) return cast_fmt<1, false>(src, rows, cols, rw, o, stream);
-  return cast_fmt<0, false>(src, rows, cols, rw, o, stream);
+  if (src->rstd) return cast_fmt<0, true>(src, count, rows, cols, rw, o, stream);  // E4M3 only
+  if (scaling & FP8L_E5M2) return cast_fmt<1, false>(src, count, rows, cols, rw, o, stream);
+  return cast_fmt<0, false>(src, count, rows, cols, rw, o, stream);
 }
 
 hipError_t encode_launch(const float *in, uint8_t *out, int64_t n, int fmt,

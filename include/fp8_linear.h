@@ -377,8 +377,8 @@ FP8L_API int fp8_swiglu_bwd(const void *dh, const void *a, const void *b, int64_
  *   scaling FP8L_TENSORWISE or FP8L_ROWWISE, of the operands and of hq
  *   workspace / workspace_bytes: >= fp8_gated_workspace_bytes(M, H, scaling)
  * H and K are multiples of 16, and M where h is quantized; sizes as for
- * fp8_linear_fwd.  The order of the fp32 additions depends on M (up to 16
- * tokens split the contraction over the waves of a workgroup); equal calls
+ * fp8_linear_fwd.  The order of the fp32 additions depends on M and H (calls of
+ * up to 16 tokens may split the contraction over a workgroup's waves); equal calls
  * give equal bits.  The workspace's contents are undefined on entry and exit,
  * not shared by calls in flight together.
  */

@@ -121,7 +121,7 @@ def test_forward(mhk, rowwise):
 
 
 @pytest.mark.parametrize("rowwise", RW, ids=RW_IDS)
-@pytest.mark.parametrize("mhk", [(17, 272, 4112), (50, 1040, 784), (65, 400, 528), (131, 256, 128), (257, 144, 272),
+@pytest.mark.parametrize("mhk", [(17, 272, 4112), (50, 1040, 784), (40, 28672, 32), (65, 400, 528), (131, 256, 128), (257, 144, 272),
                                  (769, 2048, 256), (2081, 4112, 144)], ids=lambda s: "%dx%dx%d" % s)
 def test_forward_any_number_of_tokens(mhk, rowwise):
     """M tokens give the first M rows of the padded call, and the rows behind
@@ -146,7 +146,7 @@ def test_forward_any_number_of_tokens(mhk, rowwise):
 @pytest.mark.parametrize("rowwise", RW, ids=RW_IDS)
 @pytest.mark.parametrize("mhk", [(1, 16, 16), (1, 512, 4096), (2, 144, 1040), (15, 400, 528),
                                  (16, 256, 2048), (17, 256, 1152), (33, 272, 4112), (50, 128, 784),
-                                 (64, 528, 3088)], ids=lambda s: "%dx%dx%d" % s)
+                                 (64, 528, 3088), (3, 14336, 144)], ids=lambda s: "%dx%dx%d" % s)
 def test_few_tokens(mhk, rowwise):
     M, H, K = mhk
     xq, sx = _x(M, K, rowwise, 74)
@@ -187,7 +187,7 @@ def test_few_tokens(mhk, rowwise):
 BWD = [(16, 16, 16), (80, 144, 48), (272, 400, 528), (256, 256, 128), (1040, 784, 304),
        (528, 4112, 400),
        # more than 128 large tiles: those kernels, several tiles a workgroup
-       (2064, 8208, 128), (2064, 4112, 512), (4112, 16400, 272)]
+       (64, 28672, 48), (2064, 8208, 128), (2064, 4112, 512), (4112, 16400, 272)]
 
 
 @pytest.mark.parametrize("e5m2", [False, True], ids=["e4m3", "e5m2"])
