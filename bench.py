@@ -52,6 +52,9 @@ def parse():
     p.add_argument("--ffn-block-only", action="store_true",
                    help="only measure the SwiGLU FFN block (profiling runs of its kernels); "
                         "prints its JSON object and exits")
+    p.add_argument("--fused", action="store_true",
+                   help="with --ffn-block-only: the block with its norm in front and the gate "
+                        "in the GEMMs' kernels")
     p.add_argument("--phase-timing", action="store_true",
                    help="only time the GEMM's phases per workgroup (the measurement build "
                         "libfp8phase.so) at the 8B FFN GEMM shapes and exit")
@@ -198,14 +201,17 @@ def measure_pipelined(steps, flops_per_step: int, stream, reps: int = 20):
             "gemm_avg_launch_us": round(sum(t for _, _, t in g) * 1e3 / sum(n for _, n, _ in g), 2)}
 
 
-def measure_ffn_block(steps, wl, stream, reps: int = 5, e5m2_grad: bool = False):
+def measure_ffn_block(steps, wl, stream, reps: int = 5, e5m2_grad: bool = False,
+                      fused: bool = False):
     """The SwiGLU feed-forward block on the FFN workload's tensors (x and W1
     of w1, W3 of w3, W2 and dY of w2): x quantized once for w1 and w3, the
     SwiGLU producers with the amax of h, da, db fused in, nine GEMMs, on one
     stream (the quantizes of the weights and of dY on a side stream measured
     slower: they take power from the GEMMs).  Wall time per step bracketed
     by device synchronisation; HIP events around every launch in further
-    steps for the split and the SwiGLU entry points' bandwidth."""
+    steps for the split and the SwiGLU entry points' bandwidth.  With
+    ``fused`` the block starts with a layer norm of x (and ends with its
+    backward), and the gate runs in the GEMMs' kernels."""
     import torch
     from float8_mixed_precision_amd import ops
 
@@ -213,7 +219,12 @@ def measure_ffn_block(steps, wl, stream, reps: int = 5, e5m2_grad: bool = False)
     if names != ["w1", "w3", "w2"]:
         return None
     w1, w3, w2 = steps[0], steps[1], steps[2]
-    blk = ops.SwiGLUFFNStep(w1.x, w1.w, w3.w, w2.w, w2.dy, w1.rowwise, e5m2_grad=e5m2_grad)
+    norm = None
+    if fused:
+        d = dict(dtype=torch.bfloat16, device=w1.x.device)
+        norm = (torch.ones(w1.K, **d), torch.zeros(w1.K, **d))
+    blk = ops.SwiGLUFFNStep(w1.x, w1.w, w3.w, w2.w, w2.dy, w1.rowwise, e5m2_grad=e5m2_grad,
+                            fused=fused, norm=norm)
     M, D, H = blk.M, blk.D, blk.H
     for _ in range(2):
         blk.run()
@@ -229,11 +240,11 @@ def measure_ffn_block(steps, wl, stream, reps: int = 5, e5m2_grad: bool = False)
         rec += [(k, w, None, a, b) for k, w, a, b in blk.run(record=True)]
     torch.cuda.synchronize()
     split = {}
-    for kind in ("gemm", "quantize", "swiglu"):
+    for kind in ("gemm", "quantize", "norm" if fused else "swiglu"):
         split[kind] = round(sum(a.elapsed_time(b) for k, _, _, a, b in rec if k == kind) / reps, 4)
     sw = {}
     per = [(w, a.elapsed_time(b)) for k, w, _, a, b in rec if k == "swiglu"]
-    for i, name in enumerate(("swiglu_fwd", "swiglu_bwd")):
+    for i, name in enumerate(() if fused else ("swiglu_fwd", "swiglu_bwd")):
         v = per[i::2]
         work, ms = v[0][0], sum(t for _, t in v) / len(v)
         ach = work / (ms * 1e-3) / 1e9
@@ -241,6 +252,14 @@ def measure_ffn_block(steps, wl, stream, reps: int = 5, e5m2_grad: bool = False)
                     "unit": "GB/s", "frac": round(ach / PEAK_HBM_GBS, 4),
                     "bytes_per_call": work, "avg_call_us": round(ms * 1e3, 2)}
     flops = blk.flops
+    if fused:
+        del blk
+        return {"metric": "SwiGLU FFN block fwd+bwd with a layer norm in front, the gate in the "
+                          "GEMMs' kernels (their casts counted with them)%s"
+                          % (", gradients E5M2" if e5m2_grad else ""),
+                "value": round(flops / wall / 1e12, 2), "unit": "TFLOP/s",
+                "shape": {"M": M, "D": D, "H": H}, "flops_per_step": flops, "steps": reps,
+                "ms_per_step": round(wall * 1e3, 4), "split_ms_per_step": split}
     # bytes of quantize traffic (amax pass + cast) per step, this block
     # against the same block with x quantized per linear and plain
     # quantizes of h, da, db after a SwiGLU that only writes them
@@ -807,7 +826,8 @@ def main():
     stream = torch.cuda.current_stream()
     if args.ffn_block_only:
         print("[bench] ffn block only", file=sys.stderr, flush=True)
-        print(json.dumps(measure_ffn_block(steps, wl, stream, reps=args.steps)), flush=True)
+        print(json.dumps(measure_ffn_block(steps, wl, stream, reps=args.steps,
+                                           fused=args.fused)), flush=True)
         return
 
     # one step on the current stream: per linear its quantizes, forward GEMM
@@ -908,6 +928,8 @@ def main():
             result["next_rows"]["ffn_block"] = blk
             result["next_rows"]["ffn_block_e5m2"] = measure_ffn_block(steps, wl, stream,
                                                                       e5m2_grad=True)
+            result["next_rows"]["ffn_block_fused_norm"] = measure_ffn_block(steps, wl, stream,
+                                                                            fused=True)
     if not args.no_next_rows and args.workload == "ffn8b_tw":
         # its own tensors next to the FFN's (a few GB of 288)
         print("[bench] rowwise outlier step", file=sys.stderr, flush=True)

@@ -164,9 +164,11 @@ hipError_t skinny_launch(const SkinnyArgs &p, hipStream_t stream) {
 // compute unit and cover each other's epilogue, which therefore works in the
 // accumulators' own layout: 8-byte accesses of 4 columns, no staging.
 //
-// At 1040 x 1808 (K = 784, rowwise, a and b stored) TILE_FWD_US, at 528 x 4112
-// (K = 400) backward TILE_BWD_US: with 75 and 51 tiles of the large kernel the
-// same GEMMs take 26 and 32 us.
+// Training forward of 1040 x 1808 (K = 784, rowwise, with the quantize of h) 20 us
+// against 28 with the 75 tiles of the large kernel, backward of 528 x 4112 (K =
+// 400, with both quantizes) 26 against 42 with its 51 tiles: too little work
+// to fill the chip either way, bound by the latency of the few k-tiles, the
+// epilogue and the launches after it.
 constexpr int TM = 64;
 constexpr int TB = 128;                            // rows of the B slab
 constexpr int T_STAGE = (TM + TB) * BK;            // 24 KB
@@ -215,7 +217,7 @@ __global__ __launch_bounds__(256) void k_gate_tile(GateArgs g) {
       const int r = (i < 2 ? i : i - 2) * 8 + lr;  // row of this wave's part
       // h(r) of the slab row: parts start at multiples of 16 rows
       const int c = (lane & 7) ^ (r & 7) ^ ((r >> 3) & 1);
-      const uint32_t off = k0 + c * 16 < K ? (uint32_t)(r * K + c * 16) : OOB;
+      const uint32_t off = k0 + c * 16 < K ? (uint32_t)r * (uint32_t)K + (uint32_t)(c * 16) : OOB;
       if (i < 2) dma16(rsA, st + (uint32_t)((wave * 16 + i * 8) * BK), off, (uint32_t)k0);
       else dma16(rsB, st + (uint32_t)((TM + wave * 32 + (i - 2) * 8) * BK), off, (uint32_t)k0);
     }

@@ -925,10 +925,10 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
       // row u * 8 + lane / 8 of pass i: the lane's offset in row 0, and what the
       // row adds to it (in the instruction's scalar offset)
       const int row0 = m0 + wm * WM + (lane_e >> 3);
-      const uint32_t off0 = (uint32_t)((row0 * N + scol) * 2);
+      const uint32_t off0 = ((uint32_t)row0 * (uint32_t)N + (uint32_t)scol) * 2u;
       const int rows_left = col_ok ? M - row0 : 0;
       auto offset = [&](int i, int u) { return i * FR + u * 8 < rows_left ? off0 : OOB_C; };
-      auto row_off = [&](int i, int u) { return (i * FR + u * 8) * N * 2; };
+      auto row_off = [&](int i, int u) { return (uint32_t)(i * FR + u * 8) * (uint32_t)N * 2u; };
       // the row maxima of the wave's columns (nothing is stored where no maxima
       // are wanted)
       const __amdgpu_buffer_rsrc_t rsRow = __builtin_amdgcn_make_buffer_rsrc(
@@ -1016,10 +1016,10 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
       // row u * 4 + lane / 16 of pass i: the lane's offset in row 0, and what the
       // row adds to it (in the instruction's scalar offset)
       const int row0 = m0 + wm * WM + (lane_e >> 4);
-      const uint32_t off0 = (uint32_t)((row0 * N + scol) * 2);
+      const uint32_t off0 = ((uint32_t)row0 * (uint32_t)N + (uint32_t)scol) * 2u;
       const int rows_left = col_ok ? M - row0 : 0;
       auto offset = [&](int i, int u) { return i * FR + u * 4 < rows_left ? off0 : OOB_C; };
-      auto row_off = [&](int i, int u) { return (i * FR + u * 4) * N * 2; };
+      auto row_off = [&](int i, int u) { return (uint32_t)(i * FR + u * 4) * (uint32_t)N * 2u; };
       auto load_ab = [&](int i) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {

@@ -15,7 +15,7 @@
 // Bound: HBM.  A row (or the share of one) sits in registers between the
 // reductions; TPR threads work on a row: one wave for short rows or where
 // there are many (no barrier, reductions by DPP), 256 or 1024 threads for
-// long rows or few (norm_shape).
+// long rows or few (with_shape).
 //
 // The quantize forms need y only as fp8 codes.  Per-token codes (no
 // transposed copy) come out of the same pass, since a row's amax is known

@@ -432,7 +432,9 @@ FP8L_API int fp8_gated_bwd(const void *dyq, const float *sdy, const void *w2tq,
  * Norms take any number of rows, and any 1 <= cols <= FP8L_NORM_MAX_COLS
  * except where codes are written (multiples of 16): FP8L_ESHAPE otherwise.
  * x, y, dy, dx, weight and bias need 16-byte alignment, as every tensor.
- * Outputs must not overlap inputs or one another.
+ * Outputs must not overlap inputs or one another.  The order of the fp32
+ * additions within a row depends on cols and on the number of rows; equal
+ * calls give equal bits.
  */
 #define FP8L_LAYERNORM 0
 #define FP8L_RMSNORM   1

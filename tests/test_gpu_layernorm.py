@@ -327,3 +327,43 @@ def test_side_stream_and_graph():
         step()
         for a, p in zip(results(), got):
             assert torch.equal(a, p)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 elements: the last rows of y and dx are those of the
+    formulas, the codes (both copies) those of the last rows of y."""
+    rows, cols = 1 << 20, 4112                      # 8.6 GB of bf16
+    bf = dict(dtype=BF, device=G.DEV)
+    x = torch.zeros((rows, cols), **bf)
+    tail = torch.randn((16, cols), generator=torch.Generator().manual_seed(4)).to(BF)
+    x[-16:] = tail.to(G.DEV)
+    w, b = _make(1, cols, BF, BF, 11)[1:3]
+    wd, bd = w.to(G.DEV), b.to(G.DEV)
+    G.say("layernorm past 32 bits", rows, cols)
+    y, m, r = ops.fp8_layernorm_fwd(x, wd, bd)
+    torch.cuda.synchronize()
+    m64, r64, y64, dtol, rtol, ytol = _forward64(tail, w, b, False)
+    _within(y[-16:], y64, ytol + _half(BF) * (np.abs(y64) + ytol), "y")
+    _within(m[-16:], m64, dtol, "mean")
+    assert torch.equal(y[5], bd)                    # a row of zeros gives the bias
+    want = y[-16:].clone()
+    del y
+    dx, _, _ = ops.fp8_layernorm_bwd(x, x, wd, m, r, want_w=False, want_b=False)
+    torch.cuda.synchronize()
+    dx64, _, _, xt, _, _ = _backward64(tail, tail, w, m[-16:], r[-16:], False)
+    _within(dx[-16:], dx64, xt + _half(BF) * (np.abs(dx64) + xt), "dx")
+    assert not dx[:-16].any()
+    del dx
+    for rowwise in (False, True):
+        G.say("layernorm quantize past 32 bits", rowwise)
+        qz, _, _ = ops.fp8_layernorm_quantize(x, wd, bd, rowwise=rowwise)
+        torch.cuda.synchronize()
+        v = G.host(want)
+        s = G.host(qz.scale)[-16:] if rowwise else G.host(qz.scale)
+        st = G.host(qz.scale_t)
+        f = oracle.bf16_to_f32(v)
+        q = oracle.e4m3_encode((f * (s[:, None] if rowwise else s)).astype(np.float32).ravel())
+        qt = oracle.e4m3_encode((f * st).astype(np.float32).ravel())
+        assert np.array_equal(G.host(qz.q[-16:]).ravel(), q)
+        assert np.array_equal(G.host(qz.qt[:, -16:].contiguous()).T.ravel(), qt)
+        del qz
