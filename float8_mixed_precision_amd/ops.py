@@ -392,10 +392,16 @@ def _checked(device, *tensors) -> None:
 _NO_GUARD = contextlib.nullcontext()
 
 
-def _on_device(device):
+def _on_device(device, stream=None):
     """Makes `device` current around a call: a default stream belongs to the
-    current device."""
-    if device.type != "cuda" or device.index == torch.cuda.current_device():
+    current device.  With `stream` (given where the call allocates) that stream
+    is current too, so that a workspace which the call lets go of is reused
+    in that stream's order."""
+    if device.type != "cuda":
+        raise ValueError("the tensors must be on a GPU, not on %s" % device)
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if device.index == torch.cuda.current_device():
         return _NO_GUARD
     return torch.cuda.device(device)
 
@@ -447,7 +453,8 @@ def fp8_layernorm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     _checked(dev, ("x", x, xd, x.shape), ("weight", weight, pd, (cols,)),
              ("bias", bias, pd, (cols,)), ("y", y, xd, x.shape), ("mean", mean, f32, (rows,)),
              ("rstd", rstd, f32, (rows,)))
-    with _on_device(dev):
+    given = y is not None and rstd is not None and (rms or mean is not None)
+    with _on_device(dev, None if given else stream):
         if y is None:
             y = torch.empty_like(x)
         if mean is None and not rms:
@@ -480,25 +487,30 @@ def fp8_layernorm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = Non
     ns, nst = (rows, cols) if rowwise else (1, 1)
     na = rows if not transposed else rows + cols if rowwise else 1
     dev = x.device
-    if out is None:
-        if transposed:
-            out = alloc_quantized(rows, cols, rowwise, dev)
-        else:
-            out = Quantized(torch.empty((rows, cols), dtype=u8, device=dev), None,
-                            torch.empty(rows, dtype=f32, device=dev), None,
-                            torch.empty(rows, dtype=f32, device=dev))
-    if transposed or want_stats:
-        if mean is None and not rms:
-            mean = torch.empty(rows, dtype=f32, device=dev)
-        if rstd is None:
-            rstd = torch.empty(rows, dtype=f32, device=dev)
     _checked(dev, ("x", x, bf, x.shape), ("weight", weight, pd, (cols,)),
              ("bias", bias, pd, (cols,)), ("y", y, bf, x.shape), ("mean", mean, f32, (rows,)),
-             ("rstd", rstd, f32, (rows,)), ("q", out.q, u8, (rows, cols)),
-             ("scale", out.scale, f32, (ns,)), ("amax", out.amax, f32, (na,)))
-    if transposed:
-        _checked(dev, ("qt", out.qt, u8, (cols, rows)), ("scale_t", out.scale_t, f32, (nst,)))
-    with _on_device(dev):
+             ("rstd", rstd, f32, (rows,)))
+    if out is not None:
+        _checked(dev, ("q", out.q, u8, (rows, cols)), ("scale", out.scale, f32, (ns,)),
+                 ("amax", out.amax, f32, (na,)))
+        if transposed:
+            _checked(dev, ("qt", out.qt, u8, (cols, rows)), ("scale_t", out.scale_t, f32, (nst,)))
+    want_stats = want_stats or transposed
+    given = (out is not None and (not transposed or workspace is not None)
+             and (not want_stats or (rstd is not None and (rms or mean is not None))))
+    with _on_device(dev, None if given else stream):
+        if out is None:
+            if transposed:
+                out = alloc_quantized(rows, cols, rowwise, dev)
+            else:
+                out = Quantized(torch.empty((rows, cols), dtype=u8, device=dev), None,
+                                torch.empty(rows, dtype=f32, device=dev), None,
+                                torch.empty(rows, dtype=f32, device=dev))
+        if want_stats:
+            if mean is None and not rms:
+                mean = torch.empty(rows, dtype=f32, device=dev)
+            if rstd is None:
+                rstd = torch.empty(rows, dtype=f32, device=dev)
         if transposed and workspace is None:
             workspace = alloc_layernorm_workspace(rows, cols, dev, rowwise)
         _check(lib().fp8_layernorm_quantize(
@@ -524,7 +536,10 @@ def fp8_layernorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.
     _checked(dev, ("x", x, xd, x.shape), ("dy", dy, xd, x.shape), ("weight", weight, pd, (cols,)),
              ("mean", mean, f32, (rows,)), ("rstd", rstd, f32, (rows,)), ("dx", dx, xd, x.shape),
              ("dweight", dweight, f32, (cols,)), ("dbias", dbias, f32, (cols,)))
-    with _on_device(dev):
+    given = ((dx is not None or not want_x) and (dweight is not None or not want_w)
+             and (dbias is not None or not want_b)
+             and (workspace is not None or not (want_w or want_b)))
+    with _on_device(dev, None if given else stream):
         if want_x and dx is None:
             dx = torch.empty_like(x)
         if want_w and dweight is None:
@@ -590,7 +605,8 @@ def fp8_gated_fwd(xq: torch.Tensor, sx: torch.Tensor, w1q: torch.Tensor, sw1: to
              ("h", h, bf, (M, H)))
     if out is not None:
         _checked(dev, *_quantized("h", out, M, H, rowwise))
-    with _on_device(dev):
+    given = h is not None and (out is None or workspace is not None)
+    with _on_device(dev, None if given else stream):
         if h is None:
             h = torch.empty((M, H), dtype=bf, device=dev)
         if out is not None and workspace is None:
@@ -618,7 +634,8 @@ def fp8_gated_bwd(dyq: torch.Tensor, sdy: torch.Tensor, w2tq: torch.Tensor, sw2t
     for name, z in (("da", qa), ("db", qb)):
         if z is not None:
             _checked(dev, *_quantized(name, z, M, H, rowwise))
-    with _on_device(dev):
+    given = not any(t is None for t in (da, db, qa, qb, workspace))
+    with _on_device(dev, None if given else stream):
         da = torch.empty((M, H), dtype=bf, device=dev) if da is None else da
         db = torch.empty((M, H), dtype=bf, device=dev) if db is None else db
         qa = alloc_quantized(M, H, rowwise, dev) if qa is None else qa

@@ -107,7 +107,12 @@ def test_binding_refusals():
         lambda: E.fp8_gated_bwd(x, s, w, s, ab, ab.float()),
         lambda: E.fp8_gated_bwd(x, s, w, s, ab, ab, qa=E.alloc_quantized(16, 32, True, "cpu")),
     ]
+    good = [lambda: E.fp8_gated_fwd(x, s, w, s, w, s),
+            lambda: E.fp8_gated_bwd(x, s, w, s, ab, ab)]
     for k, call in enumerate(bad):
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match="must be (a|both|dense)|rowwise|dense") as e:
             call()
-            print("call %d was accepted" % k)
+        print(k, e.value)
+    for call in good:                    # nothing wrong but the device
+        with pytest.raises(ValueError, match="on a GPU"):
+            call()

@@ -367,3 +367,20 @@ def test_offsets_past_32_bits():
         assert np.array_equal(G.host(qz.q[-16:]).ravel(), q)
         assert np.array_equal(G.host(qz.qt[:, -16:].contiguous()).T.ravel(), qt)
         del qz
+
+
+def test_given_stream_allocating():
+    """A stream given to calls that allocate their outputs and workspaces."""
+    x, w, b, dy = (t.to(G.DEV) for t in _make(64, 1040, BF, BF, 12))
+    G.say("layernorm given stream")
+    want = ops.fp8_layernorm_quantize(x, w, b)
+    grads = ops.fp8_layernorm_bwd(dy, x, w, want[1], want[2])
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    got = ops.fp8_layernorm_quantize(x, w, b, stream=st)
+    y, _, _ = ops.fp8_layernorm_fwd(x, w, b, stream=st)
+    again = ops.fp8_layernorm_bwd(dy, x, w, got[1], got[2], stream=st)
+    st.synchronize()
+    assert torch.equal(got[0].q, want[0].q) and torch.equal(got[0].qt, want[0].qt)
+    assert all(torch.equal(p, q) for p, q in zip(grads, again))
+    assert torch.equal(ops.fp8_linear_quantize(y).q, want[0].q)

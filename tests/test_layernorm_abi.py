@@ -135,7 +135,12 @@ def test_binding_refusals():
         lambda: E.fp8_layernorm_bwd(x, x, w, r.double(), r),
         lambda: E.fp8_layernorm_bwd(x, x, w, r, r, dweight=torch.zeros(32, dtype=bf)),
     ]
+    good = [lambda: E.fp8_layernorm_fwd(x, w, w), lambda: E.fp8_layernorm_quantize(x, w),
+            lambda: E.fp8_layernorm_bwd(x, x, w, r, r)]
     for k, call in enumerate(bad):
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match="must be (a|both|dense)|rowwise|dense") as e:
             call()
-            print("call %d was accepted" % k)
+        print(k, e.value)
+    for call in good:                    # nothing wrong but the device
+        with pytest.raises(ValueError, match="on a GPU"):
+            call()
