@@ -18,10 +18,10 @@
 // k_gate_tile, one tile of 64 rows x 64 columns of h (128 of da and db) per
 // workgroup.
 //
-// Few tokens (one MFMA block, 16) and H too small for the tiles to cover the
-// compute units: k_gated_skinny.  The time is that of reading W1 and W3 once.  A workgroup owns 16 columns of h, its 8 waves
-// split the contraction and join through LDS; weights go straight from memory
-// to the MFMA operands (no byte of them is used twice), x comes from L2.
+// Few tokens (at most one MFMA block, few_tokens): k_gated_skinny.  The time is
+// that of reading W1 and W3 once.  A workgroup owns 16 columns of h, its 8
+// waves split the contraction and join through LDS; weights go straight from
+// memory to the MFMA operands (no byte of them is used twice), x comes from L2.
 //
 // Part of gemm.hip (included at its end).
 #pragma once

@@ -199,7 +199,7 @@ static_assert(sizeof(GemmGroup) <= 4096, "kernel arguments");
 //             128 rows of B2, dealt so that every wave's 128 slab rows are 64
 //             of each, for the same columns.  A wave's accumulators j and
 //             j + 4 are then a and b of the same elements and the gate needs
-//             no exchange.  C receives h.
+//             no exchange.  C receives h.  EPI_GATE_AB: a and b are stored too.
 //  EPI_DGATE  the gradient through the gate: with dh = A B^T (rounded to
 //             bf16, as the plain GEMM writes it) and the forward pass's a and
 //             b read where the tile is finished, C receives
@@ -210,7 +210,6 @@ static_assert(sizeof(GemmGroup) <= 4096, "kernel arguments");
 // rowpart[o][slice][M] and the column maxima over its rows in
 // colpart[o][slice][N], one slice per wave column / wave row of the tiles
 // (EPI_DGATE takes them always).
-//  EPI_GATE_AB is EPI_GATE with a and b stored.
 constexpr int EPI_NONE = 0, EPI_GATE = 1, EPI_GATE_AB = 2, EPI_DGATE = 3;
 constexpr bool is_gate(int epi) { return epi == EPI_GATE || epi == EPI_GATE_AB; }
 struct GateArgs : GemmGroup {
@@ -232,10 +231,9 @@ struct ArgsOf<EPI_NONE> {
 };
 
 // silu(x) = x s and silu'(x) = s + x s (1 - s), s = 1 / (1 + e^-x), in fp32
-// with the hardware exponential and reciprocal (1 ulp each).  The exponent's
-// product -x log2(e) is rounded once, which the exponential turns into a
-// relative error of |x| 2^-24: s and silu are within (|x| + 4) 2^-23 of exact,
-// relatively (below x = -87, where s leaves the normal range, silu may be
+// with the hardware exponential and reciprocal (1 ulp each).  The roundings of
+// log2(e) and of the exponent x log2(e) become a relative error of at most |x|
+// 2^-23 in e^-x: s and silu are within (|x| + 4) 2^-23 of exact, relatively (below x = -87, where s leaves the normal range, silu may be
 // flushed to 0: absolute error under 2^-119).  The table of exact values that
 // the elementwise kernels use (swiglu.hip) would not fit beside the operand
 // stages in LDS; both round to the same bf16 except where the value lies that
