@@ -116,6 +116,25 @@ int check_norm(int64_t rows, int64_t cols, int kind, int dtype, int pdtype) {
   return FP8L_OK;
 }
 
+// A buffer of a call (none where p is NULL).
+struct Span {
+  const void *p;
+  int64_t bytes;
+};
+
+// Whether one of the outputs spans[0..outs) meets another of the n spans.
+template <int N>
+bool overlapping(const Span (&spans)[N], int outs) {
+  for (int i = 0; i < outs; ++i)
+    for (int j = i + 1; j < N; ++j) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(spans[i].p);
+      const uintptr_t b = reinterpret_cast<uintptr_t>(spans[j].p);
+      if (a && b && a < b + (uintptr_t)spans[j].bytes && b < a + (uintptr_t)spans[i].bytes)
+        return true;
+    }
+  return false;
+}
+
 bool bad_eps(float eps) { return !(eps >= 0.f && eps <= 3.402823466e38f); }
 
 }  // namespace
@@ -383,6 +402,10 @@ int fp8_gated_fwd(const void *xq, const float *sx, const void *w1q, const float 
     if (workspace_bytes < fp8l::gated_workspace_bytes(M, H, scaling)) return FP8L_EWORKSPACE;
     if (misaligned(workspace)) return FP8L_EALIGN;
   }
+  const int64_t mh = M * H;
+  const Span spans[] = {{a, 2 * mh}, {b, 2 * mh}, {h, 2 * mh}, {hq, mh}, {hqt, mh},
+                        {xq, M * K}, {w1q, H * K}, {w3q, H * K}};
+  if (overlapping(spans, 5)) return FP8L_EINVAL;
   const fp8l::Fp8Out o = {hq, hqt, scale, scale_t, amax_out};
   hipError_t e = fp8l::gated_fwd_launch(
       static_cast<const uint8_t *>(xq), sx, static_cast<const uint8_t *>(w1q), sw1,
@@ -410,6 +433,10 @@ int fp8_gated_bwd(const void *dyq, const float *sdy, const void *w2tq, const flo
   if (!workspace) return FP8L_EINVAL;
   if (workspace_bytes < fp8l::gated_workspace_bytes(M, H, scaling)) return FP8L_EWORKSPACE;
   if (misaligned(a) || misaligned(b) || misaligned(workspace)) return FP8L_EALIGN;
+  const int64_t mh = M * H;
+  const Span spans[] = {{da, 2 * mh}, {db, 2 * mh}, {daq, mh}, {daqt, mh}, {dbq, mh}, {dbqt, mh},
+                        {a, 2 * mh}, {b, 2 * mh}, {dyq, M * D}, {w2tq, H * D}};
+  if (overlapping(spans, 6)) return FP8L_EINVAL;
   const fp8l::Fp8Out qa = {daq, daqt, da_scale, da_scale_t, da_amax};
   const fp8l::Fp8Out qb = {dbq, dbqt, db_scale, db_scale_t, db_amax};
   hipError_t e = fp8l::gated_bwd_launch(
@@ -434,6 +461,9 @@ int fp8_layernorm_fwd(const void *x, int64_t rows, int64_t cols, int kind, int d
   if (misaligned(x) || misaligned(weight) || misaligned(bias) || misaligned(y) ||
       misaligned4(mean) || misaligned4(rstd))
     return FP8L_EALIGN;
+  const int64_t bytes = rows * cols * (dtype == FP8L_F32 ? 4 : 2);
+  const Span spans[] = {{y, bytes}, {mean, 4 * rows}, {rstd, 4 * rows}, {x, bytes}};
+  if (overlapping(spans, 3)) return FP8L_EINVAL;
   const fp8l::NormIn in = {x, weight, bias, pdtype == FP8L_F32, kind == FP8L_RMSNORM, eps,
                            rows, cols};
   hipError_t e = fp8l::norm_fwd_launch(in, dtype == FP8L_F32, y, mean, rstd,
@@ -469,14 +499,19 @@ int fp8_layernorm_quantize(const void *x, int64_t rows, int64_t cols, int kind,
   const fp8l::NormIn in = {x, weight, bias, pdtype == FP8L_F32, kind == FP8L_RMSNORM, eps,
                            rows, cols};
   hipStream_t st = static_cast<hipStream_t>(stream);
-  hipError_t e;
-  if (rows_only) {
-    e = fp8l::norm_rows_launch(in, y, mean, rstd, q, scale, amax_out, st);
-  } else {
+  if (!rows_only) {
     if (rw && !scale_t) return FP8L_OK;          // no rows, no column scales wanted
     if (!workspace) return FP8L_EINVAL;
     if (workspace_bytes < fp8l::norm_workspace_bytes(rows, cols, scaling)) return FP8L_EWORKSPACE;
     if (misaligned(workspace)) return FP8L_EALIGN;
+  }
+  const Span spans[] = {{y, 2 * rows * cols}, {q, rows * cols}, {qt, rows * cols},
+                        {mean, 4 * rows}, {rstd, 4 * rows}, {x, 2 * rows * cols}};
+  if (overlapping(spans, 5)) return FP8L_EINVAL;
+  hipError_t e;
+  if (rows_only) {
+    e = fp8l::norm_rows_launch(in, y, mean, rstd, q, scale, amax_out, st);
+  } else {
     e = fp8l::norm_quantize_launch(in, scaling, y, mean, rstd,
                                    {q, qt, scale, scale_t, amax_out}, workspace, st);
   }
@@ -501,6 +536,10 @@ int fp8_layernorm_bwd(const void *dy, const void *x, const void *weight, const f
       return FP8L_EWORKSPACE;
     if (misaligned(workspace)) return FP8L_EALIGN;
   }
+  const int64_t bytes = rows * cols * (dtype == FP8L_F32 ? 4 : 2);
+  const Span spans[] = {{dx, bytes}, {dweight, 4 * cols}, {dbias, 4 * cols}, {dy, bytes},
+                        {x, bytes}, {mean, 4 * rows}, {rstd, 4 * rows}};
+  if (overlapping(spans, 3)) return FP8L_EINVAL;
   const fp8l::NormIn in = {x, weight, nullptr, pdtype == FP8L_F32, kind == FP8L_RMSNORM, 0.f,
                            rows, cols};
   hipError_t e = fp8l::norm_bwd_launch(dy, in, dtype == FP8L_F32, mean, rstd, dx, dweight, dbias,

@@ -380,7 +380,8 @@ FP8L_API int fp8_swiglu_bwd(const void *dh, const void *a, const void *b, int64_
  * fp8_linear_fwd.  The order of the fp32 additions depends on M and H (calls of
  * up to 16 tokens may split the contraction over a workgroup's waves); equal calls
  * give equal bits.  The workspace's contents are undefined on entry and exit,
- * not shared by calls in flight together.
+ * not shared by calls in flight together.  Outputs must not overlap inputs or
+ * one another (FP8L_EINVAL for the matrices).
  */
 FP8L_API size_t fp8_gated_workspace_bytes(int64_t M, int64_t H, int scaling);
 FP8L_API int fp8_gated_fwd(const void *xq, const float *sx, const void *w1q, const float *sw1,
@@ -401,7 +402,7 @@ FP8L_API int fp8_gated_fwd(const void *xq, const float *sx, const void *w1q, con
  *           fp8_swiglu_bwd
  *   scaling FP8L_TENSORWISE or FP8L_ROWWISE, optionally | FP8L_E5M2 (dyq and
  *           the codes of da and db)
- * M, H and D are multiples of 16.
+ * M, H and D are multiples of 16.  Workspace and overlaps as above.
  */
 FP8L_API int fp8_gated_bwd(const void *dyq, const float *sdy, const void *w2tq,
                            const float *sw2t, const void *a, const void *b, int64_t M, int64_t H,
@@ -419,7 +420,9 @@ FP8L_API int fp8_gated_bwd(const void *dyq, const float *sdy, const void *w2tq,
  *   y[r][c] = (x[r][c] - mean) rstd w[c] + b[c]
  *
  * computed in fp32 (the variance about the mean) and rounded once to y's
- * type.  A row that holds a NaN or an infinity gives NaN in that row only.
+ * type.  A row that holds a NaN or an infinity gives NaN in that row only.  Sums
+ * past the fp32 range are infinities: squares that add up to 2^128 or more give
+ * rstd = 0, a sum of x that does gives NaN; squares below 2^-149 count as 0.
  *
  *   kind      FP8L_LAYERNORM or FP8L_RMSNORM
  *   dtype     FP8L_BF16 or FP8L_F32: type of x and y (and dy, dx)
@@ -432,7 +435,8 @@ FP8L_API int fp8_gated_bwd(const void *dyq, const float *sdy, const void *w2tq,
  * Norms take any number of rows, and any 1 <= cols <= FP8L_NORM_MAX_COLS
  * except where codes are written (multiples of 16): FP8L_ESHAPE otherwise.
  * x, y, dy, dx, weight and bias need 16-byte alignment, as every tensor.
- * Outputs must not overlap inputs or one another.  The order of the fp32
+ * Outputs must not overlap inputs or one another (FP8L_EINVAL for the
+ * matrices, mean, rstd and the gradients).  The order of the fp32
  * additions within a row depends on cols and on the number of rows; equal
  * calls give equal bits.
  */
@@ -466,7 +470,8 @@ FP8L_API int fp8_layernorm_fwd(const void *x, int64_t rows, int64_t cols, int ki
  *        serving; amax_out is then [rows], any number of rows is valid, the
  *        workspace is not used (it may be NULL), and y, mean and rstd are
  *        all optional
- * With qt, rows is a multiple of 16; cols always is.
+ * With qt, rows is a multiple of 16; cols always is.  The workspace's contents
+ * are undefined on entry and exit, not shared by calls in flight together.
  */
 FP8L_API int fp8_layernorm_quantize(const void *x, int64_t rows, int64_t cols, int kind,
                                     const void *weight, const void *bias, int pdtype, float eps,

@@ -116,3 +116,19 @@ def test_binding_refusals():
     for call in good:                    # nothing wrong but the device
         with pytest.raises(ValueError, match="on a GPU"):
             call()
+
+
+@no_gpu
+def test_overlapping_buffers():
+    at = lambda k: A + k * 4096                 # disjoint places
+    apart = dict(x=at(0), w1=at(1), w3=at(2), a=at(3), b=at(4), h=at(5), hq=at(6), hqt=at(7))
+    for one in ("a", "b", "h", "hq", "hqt"):
+        for other in apart:
+            if other != one:
+                assert fwd(**dict(apart, **{one: apart[other]})) == E.FP8L_EINVAL
+    apart = dict(dy=at(0), w=at(1), a=at(2), b=at(3), da=at(4), db=at(5), daq=at(6), daqt=at(7),
+                 dbq=at(8), dbqt=at(9))
+    for one in ("da", "db", "daq", "daqt", "dbq", "dbqt"):
+        for other in apart:
+            if other != one:
+                assert bwd(**dict(apart, **{one: apart[other]})) == E.FP8L_EINVAL

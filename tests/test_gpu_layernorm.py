@@ -175,7 +175,7 @@ def test_offset_row(offset):
 
 def test_constant_zero_and_nonfinite_rows():
     """A constant row normalizes to the bias, an infinity or a NaN stays in
-    its own row, and values near the type's limits do not overflow the mean."""
+    its own row."""
     cols = 1200
     x = torch.randn((6, cols), generator=torch.Generator().manual_seed(2))
     x[1] = 3.0
@@ -196,6 +196,29 @@ def test_constant_zero_and_nonfinite_rows():
         for r in (0, 5):
             tol = want[5][r] + _half(dtype) * (np.abs(want[2][r]) + want[5][r])
             assert np.all(np.abs(_d(y[r]) - want[2][r]) <= tol)
+
+
+@pytest.mark.parametrize("cols", [7, 1200, 4098])
+def test_sums_past_the_range(cols):
+    """Squares that add up past fp32 give rstd = 0 (y is the bias), a sum of x
+    past it NaN; squares below the range count as 0; the rows beside them are
+    as ever."""
+    x = torch.randn((6, cols), generator=torch.Generator().manual_seed(3))
+    sign = torch.where(torch.arange(cols) % 2 == 0, 1.0, -1.0)
+    x[0], x[1], x[2] = 1e20 * sign, 3e38, 1e-30 * sign
+    w = torch.full((cols,), 2.0)
+    b = torch.full((cols,), 0.5)
+    G.say("layernorm range %d" % cols)
+    for rms in (False, True):
+        y, mean, rstd = ops.fp8_layernorm_fwd(x.to(G.DEV), w.to(G.DEV), b.to(G.DEV), EPS, rms)
+        torch.cuda.synchronize()
+        y, rstd = y.cpu(), rstd.cpu()
+        assert rstd[0] == 0 and torch.all(y[0] == 0.5)
+        assert torch.all(y[1] == 0.5) if rms else torch.isnan(y[1]).all()
+        # 2 x / sqrt(EPS) is far below half a step of 0.5
+        assert abs(float(rstd[2]) * EPS ** 0.5 - 1) < 2.0 ** -20 and torch.all(y[2] == 0.5)
+        want = _forward64(x[3:], w, b, rms)
+        assert np.all(np.abs(_d(y[3:]) - want[2]) <= want[5] + U * (np.abs(want[2]) + want[5]))
 
 
 def _hq(qz):

@@ -144,3 +144,23 @@ def test_binding_refusals():
     for call in good:                    # nothing wrong but the device
         with pytest.raises(ValueError, match="on a GPU"):
             call()
+
+
+@no_gpu
+def test_overlapping_buffers():
+    n = 16 * 32
+    at = lambda k: A + k * 4096                 # disjoint places for [16, 32]
+    for y in (at(0), at(0) - 64, at(0) + 2 * n - 16):
+        assert fwd(x=at(0), rows=16, cols=32, y=y, mean=at(2), rstd=at(3)) == E.FP8L_EINVAL
+    assert fwd(x=at(0), rows=16, cols=32, y=at(1), mean=at(1), rstd=at(3)) == E.FP8L_EINVAL
+    apart = dict(x=at(0), mean=at(1), rstd=at(2), q=at(3), qt=at(4), y=at(5))
+    for one in ("mean", "rstd", "q", "qt", "y"):
+        for other in apart:
+            if other != one:
+                assert quant(**dict(apart, **{one: apart[other]})) == E.FP8L_EINVAL
+    apart = dict(rows=16, cols=32, dy=at(0), x=at(1), mean=at(2), rstd=at(3), dx=at(4), dw=at(5),
+                 db=at(6))
+    for one in ("dx", "dw", "db"):
+        for other in ("dy", "x", "mean", "rstd", "dx", "dw", "db"):
+            if other != one:
+                assert bwd(**dict(apart, **{one: apart[other]})) == E.FP8L_EINVAL
