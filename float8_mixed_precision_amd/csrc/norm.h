@@ -13,9 +13,8 @@
 // digits.  x is read once per pass.
 //
 // Bound: HBM.  A row (or the share of one) sits in registers between the
-// reductions; TPR threads work on a row: one wave for short rows or where
-// there are many (no barrier, reductions by DPP), 256 or 1024 threads for
-// long rows or few (with_shape).
+// reductions; TPR threads work on a row: one wave for up to 512 columns (no
+// barrier, reductions by DPP), 128 to 1024 threads for more (with_shape).
 //
 // The quantize forms need y only as fp8 codes.  Per-token codes (no
 // transposed copy) come out of the same pass, since a row's amax is known
@@ -327,11 +326,11 @@ constexpr int block_threads() {
 // the same number of rounds (a row past the end is computed on row rows - 1
 // and not stored).
 //
-// Measured, statistics and maxima of 8192 x 4096 bf16 (tensorwise): 16.6 us,
-// 4.0 TB/s, the rate at which this card reads a large array, with 256 threads a
-// row and 2048 workgroups; with a wave a row 30 us (its w and b take 128
-// registers, or twice the traffic of x when read per row: 29 us), 512 threads
-// 19 us, two rows a round 17-21 us.
+// Measured, statistics and maxima of 8192 x 4096 bf16 (tensorwise): 17.3 us,
+// 3.9 TB/s (this card reads a large array at 4.0), with 256 threads a row and
+// 2048 workgroups; with 512 threads 19.3 us; earlier forms of this kernel with a
+// wave a row 30 us (its w and b take 128 registers, or twice the traffic of x
+// when read per row: 29 us), two rows a round 25 against 18.6.
 template <class T, int LAY, int TPR, int CH, int MODE>
 __global__ __launch_bounds__((block_threads<TPR, MODE>())) void k_norm(NormArgs p) {
   constexpr int G = block_threads<TPR, MODE>() / TPR;
@@ -704,32 +703,37 @@ constexpr int kComputeUnits = 256;
 constexpr int kMaxSlices = kComputeUnits;
 
 // Calls f with a pass's kernel shape (TPR, CH) for `cols` columns: 8 columns a
-// thread, or 16 (`wide`; and always for the widest rows).
-template <class F>
+// thread, or 16 (`wide`, where WIDE allows it; and always for the widest rows).
+template <bool WIDE, class F>
 hipError_t with_shape(int cols, bool wide, F f) {
 #define FP8L_SHAPE(TPR, CH)                                                  \
   if (cols <= (TPR) * 8 * (CH))                                              \
     return f(std::integral_constant<int, TPR>(), std::integral_constant<int, CH>());
   FP8L_SHAPE(64, 1)
-  if (wide) {
-    FP8L_SHAPE(64, 2)
-    FP8L_SHAPE(128, 2)
-    FP8L_SHAPE(256, 2)
-    FP8L_SHAPE(512, 2)
-  } else {
-    FP8L_SHAPE(128, 1)
-    FP8L_SHAPE(256, 1)
-    FP8L_SHAPE(512, 1)
-    FP8L_SHAPE(1024, 1)
-  }
+  if constexpr (WIDE)
+    if (wide) {
+      FP8L_SHAPE(64, 2)
+      FP8L_SHAPE(128, 2)
+      FP8L_SHAPE(256, 2)
+      FP8L_SHAPE(512, 2)
+    }
+  FP8L_SHAPE(128, 1)
+  FP8L_SHAPE(256, 1)
+  FP8L_SHAPE(512, 1)
+  FP8L_SHAPE(1024, 1)
   FP8L_SHAPE(1024, 2)
 #undef FP8L_SHAPE
   return hipErrorInvalidValue;
 }
 
-// The forward takes 16 columns a thread where there are at least 4 rows for
-// every compute unit: one row of 4096 takes 3.9 us with 256 threads, 3.0 with
-// 512; 8192 rows 16.6 against 19.
+// The forward of bf16 rows takes 16 columns a thread where there are at least 4
+// rows for every compute unit.  Measured, 16 columns against 8, us.  Per-token
+// codes: 256 x 4096 4.1 / 3.7, 1024 x 4096 5.6 / 6.0, 4096 x 4096 14.9 / 16.5,
+// 4096 x 8192 25.5 / 27.4; quantize rowwise 1024 x 4096 19.0 / 18.6, 4096 x 4096
+// 33.3 / 34.5, 16384 x 4096 84.5 / 95.3; tensorwise 2048 x 4096 16.0 / 15.2, 16384 x
+// 4096 66.7 / 72.1; y alone 4096 x 4096 13.3 / 12.5, 16384 x 4096 43.5 / 43.1.  (One
+// rule for all of them, since their y is to be the same bits.)  fp32 rows take
+// 8: 2048 x 4096 16.1 / 13.6, 4096 x 4096 24.0 / 22.1, more rows within 3%.
 bool many_rows(int64_t rows) { return rows >= 4 * kComputeUnits; }
 
 template <class T, int LAY, int MODE>
@@ -750,7 +754,7 @@ hipError_t launch_norm(const NormArgs &a, int64_t max_blocks, int *blocks, hipSt
   if constexpr (LAY == LAY_SCALAR)
     return launch(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
   else
-    return with_shape(a.cols, many_rows(a.rows), launch);
+    return with_shape<sizeof(T) == 2>(a.cols, many_rows(a.rows), launch);
 }
 
 template <class T, int LAY>
@@ -767,7 +771,7 @@ hipError_t launch_bwd(const NormBwdArgs &a, int *blocks, hipStream_t stream) {
   if constexpr (LAY == LAY_SCALAR)
     return launch(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
   else
-    return with_shape(a.cols, false, launch);
+    return with_shape<false>(a.cols, false, launch);
 }
 
 // f(LAY) for a width
