@@ -233,11 +233,12 @@ struct ArgsOf<EPI_NONE> {
 // silu(x) = x s and silu'(x) = s + x s (1 - s), s = 1 / (1 + e^-x), in fp32
 // with the hardware exponential and reciprocal (1 ulp each).  The roundings of
 // log2(e) and of the exponent x log2(e) become a relative error of at most |x|
-// 2^-23 in e^-x: s and silu are within (|x| + 4) 2^-23 of exact, relatively (below x = -87, where s leaves the normal range, silu may be
-// flushed to 0: absolute error under 2^-119).  The table of exact values that
-// the elementwise kernels use (swiglu.hip) would not fit beside the operand
-// stages in LDS; both round to the same bf16 except where the value lies that
-// close to a rounding border.
+// 2^-23 in e^-x: s and silu are within (|x| + 4) 2^-23 of exact, relatively
+// (below x = -87, where s leaves the normal range, silu may be flushed to 0:
+// absolute error under 2^-119).  The table of exact values that the elementwise
+// kernels use (swiglu.hip) would not fit beside the operand stages in LDS; both
+// round to the same bf16 except where the value lies that close to a rounding
+// border.
 __device__ __forceinline__ float gate_sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.44269504088896341f));
 }
