@@ -330,7 +330,7 @@ constexpr int block_threads() {
 // 3.9 TB/s (this card reads a large array at 4.0), with 256 threads a row and
 // 2048 workgroups; with 512 threads 19.3 us; earlier forms of this kernel with a
 // wave a row 30 us (its w and b take 128 registers, or twice the traffic of x
-// when read per row: 29 us), two rows a round 25 against 18.6.
+// when read per row: 29 us), two rows a round 17-21 against 16.6 side by side.
 template <class T, int LAY, int TPR, int CH, int MODE>
 __global__ __launch_bounds__((block_threads<TPR, MODE>())) void k_norm(NormArgs p) {
   constexpr int G = block_threads<TPR, MODE>() / TPR;

@@ -7,6 +7,7 @@
 //   rowwise:
 //   1. k_amax_partial  : one read pass; per-tile row / column maxima
 //   2. k_finalize_rowwise: reduce the partials, one scale per row / column
+//                        (small matrices: in k_cast_transpose, scales_in_cast)
 //   both:
 //   3. k_cast_transpose: second read pass; writes q (row-major) directly and
 //                        qt (the transpose) through an LDS tile
@@ -288,7 +289,15 @@ __global__ __launch_bounds__(256) void k_finalize_rowwise(FinalizeJob job0, Fina
 // FMT: 0 = E4M3 codes, 1 = E5M2 codes (scale onto 57344).
 // NORM: x is normalized on the way (nm: the layer norm's parameters and
 // statistics), so that a norm whose y nobody else reads is not written out.
-constexpr int MODE_TW = 0, MODE_RW = 1, MODE_GIVEN = 2;
+// MODE_RP: rowwise; each workgroup takes the maxima of its own 128 rows and 128
+// columns from the partial maxima (rp), in place of k_finalize_rowwise; the
+// first tile of a row of tiles stores the row scales, of a column of tiles the
+// column scales.
+constexpr int MODE_TW = 0, MODE_RW = 1, MODE_GIVEN = 2, MODE_RP = 3;
+struct RowParts {
+  const uint16_t *row, *col;
+  int row_slices, col_slices;
+};
 struct CastNorm {
   const void *w, *b;
   int wf32;
@@ -318,7 +327,8 @@ __device__ __forceinline__ void cast_tile(
     const uint16_t *__restrict__ x, int rows, int cols, int tiles_c,
     float *__restrict__ scale, float *__restrict__ scale_t,
     const uint32_t *__restrict__ part, int nparts, float *__restrict__ amax_out,
-    uint8_t *__restrict__ q, uint8_t *__restrict__ qt, const CastNorm &nm) {
+    uint8_t *__restrict__ q, uint8_t *__restrict__ qt, const CastNorm &nm,
+    const RowParts &rp) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[CT_T * CT_T];
   const int tid = threadIdx.x;
   // block -> (tile_r, tile_c): groups of CT_GROUP row tiles (the last one
@@ -336,16 +346,53 @@ __device__ __forceinline__ void cast_tile(
   const int rg = tid >> 4;
   const int c = c0 + c8 * 8;
   const bool col_ok = c < cols;
-  constexpr bool ROWWISE = MODE == MODE_RW;
+  constexpr bool ROWWISE = MODE == MODE_RW || MODE == MODE_RP;
+
+  __shared__ float rps[MODE == MODE_RP ? 2 * CT_T : 1];   // row, then column scales
+  if constexpr (MODE == MODE_RP) {
+    // 256 outputs, two threads each, 16 loads in flight (index clamped into the
+    // array, value masked)
+    __shared__ uint32_t half[2 * CT_T];
+    const int o = tid & (2 * CT_T - 1), h = tid / (2 * CT_T);
+    const bool is_row = o < CT_T;                     // wave-uniform
+    const int i = is_row ? r0 + o : c0 + o - CT_T;
+    const int n = is_row ? rows : cols;
+    const int T = is_row ? rp.row_slices : rp.col_slices;
+    const uint16_t *__restrict__ pt = is_row ? rp.row : rp.col;
+    const int ic = min(i, n - 1);
+    uint32_t m = 0;
+    for (int t0 = h; t0 < T; t0 += 32) {
+      uint32_t v[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) v[u] = pt[(size_t)min(t0 + 2 * u, T - 1) * n + ic];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) m = max(m, t0 + 2 * u < T ? v[u] : 0u);
+    }
+    if (h == 1) half[o] = m;
+    __syncthreads();
+    if (h == 0) {
+      const float a = bf16_to_f32(max(m, half[o]));
+      const float s = scale_from_amax<FMT>(a);
+      rps[o] = s;
+      if (i < n && (is_row ? tile_c : tile_r) == 0) {
+        (is_row ? scale : scale_t)[i] = s;
+        if (amax_out) amax_out[is_row ? i : rows + i] = a;
+      }
+    }
+    __syncthreads();
+  }
 
   // rowwise scale vectors 16-byte aligned (the interface promises 4): read
   // them as float4, else one float at a time
   const bool vec_scales =
-      ROWWISE && ((reinterpret_cast<uintptr_t>(scale) | reinterpret_cast<uintptr_t>(scale_t)) &
+      MODE == MODE_RW && ((reinterpret_cast<uintptr_t>(scale) | reinterpret_cast<uintptr_t>(scale_t)) &
                   15u) == 0;
   float sc[8];                    // column scales (rowwise) of the 8 columns
   float s_t = 0.f;                // tensor scale
-  if (ROWWISE) {
+  if (MODE == MODE_RP) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sc[j] = rps[CT_T + c8 * 8 + j];
+  } else if (ROWWISE) {
     if (col_ok && vec_scales) {
       const float4 a = *reinterpret_cast<const float4 *>(scale_t + c);
       const float4 b = *reinterpret_cast<const float4 *>(scale_t + c + 4);
@@ -385,7 +432,10 @@ __device__ __forceinline__ void cast_tile(
     if (ok) {
       // the 4 rows' scales (rowwise; r is a multiple of 4)
       float srs[4] = {s_t, s_t, s_t, s_t};
-      if (ROWWISE) {
+      if (MODE == MODE_RP) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) srs[j] = rps[rl + j];
+      } else if (ROWWISE) {
         if (vec_scales) {
           const float4 v = *reinterpret_cast<const float4 *>(scale + r);
           srs[0] = v.x; srs[1] = v.y; srs[2] = v.z; srs[3] = v.w;
@@ -483,9 +533,9 @@ __global__ __launch_bounds__(CT_THREADS) void k_cast_transpose(
     const uint16_t *__restrict__ x, int rows, int cols, int tiles_c,
     float *__restrict__ scale, float *__restrict__ scale_t,
     const uint32_t *__restrict__ part, int nparts, float *__restrict__ amax_out,
-    uint8_t *__restrict__ q, uint8_t *__restrict__ qt, CastNorm nm) {
+    uint8_t *__restrict__ q, uint8_t *__restrict__ qt, CastNorm nm, RowParts rp) {
   cast_tile<MODE, FMT, NORM>(x, rows, cols, tiles_c, scale, scale_t, part, nparts, amax_out, q,
-                             qt, nm);
+                             qt, nm, rp);
 }
 
 // Two tensors of one shape (and one count of partials) in one launch: grid
@@ -497,16 +547,17 @@ struct CastJob {
   const uint32_t *part;
   float *amax_out;
   uint8_t *q, *qt;
+  RowParts rp;
 };
 template <int MODE, int FMT>
 __global__ __launch_bounds__(CT_THREADS) void k_cast_pair(CastJob a, CastJob b, int rows, int cols,
                                                           int tiles_c, int nparts) {
   if (blockIdx.y == 0)
     cast_tile<MODE, FMT, false>(a.x, rows, cols, tiles_c, a.scale, a.scale_t, a.part, nparts,
-                                a.amax_out, a.q, a.qt, CastNorm{});
+                                a.amax_out, a.q, a.qt, CastNorm{}, a.rp);
   else
     cast_tile<MODE, FMT, false>(b.x, rows, cols, tiles_c, b.scale, b.scale_t, b.part, nparts,
-                                b.amax_out, b.q, b.qt, CastNorm{});
+                                b.amax_out, b.q, b.qt, CastNorm{}, b.rp);
 }
 
 // --------------------------------------------------------------- encode --
@@ -559,12 +610,27 @@ size_t quantize_workspace_bytes(int64_t rows, int64_t cols, int scaling) {
 
 namespace {
 
+// Rowwise: whether the cast takes the scales from the partial maxima itself
+// (MODE_RP), which saves the launch between but reads an output's partials once
+// for every tile that needs it.  Measured, in the cast / in a launch of their
+// own, us a quantize: 512 x 512 8.4 / 9.8, 1024 x 4096 10.1 / 11.4 and 2048 x 4096
+// 13.7 / 15.1 (256 and 512 tiles of 32 and 48 partials), 8192 x 1024 16.6 / 16.9
+// (512 of 132), 4096 x 4096 23.4 / 22.9 (1024 of 80), 8192 x 4096 42.2 / 38.3 (2048 of
+// 144); a gated forward of 1024 x 4096 29.4 / 30.4 (256 of 160).  Many partials of one
+// output lose with few tiles too: 128 x 14336 24.4 / 22.9 (112 of 448 + 4).
+bool scales_in_cast(const CastSource &s, int64_t rows, int64_t cols) {
+  const int64_t t = cdiv(rows, CT_T) * cdiv(cols, CT_T);
+  return t > 0 && s.row_slices <= 256 && s.col_slices <= 256 &&
+         t * (s.row_slices + s.col_slices) <= 1 << 16;
+}
+
 template <int FMT, bool NORM>
 hipError_t cast_fmt(const CastSource *src, int count, int64_t rows, int64_t cols, bool rowwise,
                     const Fp8Out *o, hipStream_t stream) {
   const int R = (int)rows, C = (int)cols, l = count - 1;   // l: the last tensor
   const CastNorm nm = {src->w, src->b, src->wf32, src->mean, src->rstd};
-  if (rowwise) {
+  const bool in_cast = rowwise && scales_in_cast(*src, rows, cols);
+  if (rowwise && !in_cast) {
     const int64_t nbr = cdiv(rows, FR_OUT), nbc = cdiv(cols, FR_OUT);
     auto job = [&](int i) {
       return FinalizeJob{src[i].rowpart, src[i].colpart, o[i].scale, o[i].scale_t, o[i].amax};
@@ -573,7 +639,7 @@ hipError_t cast_fmt(const CastSource *src, int count, int64_t rows, int64_t cols
       hipLaunchKernelGGL(k_finalize_rowwise<FMT>, dim3((unsigned)(nbr + nbc), (unsigned)count),
                          dim3(256), 0, stream, job(0), job(l), R, C, src->row_slices,
                          src->col_slices, (int)nbr);
-  } else if (src->nparts == 0) {
+  } else if (!rowwise && src->nparts == 0) {
     for (int i = 0; i < count; ++i)
       hipLaunchKernelGGL(k_finalize_tw_empty<FMT>, dim3(1), dim3(64), 0, stream, o[i].scale,
                          o[i].scale_t, o[i].amax);
@@ -585,11 +651,15 @@ hipError_t cast_fmt(const CastSource *src, int count, int64_t rows, int64_t cols
     const unsigned nb = (unsigned)(ct_r * ct_c);
     auto job = [&](int i) {
       return CastJob{static_cast<const uint16_t *>(src[i].x), o[i].scale, o[i].scale_t, src[i].part,
-                     o[i].amax, static_cast<uint8_t *>(o[i].q), static_cast<uint8_t *>(o[i].qt)};
+                     o[i].amax, static_cast<uint8_t *>(o[i].q), static_cast<uint8_t *>(o[i].qt),
+                     {src[i].rowpart, src[i].colpart, src[i].row_slices, src[i].col_slices}};
     };
     const CastJob j = job(0);
     if (count == 2) {
-      if (rowwise)
+      if (in_cast)
+        hipLaunchKernelGGL((k_cast_pair<MODE_RP, FMT>), dim3(nb, 2), dim3(CT_THREADS), 0, stream,
+                           j, job(1), R, C, (int)ct_c, 0);
+      else if (rowwise)
         hipLaunchKernelGGL((k_cast_pair<MODE_RW, FMT>), dim3(nb, 2), dim3(CT_THREADS), 0, stream,
                            j, job(1), R, C, (int)ct_c, 0);
       else
@@ -598,11 +668,15 @@ hipError_t cast_fmt(const CastSource *src, int count, int64_t rows, int64_t cols
     } else if (!rowwise) {
       hipLaunchKernelGGL((k_cast_transpose<MODE_TW, FMT, NORM>), dim3(nb), dim3(CT_THREADS), 0,
                          stream, j.x, R, C, (int)ct_c, j.scale, j.scale_t, j.part, src->nparts,
-                         j.amax_out, j.q, j.qt, nm);
+                         j.amax_out, j.q, j.qt, nm, j.rp);
+    } else if (in_cast) {
+      hipLaunchKernelGGL((k_cast_transpose<MODE_RP, FMT, NORM>), dim3(nb), dim3(CT_THREADS), 0,
+                         stream, j.x, R, C, (int)ct_c, j.scale, j.scale_t, nullptr, 0, j.amax_out,
+                         j.q, j.qt, nm, j.rp);
     } else {
       hipLaunchKernelGGL((k_cast_transpose<MODE_RW, FMT, NORM>), dim3(nb), dim3(CT_THREADS), 0,
                          stream, j.x, R, C, (int)ct_c, j.scale, j.scale_t, nullptr, 0, nullptr,
-                         j.q, j.qt, nm);
+                         j.q, j.qt, nm, j.rp);
     }
   }
   return hipGetLastError();
@@ -712,7 +786,7 @@ hipError_t quantize_scaled_launch(const void *x, int64_t rows, int64_t cols,
                        dim3(CT_THREADS), 0, stream, static_cast<const uint16_t *>(x), (int)rows,
                        (int)cols, (int)ct_c, const_cast<float *>(scale), nullptr, nullptr, 0,
                        nullptr, static_cast<uint8_t *>(q), static_cast<uint8_t *>(qt),
-                       CastNorm{});
+                       CastNorm{}, RowParts{});
   return hipGetLastError();
 }
 
