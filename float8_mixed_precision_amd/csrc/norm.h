@@ -729,8 +729,8 @@ hipError_t with_shape(int cols, bool wide, F f) {
 // The forward of bf16 rows takes 16 columns a thread where there are at least 4
 // rows for every compute unit.  Measured, 16 columns against 8, us.  Per-token
 // codes: 256 x 4096 4.1 / 3.7, 1024 x 4096 5.6 / 6.0, 4096 x 4096 14.9 / 16.5,
-// 4096 x 8192 25.5 / 27.4; quantize rowwise 1024 x 4096 19.0 / 18.6, 4096 x 4096
-// 33.3 / 34.5, 16384 x 4096 84.5 / 95.3; tensorwise 2048 x 4096 16.0 / 15.2, 16384 x
+// 4096 x 8192 25.5 / 27.4; quantize rowwise 1024 x 4096 0.4 more, 4096 x 4096 1.2
+// less, 16384 x 4096 11 less (83 in all); tensorwise 2048 x 4096 16.0 / 15.2, 16384 x
 // 4096 66.7 / 72.1; y alone 4096 x 4096 13.3 / 12.5, 16384 x 4096 43.5 / 43.1.  (One
 // rule for all of them, since their y is to be the same bits.)  fp32 rows take
 // 8: 2048 x 4096 16.1 / 13.6, 4096 x 4096 24.0 / 22.1, more rows within 3%.

@@ -205,21 +205,23 @@ __global__ __launch_bounds__(AM_THREADS) void k_amax_partial(
 // One scale per row and per column from the partial maxima.  Workgroups
 // [0, nbr) cover 64 rows each (max over tiles_c row partials), the rest 64
 // columns each (max over tiles_r column partials).  Thread (o, sl), o =
-// tid % 64, sl = tid / 64, reduces partials sl, sl + 4, ... of output o with
-// eight loads in flight at a time (index clamped into the array, value
-// masked), and the four slices meet in LDS.  (One thread per output walking
-// its partials serially took as long as the amax pass itself.)
+// tid % 64, sl = tid / 64, reduces partials sl, sl + 8, ... of output o with
+// 16 loads in flight at a time (index clamped into the array, value
+// masked), and the eight slices meet in LDS.  (One thread per output walking
+// its partials serially took as long as the amax pass itself.  4 slices of 8
+// loads: 1 us more at 8192 x 4096, where a column has 128 partials, 2 us more
+// after a norm, where it has 256; 16 slices: the same.)
 constexpr int FR_OUT = 64;
-constexpr int FR_SLICES = 4;
-constexpr int FR_UNROLL = 8;
-static_assert(FR_OUT * FR_SLICES == 256, "one finalize workgroup is 256 threads");
+constexpr int FR_SLICES = 8;
+constexpr int FR_UNROLL = 16;
+constexpr int FR_THREADS = FR_OUT * FR_SLICES;
 // Grid row y finalizes tensor y of a pair (one shape, one count of partials).
 struct FinalizeJob {
   const uint16_t *rowpart, *colpart;
   float *scale, *scale_t, *amax_out;
 };
 template <int FMT>
-__global__ __launch_bounds__(256) void k_finalize_rowwise(FinalizeJob job0, FinalizeJob job1,
+__global__ __launch_bounds__(FR_THREADS) void k_finalize_rowwise(FinalizeJob job0, FinalizeJob job1,
                                                           int rows, int cols, int tiles_c,
                                                           int tiles_r, int nbr) {
   const bool second = blockIdx.y != 0;
@@ -612,16 +614,17 @@ namespace {
 
 // Rowwise: whether the cast takes the scales from the partial maxima itself
 // (MODE_RP), which saves the launch between but reads an output's partials once
-// for every tile that needs it.  Measured, in the cast / in a launch of their
-// own, us a quantize: 512 x 512 8.4 / 9.8, 1024 x 4096 10.1 / 11.4 and 2048 x 4096
-// 13.7 / 15.1 (256 and 512 tiles of 32 and 48 partials), 8192 x 1024 16.6 / 16.9
-// (512 of 132), 4096 x 4096 23.4 / 22.9 (1024 of 80), 8192 x 4096 42.2 / 38.3 (2048 of
-// 144); a gated forward of 1024 x 4096 29.4 / 30.4 (256 of 160).  Many partials of one
-// output lose with few tiles too: 128 x 14336 24.4 / 22.9 (112 of 448 + 4).
+// for every tile that needs it, and one output's by fewer threads.  Measured, in
+// the cast / in a launch of their own, us a quantize, by tiles and partials of a
+// row + of a column: 512 x 512 8.3 / 9.9 (16, 2 + 8), 1024 x 4096 9.9 / 11.4 (256, 16
+// + 16), 2048 x 4096 13.6 / 15.2 (512, 16 + 32), 4096 x 2048 14.7 / 15.4 (512, 8 + 64),
+// 4096 x 4096 23.4 / 22.8 (1024, 16 + 64), 1024 x 14336 22.0 / 21.2 (896, 56 + 16), 8192 x
+// 1024 16.5 / 15.6 (512, 4 + 128).  Gated forward 640 x 2048 16.2 / 17.0 (80, 64 + 20), 784
+// x 6144 33.0 / 33.1 (336, 96 + 8), 128 x 8192 17.2 / 15.2 (64, 256 + 4).
 bool scales_in_cast(const CastSource &s, int64_t rows, int64_t cols) {
   const int64_t t = cdiv(rows, CT_T) * cdiv(cols, CT_T);
-  return t > 0 && s.row_slices <= 256 && s.col_slices <= 256 &&
-         t * (s.row_slices + s.col_slices) <= 1 << 16;
+  return t > 0 && s.row_slices <= 96 && s.col_slices <= 96 &&
+         t * (s.row_slices + s.col_slices) <= 48 << 10;
 }
 
 template <int FMT, bool NORM>
@@ -637,7 +640,7 @@ hipError_t cast_fmt(const CastSource *src, int count, int64_t rows, int64_t cols
     };
     if (nbr + nbc > 0)
       hipLaunchKernelGGL(k_finalize_rowwise<FMT>, dim3((unsigned)(nbr + nbc), (unsigned)count),
-                         dim3(256), 0, stream, job(0), job(l), R, C, src->row_slices,
+                         dim3(FR_THREADS), 0, stream, job(0), job(l), R, C, src->row_slices,
                          src->col_slices, (int)nbr);
   } else if (!rowwise && src->nparts == 0) {
     for (int i = 0; i < count; ++i)
