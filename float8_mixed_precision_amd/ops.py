@@ -496,6 +496,9 @@ def fp8_layernorm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = Non
         _checked(dev, ("q", out.q, u8, (rows, cols)), ("scale", out.scale, f32, (ns,)),
                  ("amax", out.amax, f32, (na,)))
         if transposed:
+            # (without qt the library takes the call for the serving form)
+            if out.scale_t is None or (out.qt is None and rows > 0):
+                raise ValueError("out must have qt and scale_t unless transposed=False")
             _checked(dev, ("qt", out.qt, u8, (cols, rows)), ("scale_t", out.scale_t, f32, (nst,)))
     want_stats = want_stats or transposed
     given = (out is not None and (not transposed or workspace is not None)
