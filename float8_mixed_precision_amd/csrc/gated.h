@@ -434,21 +434,29 @@ hipError_t launch_gate(GateArgs &g, bool rowwise, int *nparts, hipStream_t strea
 // maxima per wave row; tensorwise one u32 per wave of at most 256 workgroups, or
 // per workgroup of at most 8 SMALL_TILES.  A large tile holds 8 small ones.
 // (Columns per large tile: bn; a small tile has half as many.)
-int64_t row_slices(int64_t M, int64_t H, int bn) {
-  return 2 * (small_tiles(M, H, bn) ? tiles(H, bn / 2) : tiles(H, bn));
+int64_t row_slices(bool small, int64_t H, int bn) { return 2 * tiles(H, small ? bn / 2 : bn); }
+int64_t col_slices(bool small, int64_t M) { return 2 * tiles(M, small ? TM : BM); }
+size_t colpart_at(bool small, int64_t M, int64_t H, int bn) {
+  return ((size_t)(row_slices(small, H, bn) * M) * sizeof(uint16_t) + 255) & ~(size_t)255;
 }
-int64_t col_slices(int64_t M, int64_t H, int bn) {
-  return 2 * (small_tiles(M, H, bn) ? tiles(M, TM) : tiles(M, BM));
-}
-size_t colpart_at(int64_t M, int64_t H, int bn) {
-  return ((size_t)(row_slices(M, H, bn) * M) * sizeof(uint16_t) + 255) & ~(size_t)255;
+size_t rowwise_share(bool small, int64_t M, int64_t H, int bn) {
+  return colpart_at(small, M, H, bn) + (size_t)(col_slices(small, M) * H) * sizeof(uint16_t);
 }
 constexpr size_t TW_PARTS = 8 * SMALL_TILES > 4 * 256 ? 8 * SMALL_TILES : 4 * 256;
 static_assert(TW_PARTS <= TW_MAX_BLOCKS, "the cast reduces at most that many");
+// The size of a share does not fall as M or H grows, so that a workspace for
+// the largest batch serves the smaller ones, although the small tiles leave up
+// to four times the partials of the large ones: it is what the large tiles
+// need, and at least what small tiles need for any M' <= M and H' <= H.  (They
+// are at most 8 SMALL_TILES, each with 2 TM row and bn column maxima.)
 size_t gate_share_bytes(int64_t M, int64_t H, bool rowwise, int bn) {
-  const size_t b = rowwise ? colpart_at(M, H, bn) +
-                                 (size_t)(col_slices(M, H, bn) * H) * sizeof(uint16_t)
-                           : TW_PARTS * sizeof(uint32_t);
+  size_t b = TW_PARTS * sizeof(uint32_t);
+  if (rowwise) {
+    const size_t most = 8 * SMALL_TILES * (2 * TM + bn) * sizeof(uint16_t) + 256;
+    const size_t s = rowwise_share(true, M, H, bn);
+    b = rowwise_share(false, M, H, bn);
+    if (b < (s < most ? s : most)) b = s < most ? s : most;
+  }
   return (b + 255) & ~(size_t)255;
 }
 
@@ -456,13 +464,14 @@ size_t gate_share_bytes(int64_t M, int64_t H, bool rowwise, int bn) {
 // the cast reads them (src).
 void set_partials(GateArgs &g, int o, CastSource &src, void *share, bool rowwise, int bn) {
   if (rowwise) {
+    const bool small = small_tiles(g.M[0], g.N[0], bn);
     g.rowpart[o] = static_cast<uint16_t *>(share);
     g.colpart[o] = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(share) +
-                                                colpart_at(g.M[0], g.N[0], bn));
+                                                colpart_at(small, g.M[0], g.N[0], bn));
     src.rowpart = g.rowpart[o];
     src.colpart = g.colpart[o];
-    src.row_slices = (int)row_slices(g.M[0], g.N[0], bn);
-    src.col_slices = (int)col_slices(g.M[0], g.N[0], bn);
+    src.row_slices = (int)row_slices(small, g.N[0], bn);
+    src.col_slices = (int)col_slices(small, g.M[0]);
   } else {
     g.part[o] = static_cast<uint32_t *>(share);
     src.part = g.part[o];

@@ -570,7 +570,7 @@ def fp8_gated_workspace_bytes(M: int, H: int, rowwise: bool = False) -> int:
 
 def alloc_gated_workspace(M: int, H: int, rowwise: bool, device) -> torch.Tensor:
     """Workspace of fp8_gated_fwd (with a quantized h) and fp8_gated_bwd for
-    [M, H] outputs; needs no clearing."""
+    outputs of up to [M, H]; needs no clearing."""
     return torch.empty(max(fp8_gated_workspace_bytes(M, H, rowwise), 256), dtype=torch.uint8,
                        device=device)
 

@@ -375,7 +375,9 @@ FP8L_API int fp8_swiglu_bwd(const void *dh, const void *a, const void *b, int64_
  *           quantized, the workspace is not used (it may be NULL) and M is
  *           any number of tokens >= 0
  *   scaling FP8L_TENSORWISE or FP8L_ROWWISE, of the operands and of hq
- *   workspace / workspace_bytes: >= fp8_gated_workspace_bytes(M, H, scaling)
+ *   workspace / workspace_bytes: >= fp8_gated_workspace_bytes(M, H, scaling),
+ *           which does not fall as M or H grows: one for the largest batch serves
+ *           the smaller ones
  * H and K are multiples of 16, and M where h is quantized; sizes as for
  * fp8_linear_fwd.  The order of the fp32 additions depends on M and H (calls of
  * up to 16 tokens may split the contraction over a workgroup's waves); equal calls

@@ -21,3 +21,30 @@ def test_transposed_outputs_must_be_there(rowwise):
                     torch.empty(16))
     with pytest.raises(ValueError, match="on a GPU"):       # nothing wrong but the device
         E.fp8_layernorm_quantize(x, rowwise=True, transposed=False, out=z)
+
+
+def test_workspace_never_shrinks():
+    """A workspace sized for the largest batch (or width) serves every
+    smaller one, and it holds the partial maxima of both tile sizes: the rows' per
+    wave column, the columns' per wave row, of small tiles (64 rows x half a
+    large tile's columns) wherever those may be in use."""
+    f = E.lib().fp8_gated_workspace_bytes
+    Ms = (list(range(0, 320, 16)) + [1, 17, 63, 65, 255, 257] + list(range(320, 4200, 48))
+          + [8192, 16384, 65536])
+    Hs = [16, 64, 128, 144, 256, 400, 1024, 2048, 3968, 4096, 4112, 8192, 8208, 12272, 14336,
+          16384, 16400, 20480, 20496, 28672, 65536, 65552, 131072, 131088]
+    for scaling in (0, 1, 2, 3):
+        for grid, at in (([sorted(Ms), Hs], lambda u, v: f(u, v, scaling)),
+                         ([Hs, sorted(Ms)], lambda u, v: f(v, u, scaling))):
+            for v in grid[1]:
+                sizes = [at(u, v) for u in grid[0]]
+                assert all(p <= q for p, q in zip(sizes, sizes[1:])), (scaling, v, sizes)
+    up = lambda n, d: -(-n // d)
+    for M in Ms:
+        for H in Hs:
+            for bn in (128, 256):                # h; da and db
+                n = up(M, 256) * up(H, bn)
+                few = n <= (128 if bn == 128 else 80) or (M <= 64 and up(H, bn // 2) <= 1024)
+                tm, tn = (64, bn // 2) if few else (256, bn)
+                need = 2 * 2 * (up(H, tn) * M + up(M, tm) * H)
+                assert f(M, H, 1) >= need * (1 if bn == 128 else 2), (M, H, bn)
