@@ -122,14 +122,16 @@ struct Span {
   int64_t bytes;
 };
 
-// Whether one of the outputs spans[0..outs) meets another of the n spans.
+// Whether one of the outputs spans[0..outs) meets another of the n spans.  (A
+// workspace counts as an output, with the bytes that the call asks for.)
 template <int N>
 bool overlapping(const Span (&spans)[N], int outs) {
   for (int i = 0; i < outs; ++i)
     for (int j = i + 1; j < N; ++j) {
       const uintptr_t a = reinterpret_cast<uintptr_t>(spans[i].p);
       const uintptr_t b = reinterpret_cast<uintptr_t>(spans[j].p);
-      if (a && b && a < b + (uintptr_t)spans[j].bytes && b < a + (uintptr_t)spans[i].bytes)
+      if (a && b && spans[i].bytes > 0 && spans[j].bytes > 0 &&
+          a < b + (uintptr_t)spans[j].bytes && b < a + (uintptr_t)spans[i].bytes)
         return true;
     }
   return false;
@@ -395,17 +397,22 @@ int fp8_gated_fwd(const void *xq, const float *sx, const void *w1q, const float 
   if (s != FP8L_OK) return s;
   if (M * H > 0 && !a != !b) return FP8L_EINVAL;
   if (misaligned(a) || misaligned(b)) return FP8L_EALIGN;
+  size_t need = 0;
   if (quant) {
     s = check_quantize_args(h, M, H, scaling, hq, hqt, scale, scale_t, amax_out);
     if (s != FP8L_OK) return s;
     if (!workspace) return FP8L_EINVAL;
-    if (workspace_bytes < fp8l::gated_workspace_bytes(M, H, scaling)) return FP8L_EWORKSPACE;
+    need = fp8l::gated_workspace_bytes(M, H, scaling);
+    if (workspace_bytes < need) return FP8L_EWORKSPACE;
     if (misaligned(workspace)) return FP8L_EALIGN;
   }
   const int64_t mh = M * H;
-  const Span spans[] = {{a, 2 * mh}, {b, 2 * mh}, {h, 2 * mh}, {hq, mh}, {hqt, mh},
-                        {xq, M * K}, {w1q, H * K}, {w3q, H * K}};
-  if (overlapping(spans, 5)) return FP8L_EINVAL;
+  const bool rw = scaling == FP8L_ROWWISE;
+  const int64_t sm = rw ? 4 * M : 4, sh = rw ? 4 * H : 4;   // bytes of the scale vectors
+  const Span spans[] = {{a, 2 * mh}, {b, 2 * mh}, {h, 2 * mh}, {hq, mh}, {hqt, mh}, {scale, sm},
+                        {scale_t, sh}, {amax_out, rw ? sm + sh : 4}, {workspace, (int64_t)need},
+                        {xq, M * K}, {w1q, H * K}, {w3q, H * K}, {sx, sm}, {sw1, sh}, {sw3, sh}};
+  if (overlapping(spans, 9)) return FP8L_EINVAL;
   const fp8l::Fp8Out o = {hq, hqt, scale, scale_t, amax_out};
   hipError_t e = fp8l::gated_fwd_launch(
       static_cast<const uint8_t *>(xq), sx, static_cast<const uint8_t *>(w1q), sw1,
@@ -431,12 +438,18 @@ int fp8_gated_bwd(const void *dyq, const float *sdy, const void *w2tq, const flo
   if (s != FP8L_OK) return s;
   if (M * H > 0 && (!a || !b)) return FP8L_EINVAL;
   if (!workspace) return FP8L_EINVAL;
-  if (workspace_bytes < fp8l::gated_workspace_bytes(M, H, scaling)) return FP8L_EWORKSPACE;
+  const size_t need = fp8l::gated_workspace_bytes(M, H, scaling);
+  if (workspace_bytes < need) return FP8L_EWORKSPACE;
   if (misaligned(a) || misaligned(b) || misaligned(workspace)) return FP8L_EALIGN;
   const int64_t mh = M * H;
+  const bool rw = (scaling & FP8L_ROWWISE) != 0;
+  const int64_t sm = rw ? 4 * M : 4, sh = rw ? 4 * H : 4, am = rw ? sm + sh : 4;
   const Span spans[] = {{da, 2 * mh}, {db, 2 * mh}, {daq, mh}, {daqt, mh}, {dbq, mh}, {dbqt, mh},
-                        {a, 2 * mh}, {b, 2 * mh}, {dyq, M * D}, {w2tq, H * D}};
-  if (overlapping(spans, 6)) return FP8L_EINVAL;
+                        {da_scale, sm}, {da_scale_t, sh}, {da_amax, am}, {db_scale, sm},
+                        {db_scale_t, sh}, {db_amax, am}, {workspace, (int64_t)need},
+                        {a, 2 * mh}, {b, 2 * mh}, {dyq, M * D}, {w2tq, H * D}, {sdy, sm},
+                        {sw2t, sh}};
+  if (overlapping(spans, 13)) return FP8L_EINVAL;
   const fp8l::Fp8Out qa = {daq, daqt, da_scale, da_scale_t, da_amax};
   const fp8l::Fp8Out qb = {dbq, dbqt, db_scale, db_scale_t, db_amax};
   hipError_t e = fp8l::gated_bwd_launch(
@@ -462,7 +475,9 @@ int fp8_layernorm_fwd(const void *x, int64_t rows, int64_t cols, int kind, int d
       misaligned4(mean) || misaligned4(rstd))
     return FP8L_EALIGN;
   const int64_t bytes = rows * cols * (dtype == FP8L_F32 ? 4 : 2);
-  const Span spans[] = {{y, bytes}, {mean, 4 * rows}, {rstd, 4 * rows}, {x, bytes}};
+  const int64_t pb = cols * (pdtype == FP8L_F32 ? 4 : 2);
+  const Span spans[] = {{y, bytes}, {mean, 4 * rows}, {rstd, 4 * rows}, {x, bytes}, {weight, pb},
+                        {bias, pb}};
   if (overlapping(spans, 3)) return FP8L_EINVAL;
   const fp8l::NormIn in = {x, weight, bias, pdtype == FP8L_F32, kind == FP8L_RMSNORM, eps,
                            rows, cols};
@@ -499,15 +514,20 @@ int fp8_layernorm_quantize(const void *x, int64_t rows, int64_t cols, int kind,
   const fp8l::NormIn in = {x, weight, bias, pdtype == FP8L_F32, kind == FP8L_RMSNORM, eps,
                            rows, cols};
   hipStream_t st = static_cast<hipStream_t>(stream);
+  size_t need = 0;
   if (!rows_only) {
     if (rw && !scale_t) return FP8L_OK;          // no rows, no column scales wanted
     if (!workspace) return FP8L_EINVAL;
-    if (workspace_bytes < fp8l::norm_workspace_bytes(rows, cols, scaling)) return FP8L_EWORKSPACE;
+    need = fp8l::norm_workspace_bytes(rows, cols, scaling);
+    if (workspace_bytes < need) return FP8L_EWORKSPACE;
     if (misaligned(workspace)) return FP8L_EALIGN;
   }
-  const Span spans[] = {{y, 2 * rows * cols}, {q, rows * cols}, {qt, rows * cols},
-                        {mean, 4 * rows}, {rstd, 4 * rows}, {x, 2 * rows * cols}};
-  if (overlapping(spans, 5)) return FP8L_EINVAL;
+  const int64_t n = rows * cols, pb = cols * (pdtype == FP8L_F32 ? 4 : 2);
+  const int64_t sr = rw ? 4 * rows : 4, sc = rows_only ? 0 : rw ? 4 * cols : 4;
+  const Span spans[] = {{y, 2 * n}, {q, n}, {qt, n}, {mean, 4 * rows}, {rstd, 4 * rows},
+                        {scale, sr}, {scale_t, sc}, {amax_out, rw ? sr + sc : 4},
+                        {workspace, (int64_t)need}, {x, 2 * n}, {weight, pb}, {bias, pb}};
+  if (overlapping(spans, 9)) return FP8L_EINVAL;
   hipError_t e;
   if (rows_only) {
     e = fp8l::norm_rows_launch(in, y, mean, rstd, q, scale, amax_out, st);
@@ -530,16 +550,19 @@ int fp8_layernorm_bwd(const void *dy, const void *x, const void *weight, const f
     return FP8L_EALIGN;
   for (const float *f : {mean, rstd, (const float *)dweight, (const float *)dbias})
     if (misaligned4(f)) return FP8L_EALIGN;
+  size_t need = 0;
   if (dweight || dbias) {
     if (!workspace) return FP8L_EINVAL;
-    if (workspace_bytes < fp8l::norm_workspace_bytes(rows, cols, FP8L_TENSORWISE))
-      return FP8L_EWORKSPACE;
+    need = fp8l::norm_workspace_bytes(rows, cols, FP8L_TENSORWISE);
+    if (workspace_bytes < need) return FP8L_EWORKSPACE;
     if (misaligned(workspace)) return FP8L_EALIGN;
   }
   const int64_t bytes = rows * cols * (dtype == FP8L_F32 ? 4 : 2);
-  const Span spans[] = {{dx, bytes}, {dweight, 4 * cols}, {dbias, 4 * cols}, {dy, bytes},
-                        {x, bytes}, {mean, 4 * rows}, {rstd, 4 * rows}};
-  if (overlapping(spans, 3)) return FP8L_EINVAL;
+  const Span spans[] = {{dx, bytes}, {dweight, 4 * cols}, {dbias, 4 * cols},
+                        {workspace, (int64_t)need}, {dy, bytes}, {x, bytes},
+                        {weight, cols * (pdtype == FP8L_F32 ? 4 : 2)}, {mean, 4 * rows},
+                        {rstd, 4 * rows}};
+  if (overlapping(spans, 4)) return FP8L_EINVAL;
   const fp8l::NormIn in = {x, weight, nullptr, pdtype == FP8L_F32, kind == FP8L_RMSNORM, 0.f,
                            rows, cols};
   hipError_t e = fp8l::norm_bwd_launch(dy, in, dtype == FP8L_F32, mean, rstd, dx, dweight, dbias,

@@ -382,8 +382,8 @@ FP8L_API int fp8_swiglu_bwd(const void *dh, const void *a, const void *b, int64_
  * fp8_linear_fwd.  The order of the fp32 additions depends on M and H (calls of
  * up to 16 tokens may split the contraction over a workgroup's waves); equal calls
  * give equal bits.  The workspace's contents are undefined on entry and exit,
- * not shared by calls in flight together.  Outputs must not overlap inputs or
- * one another (FP8L_EINVAL for the matrices).
+ * not shared by calls in flight together.  Outputs and the workspace must not
+ * overlap inputs or one another (FP8L_EINVAL).
  */
 FP8L_API size_t fp8_gated_workspace_bytes(int64_t M, int64_t H, int scaling);
 FP8L_API int fp8_gated_fwd(const void *xq, const float *sx, const void *w1q, const float *sw1,
@@ -437,10 +437,9 @@ FP8L_API int fp8_gated_bwd(const void *dyq, const float *sdy, const void *w2tq,
  * Norms take any number of rows, and any 1 <= cols <= FP8L_NORM_MAX_COLS
  * except where codes are written (multiples of 16): FP8L_ESHAPE otherwise.
  * x, y, dy, dx, weight and bias need 16-byte alignment, as every tensor.
- * Outputs must not overlap inputs or one another (FP8L_EINVAL for the
- * matrices, mean, rstd and the gradients).  The order of the fp32
- * additions within a row depends on cols and on the number of rows; equal
- * calls give equal bits.
+ * Outputs and the workspace must not overlap inputs or one another
+ * (FP8L_EINVAL).  The order of the fp32 additions within a row depends on cols
+ * and on the number of rows; equal calls give equal bits.
  */
 #define FP8L_LAYERNORM 0
 #define FP8L_RMSNORM   1

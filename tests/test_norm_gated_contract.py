@@ -4,6 +4,12 @@ import pytest
 import torch
 
 from float8_mixed_precision_amd import ops as E
+from tests import test_gated_abi as gated_abi
+from tests import test_layernorm_abi as norm_abi
+
+A = 0x10000
+no_gpu = pytest.mark.skipif(torch.cuda.device_count() != 0,
+                            reason="fake-pointer cases run without a GPU only")
 
 
 @pytest.mark.parametrize("rowwise", [False, True], ids=["tensorwise", "rowwise"])
@@ -48,3 +54,39 @@ def test_workspace_never_shrinks():
                 tm, tn = (64, bn // 2) if few else (256, bn)
                 need = 2 * 2 * (up(H, tn) * M + up(M, tm) * H)
                 assert f(M, H, 1) >= need * (1 if bn == 128 else 2), (M, H, bn)
+
+
+@no_gpu
+def test_every_output_apart_from_every_buffer():
+    """An output (or the workspace) that meets any other buffer of its call is
+    refused: parameters, scale vectors and amax as well as the matrices, and a
+    buffer inside the workspace.  (Fake addresses, 2^24 bytes apart.)"""
+    at = lambda names: {n: A + (k << 24) for k, n in enumerate(names.split())}
+
+    def check(call, names, outs):
+        apart = at(names)
+        for one in outs.split():
+            for other in apart:
+                if other != one:
+                    assert call(**dict(apart, **{one: apart[other]})) == E.FP8L_EINVAL, (one, other)
+        if "ws" in apart:
+            for other in apart:
+                if other != "ws":
+                    inside = dict(apart, **{other: apart["ws"] + 64})
+                    assert call(**inside) == E.FP8L_EINVAL, (other, "in the workspace")
+
+    n = dict(rows=16, cols=32)
+    check(lambda **k: norm_abi.fwd(**n, **k), "x w b y mean rstd", "y mean rstd")
+    for scaling in (0, 1):
+        check(lambda **k: norm_abi.quant(scaling=scaling, **n, **k),
+              "x w b y mean rstd q qt s st amax ws", "y mean rstd q qt s st amax ws")
+    check(lambda **k: norm_abi.quant(scaling=1, qt=None, st=None, ws=None, wsb=0, **n, **k),
+          "x w b y mean rstd q s amax", "y mean rstd q s amax")
+    check(lambda **k: norm_abi.bwd(**n, **k), "dy x w mean rstd dx dw db ws", "dx dw db ws")
+    for scaling in (0, 1):
+        check(lambda **k: gated_abi.fwd(scaling=scaling, **k),
+              "x sx w1 s1 w3 s3 a b h hq hqt s st amax ws", "a b h hq hqt s st amax ws")
+    for scaling in (0, 1, 2, 3):
+        check(lambda **k: gated_abi.bwd(scaling=scaling, **k),
+              "dy sdy w sw a b da db daq daqt das dast daa dbq dbqt dbs dbst dba ws",
+              "da db daq daqt das dast daa dbq dbqt dbs dbst dba ws")
