@@ -933,6 +933,8 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
       const __amdgpu_buffer_rsrc_t rsRow = __builtin_amdgcn_make_buffer_rsrc(
           RW ? g.rowpart[0] + (size_t)((n0 / TN) * 2 + wn) * M : nullptr, (short)0,
           RW && g.maxima ? M * 2 : 0, 0x00020000);
+      // (the whole offset is checked against the resource, which drops rows past M)
+      const uint32_t row_at = (lane_e & 7) == 0 ? (uint32_t)row0 * 2 : OOB_C;
       // h of pass i: stored, its maxima taken
       auto finish = [&](int i) {
 #pragma unroll
@@ -950,10 +952,8 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
           if (!RW) tmax = pk_max(tmax, rm);
           if (RW) {
             rm = lanes_max<8>(hmax16(rm));
-            __builtin_amdgcn_raw_buffer_store_b16(
-                (unsigned short)rm, rsRow,
-                (lane_e & 7) == 0 && i * FR + u * 8 < M - row0 ? (uint32_t)row0 * 2 : OOB_C,
-                (i * FR + u * 8) * 2, 0);
+            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)rm, rsRow,
+                                                  row_at + (i * FR + u * 8) * 2, 0, 0);
           }
         }
       };
@@ -1015,6 +1015,8 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
       // row u * 4 + lane / 16 of pass i: the lane's offset in row 0, and what the
       // row adds to it (in the instruction's scalar offset)
       const int row0 = m0 + wm * WM + (lane_e >> 4);
+      // (the whole offset is checked against the resource, which drops rows past M)
+      const uint32_t row_at = (lane_e & 15) == 0 ? (uint32_t)row0 * 2 : OOB_C;
       const uint32_t off0 = ((uint32_t)row0 * (uint32_t)N + (uint32_t)scol) * 2u;
       const int rows_left = col_ok ? M - row0 : 0;
       auto offset = [&](int i, int u) { return i * FR + u * 4 < rows_left ? off0 : OOB_C; };
@@ -1080,12 +1082,10 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
           if (RW) {
             rm0 = lanes_max<16>(hmax16(rm0));
             rm1 = lanes_max<16>(hmax16(rm1));
-            const uint32_t at = (lane_e & 15) == 0 && i * FR + u * 4 < M - row0
-                                    ? (uint32_t)row0 * 2 : OOB_C;
-            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)rm0, rsRow0, at,
-                                                  (i * FR + u * 4) * 2, 0);
-            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)rm1, rsRow1, at,
-                                                  (i * FR + u * 4) * 2, 0);
+            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)rm0, rsRow0,
+                                                  row_at + (i * FR + u * 4) * 2, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)rm1, rsRow1,
+                                                  row_at + (i * FR + u * 4) * 2, 0, 0);
           } else {
             tmax.x = pk_max(tmax.x, rm0);
             tmax.y = pk_max(tmax.y, rm1);

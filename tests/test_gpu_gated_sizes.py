@@ -10,7 +10,7 @@ import oracle
 from float8_mixed_precision_amd import ops
 from float8_mixed_precision_amd import workloads as W
 from tests import gpu_util as G
-from tests.test_gpu_gated import RW, RW_IDS, _hq, _weights, _x, check_h
+from tests.test_gpu_gated import RW, RW_IDS, _hq, _pad16, _weights, _x, check_dab, check_h
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +39,53 @@ def test_one_workspace_for_shrinking_batches(rowwise):
         for p, q in zip(*out):
             assert np.array_equal(p, q), M
         assert torch.all(buf[size:] == 0x5A)
+
+
+# Large tiles with fewer rows than a wave's 128 (and than the 120 rows that its
+# row offsets reach): one row of tiles, more than 128 (forward) or 80 (backward)
+# of them; up to 64 rows where even the small tiles would be more than 1024.
+@pytest.mark.parametrize("rowwise", RW, ids=RW_IDS)
+@pytest.mark.parametrize("mh", [(80, 16400), (112, 16512), (67, 16400), (48, 65552)],
+                         ids=lambda s: "%dx%d" % s)
+def test_forward_one_row_of_large_tiles(mh, rowwise):
+    M, H = mh
+    K = 144
+    P = _pad16(M)
+    xq, sx = _x(M, K, rowwise, 92)
+    (w1, s1), (w3, s3) = _weights(H, K, rowwise, 92)
+    G.say("gated fwd, one row of large tiles", mh, "rowwise", rowwise)
+    pa, pb = (ops.fp8_linear_fwd(xq, sx, w, s, rowwise) for w, s in ((w1, s1), (w3, s3)))
+    xs, ss = xq[:M].clone(), sx[:M].clone() if rowwise else sx
+    z = ops.alloc_quantized(M, H, rowwise, G.DEV) if M == P else None
+    bufs = [torch.full((P + 1, H), 7.0, dtype=torch.bfloat16, device=G.DEV) for _ in range(3)]
+    h = ops.fp8_gated_fwd(xs, ss, w1, s1, w3, s3, rowwise, h=bufs[0][:M], a=bufs[1][:M],
+                          b=bufs[2][:M], out=z)
+    h2 = ops.fp8_gated_fwd(xs, ss, w1, s1, w3, s3, rowwise)
+    torch.cuda.synchronize()
+    assert torch.equal(bufs[1][:M], pa[:M]) and torch.equal(bufs[2][:M], pb[:M])
+    assert torch.equal(h, h2)
+    for t in bufs:
+        assert torch.all(t[M:] == 7.0)
+    check_h(G.host(h), G.host(pa[:M]), G.host(pb[:M]), "h %s" % (mh,))
+    if z is not None:
+        G.assert_quantize_equal(_hq(z), oracle.quantize(G.host(h), rowwise), "codes %s" % (mh,))
+
+
+@pytest.mark.parametrize("rowwise", RW, ids=RW_IDS)
+@pytest.mark.parametrize("mh", [(80, 20496), (112, 20736), (16, 131088)],
+                         ids=lambda s: "%dx%d" % s)
+def test_backward_one_row_of_large_tiles(mh, rowwise):
+    M, H = mh
+    D = 80
+    qdy = ops.fp8_linear_quantize(G.dev_bf16(W.random_bf16(93, (M, D), 1e-2, 0)), rowwise)
+    qw = ops.fp8_linear_quantize(G.dev_bf16(W.random_bf16(93, (D, H), 0.02, 1)), rowwise)
+    a, b = W.random_bf16(94, (M, H), 3.0, 0), W.random_bf16(94, (M, H), 1.0, 1)
+    G.say("gated bwd, one row of large tiles", mh, "rowwise", rowwise)
+    da, db, qa, qb = ops.fp8_gated_bwd(qdy.q, qdy.scale, qw.qt, qw.scale_t, G.dev_bf16(a),
+                                       G.dev_bf16(b), rowwise)
+    dh, _ = ops.fp8_linear_bwd(qdy.q, qdy.scale, None, None, qw.qt, qw.scale_t, None, None, M, D,
+                               H, rowwise, want_w=False)
+    torch.cuda.synchronize()
+    check_dab(G.host(da), G.host(db), G.host(dh), a, b, "bwd %s" % (mh,))
+    for z, t in ((qa, da), (qb, db)):
+        G.assert_quantize_equal(_hq(z), oracle.quantize(G.host(t), rowwise), "codes %s" % (mh,))
