@@ -10,6 +10,7 @@ import oracle
 from float8_mixed_precision_amd import ops
 from float8_mixed_precision_amd import workloads as W
 from tests import gpu_util as G
+from tests import test_gpu_gated
 from tests.test_gpu_gated import RW, RW_IDS, _hq, _pad16, _weights, _x, check_dab, check_h
 
 pytestmark = pytest.mark.gpu
@@ -89,3 +90,28 @@ def test_backward_one_row_of_large_tiles(mh, rowwise):
     check_dab(G.host(da), G.host(db), G.host(dh), a, b, "bwd %s" % (mh,))
     for z, t in ((qa, da), (qb, db)):
         G.assert_quantize_equal(_hq(z), oracle.quantize(G.host(t), rowwise), "codes %s" % (mh,))
+
+
+# 5 to 16 tokens on both sides of where the few-token kernel hands over to the
+# small tiles (192 of 64 columns), and 4 tokens, which it keeps at any width.
+@pytest.mark.parametrize("rowwise", RW, ids=RW_IDS)
+@pytest.mark.parametrize("mh", [(4, 14336), (5, 12272), (16, 12272), (5, 12288), (8, 14336),
+                                (13, 14336), (16, 12288), (16, 14336)],
+                         ids=lambda s: "%dx%d" % s)
+def test_decode_batches_of_wide_blocks(mh, rowwise):
+    """a, b within the instruction's bound of the oracle's, h from them, the
+    codes of h at 16 tokens (test_few_tokens' checks); the small tiles' a and b
+    are the plain GEMM's bits, at any number of tokens the padded call's."""
+    M, H = mh
+    K = 272
+    test_gpu_gated.test_few_tokens((M, H, K), rowwise)
+    if M > 4 and H >= 12288:
+        xq, sx = _x(M, K, rowwise, 95)
+        (w1, s1), (w3, s3) = _weights(H, K, rowwise, 95)
+        G.say("gated decode batch", mh, "rowwise", rowwise)
+        pa, pb = (ops.fp8_linear_fwd(xq, sx, w, s, rowwise) for w, s in ((w1, s1), (w3, s3)))
+        xs, ss = xq[:M].clone(), sx[:M].clone() if rowwise else sx
+        a, b = (torch.empty((M, H), dtype=torch.bfloat16, device=G.DEV) for _ in range(2))
+        ops.fp8_gated_fwd(xs, ss, w1, s1, w3, s3, rowwise, a=a, b=b)
+        torch.cuda.synchronize()
+        assert torch.equal(a, pa[:M]) and torch.equal(b, pb[:M])
