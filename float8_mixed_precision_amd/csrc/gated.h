@@ -6,9 +6,10 @@
 //
 // a, b and dh are rounded to bf16 before the gate, as the separate GEMM and
 // elementwise passes round them: a and b are outputs themselves, and h, da and
-// db are those of the stored a and b.  (The fp32 accumulators of the same
-// operands come out of the same instructions in the same order as the plain
-// GEMM's, so a, b and dh equal its outputs bit for bit.)
+// db are those of the stored a and b.  (In the large and small tiles the fp32
+// accumulators of the same operands come out of the same instructions in the
+// same order as the plain GEMM's, so a, b and dh equal its outputs bit for bit;
+// the few-token kernel splits the contraction and adds in another order.)
 //
 // Large M: the persistent GEMM with EPI_GATE / EPI_DGATE (gemm.hip).  Saved
 // against the separate passes: a and b are not read back to form h, dh is

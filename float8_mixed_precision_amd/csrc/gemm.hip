@@ -235,7 +235,9 @@ struct ArgsOf<EPI_NONE> {
 // log2(e) and of the exponent x log2(e) become a relative error of at most |x|
 // 2^-23 in e^-x: s and silu are within (|x| + 4) 2^-23 of exact, relatively
 // (below x = -87, where s leaves the normal range, silu may be flushed to 0:
-// absolute error under 2^-119).  The table of exact values that the elementwise
+// absolute error under 2^-119).  silu' adds two terms that cancel near its zero at
+// x = -1.278, so its error is stated absolutely: at most r (s + 2 |u|) + 2^-22 (s +
+// |u|), u = silu(x), r = (|x| + 4) 2^-23.  The table of exact values that the elementwise
 // kernels use (swiglu.hip) would not fit beside the operand stages in LDS; both
 // round to the same bf16 except where the value lies that close to a rounding
 // border.

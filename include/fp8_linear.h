@@ -361,10 +361,14 @@ FP8L_API int fp8_swiglu_bwd(const void *dh, const void *a, const void *b, int64_
  *   a[m][j] = fp8_linear_fwd's out for (xq, w1q),  b[m][j] for (xq, w3q)
  *   h       = bf16( fl32( silu(a) * b ) )
  *
- * from the bf16 a and b.  silu and silu' are computed in fp32 here (relative
- * error at most (|a| + 4) 2^-23; where the exact silu is below 2^-119 it may
- * be 0), so that h, da and db can differ from fp8_swiglu_fwd / _bwd's by one
- * bf16 step where the value lies next to a rounding border.
+ * from the bf16 a and b.  silu and silu' are computed in fp32 here.  With
+ * s = 1 / (1 + e^-a), u = a s and r = (|a| + 4) 2^-23, silu has a relative error
+ * of at most r (where the exact silu is below 2^-119 it may be 0); silu', which
+ * cancels near its zero at a = -1.278, an absolute one of at most
+ * r (s + 2 |u|) + 2^-22 (s + |u|) + 2^-118.  So h, da and db can differ from
+ * fp8_swiglu_fwd / _bwd's by one bf16 step where the value lies next to a
+ * rounding border.  Calls of up to 16 tokens may add a and b up in another order
+ * than fp8_linear_fwd (below).
  *
  *   xq [M, K], sx;  w1q, w3q [H, K], sw1, sw3   as fp8_linear_fwd's operands
  *   a, b    [M, H] bf16 (written), both or neither NULL: what fp8_gated_bwd

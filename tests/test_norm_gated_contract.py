@@ -1,5 +1,6 @@
 """What the norm's and the gated feed-forward's entry points promise beyond
 their argument checks: host side, no GPU needed."""
+import numpy as np
 import pytest
 import torch
 
@@ -90,3 +91,38 @@ def test_every_output_apart_from_every_buffer():
         check(lambda **k: gated_abi.bwd(scaling=scaling, **k),
               "dy sdy w sw a b da db daq daqt das dast daa dbq dbqt dbs dbst dba ws",
               "da db daq daqt das dast daa dbq dbqt dbs dbst dba ws")
+
+
+def test_stated_errors_of_silu():
+    """The header's error bounds against the kernels' sequence in 32 bits
+    (hardware exponential and reciprocal taken as correctly rounded, and one unit
+    off either way), for every finite bf16 gate: silu relative, silu' absolute.  A
+    relative bound of the same size does not hold for silu' near its zero."""
+    f32, f64 = np.float32, np.float64
+    x = (np.arange(1 << 16, dtype=np.uint32) << 16).view(f32)
+    x = x[np.isfinite(x) & (np.abs(x) < 2.0 ** 100)]
+    a = x.astype(f64)
+    unit = 2.0 ** -23
+    with np.errstate(all="ignore"):
+        s = 1 / (1 + np.exp(-a))
+        u = a * s
+        d = s + u * (1 - s)
+        r = (np.abs(a) + 4) * unit
+        worst = 0.0
+        for de in (-1, 0, 1):
+            for dr in (-1, 0, 1):
+                e = np.exp2((x * f32(-1.44269504088896341)).astype(f64))
+                e = (e * (1 + de * unit)).astype(f32)
+                sk = (1 / (f32(1) + e).astype(f64) * (1 + dr * unit)).astype(f32)
+                uk = x * sk
+                dk = (uk.astype(f64) * (f32(1) - sk).astype(f64) + sk).astype(f32)   # one rounding
+                assert np.all(np.abs(uk - u) <= r * np.abs(u) + 2.0 ** -119)
+                err = np.abs(dk - d)
+                assert np.all(err <= r * (s + 2 * np.abs(u)) + 2.0 ** -22 * (s + np.abs(u))
+                              + 2.0 ** -118)
+                # (no bf16 gate lies so near the zero that da is off by more than a
+                # rounding border's width)
+                assert np.all((err < 2.0 ** -10 * np.abs(d))[np.abs(a) < 80])
+                near = np.abs(a + 1.278) < 0.01
+                worst = max(worst, np.max((err / np.abs(d) / r)[near]))
+    assert worst > 10
