@@ -305,11 +305,19 @@ __device__ __forceinline__ float quotient(float s, float n, float inv) {
   return __builtin_fmaf(__builtin_fmaf(-q, n, s), inv, q);
 }
 
-// 1 / sqrt(v) by the hardware estimate (1 ulp), which takes v below the normal
-// range as 0: such v are scaled first.
+// 1 / sqrt(v): the hardware estimate (1 ulp; it takes v below the normal range
+// as 0, so such v are scaled first) and a Newton step with the residual 1 - v r^2
+// in two terms, which leaves the rounding of the result alone.  v = 0 gives
+// infinity, an infinite v 0, and NaN NaN: there the estimate stays.  (The step
+// costs 8192 x 4096 with its quantize 38.50 -> 38.55 us, 8192 x 8192 rowwise 79.95 ->
+// 80.25, y alone of 4096 x 4096 13.66 -> 13.86, of 65536 x 256 16.9 -> 17.3.)
 __device__ __forceinline__ float inverse_root(float v) {
   const bool tiny = v < 0x1p-100f;
-  return __builtin_amdgcn_rsqf(tiny ? v * 0x1p64f : v) * (tiny ? 0x1p32f : 1.0f);
+  const float u = tiny ? v * 0x1p64f : v;
+  const float r = __builtin_amdgcn_rsqf(u);
+  const float p = u * r;
+  const float e = __builtin_fmaf(-__builtin_fmaf(u, r, -p), r, __builtin_fmaf(-p, r, 1.0f));
+  return (__builtin_fabsf(e) < 1.0f ? __builtin_fmaf(0.5f * e, r, r) : r) * (tiny ? 0x1p32f : 1.0f);
 }
 
 // --------------------------------------------------------------- forward --
