@@ -19,8 +19,8 @@
 // k_gate_tile, one tile of 64 rows x 64 columns of h (128 of da and db) per
 // workgroup.
 //
-// Few tokens (at most one MFMA block, few_tokens): k_gated_skinny.  The time is
-// that of reading W1 and W3 once.  A workgroup owns 16 columns of h, its 8
+// Few tokens (at most one MFMA block, few_tokens): k_gated_skinny, bound by
+// reading W1 and W3 once.  A workgroup owns 16 columns of h, its 8
 // waves split the contraction and join through LDS; weights go straight from
 // memory to the MFMA operands (no byte of them is used twice), x comes from L2.
 //
@@ -64,9 +64,11 @@ __device__ __forceinline__ v8i frag(v4u lo, v4u hi) {
 // that one load instruction reads 64 contiguous bytes of each of 16 weight
 // rows.  Rows past M read row M - 1 (not stored).
 //
-// One token, 14336 columns, K = 4096: 23.8 us, 4.9 TB/s of weights, the rate of a
-// large copy; with 4 waves and the same loads in flight 26, with 2 k-tiles
-// together 28, with non-temporal loads 27.
+// One token, 14336 columns, K = 4096, rowwise: 25.5 us with six sets of weights in
+// turn, 4.6 TB/s from memory (a plain read of 112 MiB: 20.1 us, 5.85 TB/s); 21.8 us
+// with one set again and again, which the Infinity Cache then holds in part.
+// Called from Python, one set: 23.8 us; with 4 waves and the same loads in flight
+// 26, with 2 k-tiles together 28, with non-temporal loads 27.
 template <bool KFULL>
 __global__ __launch_bounds__(64 * SK_WAVES) void k_gated_skinny(SkinnyArgs p) {
   __shared__ v4f red[SK_WAVES][2][64];
@@ -141,7 +143,11 @@ __global__ __launch_bounds__(64 * SK_WAVES) void k_gated_skinny(SkinnyArgs p) {
 // units.  Measured, this kernel against the tiles, K = 4096, us for one token
 // and for 16: H = 4096 7.5 / 15.1 and 8.3 / 15.3, 8192 13.5 / 15.4 and 15.0 / 16.3,
 // 10240 19.3 / 21.3 and 21.6 / 21.0, 14336 24.1 / 23.0 (rowwise 24.3 / 27.4) and
-// 29.5 / 24.3; 4 tokens 25.2 / 26.5, 8 tokens 26.7 / 23.4.  (With more tokens every
+// 29.5 / 24.3; 4 tokens 25.2 / 26.5, 8 tokens 26.7 / 23.4.  Those are of one set of
+// weights, partly in the Infinity Cache.  From memory (H = 14336, six sets in
+// turn, rowwise and tensorwise) this kernel is ahead for longer: one token 25.5 /
+// 29.4 and 25.8 / 28.8, 4 tokens 26.2 / 29.4 and 26.5 / 28.9, 8 tokens 27.3 / 29.4 and
+// 27.2 / 28.9, 16 tokens 29.7 / 29.4 and 30.0 / 28.9.  (With more tokens every
 // workgroup reads all of x: a form with 4 token blocks took 33 us at 64 tokens
 // and H = 14336, the tiles 28.)
 bool few_tokens(int64_t M, int64_t H) { return M <= 4 || (M <= SKINNY_M && H < 64 * 192); }
@@ -162,14 +168,17 @@ hipError_t skinny_launch(const SkinnyArgs &p, hipStream_t stream) {
 // blocks of the same MFMA.  Three 24 KB stages of one 128-byte k-tile, filled
 // by DMA two k-tiles ahead, in the layout of the large kernel (16-byte chunk c
 // of row r at c ^ h(r)); one barrier per k-tile.  Two workgroups live on a
-// compute unit and cover each other's epilogue, which therefore works in the
-// accumulators' own layout: 8-byte accesses of 4 columns, no staging.
+// compute unit and cover each other's waits.  The epilogue works in the
+// accumulators' own layout: 8-byte accesses of 4 columns, 32 contiguous bytes a
+// row, no staging.
 //
 // Training forward of 1040 x 1808 (K = 784, rowwise, with the quantize of h) 20 us
 // against 28 with the 75 tiles of the large kernel, backward of 528 x 4112 (K =
 // 400, with both quantizes) 26 against 42 with its 51 tiles: too little work
-// to fill the chip either way, bound by the latency of the few k-tiles, the
-// epilogue and the launches after it.
+// to fill the chip either way.  Of the forward's 15.7 us in this kernel the 56
+// matrix instructions of a wave are less than 1; the rest (loads of 7 k-tiles two
+// ahead, the epilogue of a launch that is one round of workgroups) is not
+// broken down.
 constexpr int TM = 64;
 constexpr int TB = 128;                            // rows of the B slab
 constexpr int T_STAGE = (TM + TB) * BK;            // 24 KB
@@ -389,7 +398,9 @@ int64_t tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
 // 34.  Backward: 51 tiles 23 / 33, 64 tiles 32 / 45 and 38 / 60, 85 tiles 44 / 40, 112
 // tiles 55 / 60, 128 tiles 47 / 43.  One row of small tiles is better than one of
 // large ones at any number: 64 x 28672, K = 8192, 224 tiles, 103 / 132; backward 112
-// tiles 51 / 90; at 128 rows 137 / 154 but rowwise 154 / 129.  (The tensorwise
+// tiles 51 / 90; at 128 rows 137 / 154 but rowwise 154 / 129.  (No limit suits every
+// shape: the backward's 80 has 112 tiles, 5 us better small, on the wrong side,
+// with 85 and 128, 4 us better large, on the right one.  The tensorwise
 // maxima, one per small tile, bound that number.)
 constexpr int64_t SMALL_TILES = 128, SMALL_TILES_BWD = 80;
 bool small_tiles(int64_t M, int64_t H, int bn) {
