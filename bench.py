@@ -32,8 +32,9 @@ if ROOT not in sys.path:
 PEAK_FP8_TFLOPS = 5000.0      # MI355X dense fp8 MFMA
 PEAK_HBM_GBS = 8000.0         # MI355X HBM3E
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "gemm_traffic.json")
+# gemm.hip and every file of this library that it includes
 GEMM_SOURCES = [os.path.join(ROOT, "float8_mixed_precision_amd", "csrc", f)
-                for f in ("gemm.hip", "gemm_schedule.h")]
+                for f in ("gemm.hip", "fp8l_internal.h", "gemm_schedule.h", "gated.h")]
 
 
 def parse():
@@ -78,7 +79,7 @@ def copy_calibration(nbytes: int):
 
 
 def gemm_source_hash() -> str:
-    """Hash of the GEMM's sources (the kernel and its host-side schedule)."""
+    """Hash of the GEMM's sources (its whole translation unit)."""
     h = hashlib.sha256()
     for path in GEMM_SOURCES:
         with open(path, "rb") as f:
