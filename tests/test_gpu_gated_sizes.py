@@ -115,3 +115,47 @@ def test_decode_batches_of_wide_blocks(mh, rowwise):
         ops.fp8_gated_fwd(xs, ss, w1, s1, w3, s3, rowwise, a=a, b=b)
         torch.cuda.synchronize()
         assert torch.equal(a, pa[:M]) and torch.equal(b, pb[:M])
+
+
+@pytest.mark.parametrize("rowwise", RW, ids=RW_IDS)
+def test_outputs_of_almost_2_31_bytes(rowwise):
+    """[M, H] bf16 matrices just below 2^31 bytes, the largest that are taken: a
+    and b are the plain GEMM's, h, da and db follow from them in sampled rows (first,
+    last, random), the amax is that of the stored matrix and a sampled row's
+    rowwise codes are the oracle's; nothing is written behind an output."""
+    M, H, K = 65520, 16384, 32
+    xq, sx = _x(M, K, rowwise, 96)
+    (w1, s1), (w3, s3) = _weights(H, K, rowwise, 96)
+    w2 = ops.fp8_linear_quantize(G.dev_bf16(W.random_bf16(97, (K, H), 0.02, 3)), rowwise)
+    G.say("gated 2^31 bytes", "rowwise", rowwise)
+    bufs = [torch.full((M * H + 4096,), 7.0, dtype=torch.bfloat16, device=G.DEV)
+            for _ in range(5)]
+    h, a, b, da, db = (t[:M * H].view(M, H) for t in bufs)
+    z = ops.alloc_quantized(M, H, rowwise, G.DEV)
+    ws = ops.alloc_gated_workspace(M, H, rowwise, G.DEV)
+    ops.fp8_gated_fwd(xq, sx, w1, s1, w3, s3, rowwise, h=h, a=a, b=b, out=z, workspace=ws)
+    for t, w, s in ((a, w1, s1), (b, w3, s3)):
+        assert torch.equal(t, ops.fp8_linear_fwd(xq, sx, w, s, rowwise))
+    _, _, qa, qb = ops.fp8_gated_bwd(xq, sx, w2.qt, w2.scale_t, a, b, rowwise, da=da, db=db,
+                                     workspace=ws)
+    dh, _ = ops.fp8_linear_bwd(xq, sx, None, None, w2.qt, w2.scale_t, None, None, M, K, H, rowwise,
+                               want_w=False)
+    torch.cuda.synchronize()
+    for t in bufs:
+        assert torch.all(t[M * H:] == 7.0)
+    rows = torch.tensor(sorted({0, 1, M - 1, M - 2, 65279, 65280}
+                               | set(np.random.default_rng(5).integers(0, M, 26).tolist())),
+                        device=G.DEV)
+    some = lambda t: G.host(t[rows])
+    check_h(some(h), some(a), some(b), "h")
+    check_dab(some(da), some(db), some(dh), some(a), some(b), "da db")
+    for q, t in ((z, h), (qa, da), (qb, db)):
+        if rowwise:
+            assert torch.equal(q.amax[:M], t.abs().amax(1).float())
+            assert torch.equal(q.amax[M:], t.abs().amax(0).float())
+            sample = some(t)
+            for k, r in enumerate(rows.tolist()):
+                ref = oracle.quantize(np.repeat(sample[k:k + 1], 16, 0), True)
+                assert np.array_equal(G.host(q.q[r]), ref[0][0]), r
+        else:
+            assert q.amax.item() == t.abs().amax().item()
