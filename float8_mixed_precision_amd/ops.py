@@ -609,6 +609,9 @@ def fp8_gated_fwd(xq: torch.Tensor, sx: torch.Tensor, w1q: torch.Tensor, sw1: to
              *_operand("w3q", w3q, sw3, H, K, rowwise), ("a", a, bf, (M, H)), ("b", b, bf, (M, H)),
              ("h", h, bf, (M, H)))
     if out is not None:
+        # (without any of them the library takes the call for one that wants no codes)
+        if out.q is None or out.qt is None or out.scale is None or out.scale_t is None:
+            raise ValueError("out must have q, qt, scale and scale_t")
         _checked(dev, *_quantized("h", out, M, H, rowwise))
     given = h is not None and (out is None or workspace is not None)
     with _on_device(dev, None if given else stream):

@@ -30,6 +30,24 @@ def test_transposed_outputs_must_be_there(rowwise):
         E.fp8_layernorm_quantize(x, rowwise=True, transposed=False, out=z)
 
 
+@pytest.mark.parametrize("rowwise", [False, True], ids=["tensorwise", "rowwise"])
+def test_codes_of_h_must_be_there(rowwise):
+    """An `out` that holds no codes is refused, not taken for a call without one."""
+    x, w = (torch.zeros((n, 48), dtype=torch.uint8) for n in (16, 32))
+    sx, sw = (torch.ones(n if rowwise else 1) for n in (16, 32))
+    z = E.alloc_quantized(16, 32, rowwise, "cpu")
+    for out in (E.Quantized(None, None, None, None, None),
+                E.Quantized(None, z.qt, z.scale, z.scale_t, z.amax),
+                E.Quantized(z.q, None, z.scale, z.scale_t, z.amax),
+                E.Quantized(z.q, z.qt, None, z.scale_t, z.amax),
+                E.Quantized(z.q, z.qt, z.scale, None, z.amax)):
+        with pytest.raises(ValueError, match="out must have q, qt, scale and scale_t"):
+            E.fp8_gated_fwd(x, sx, w, sw, w, sw, rowwise, out=out)
+    z.amax = None                                            # optional
+    with pytest.raises(ValueError, match="on a GPU"):
+        E.fp8_gated_fwd(x, sx, w, sw, w, sw, rowwise, out=z)
+
+
 def test_workspace_never_shrinks():
     """A workspace sized for the largest batch (or width) serves every
     smaller one, and it holds the partial maxima of both tile sizes: the rows' per
