@@ -12,8 +12,9 @@
 // from the values held in registers, so a large common offset costs no
 // digits.  x is read once per pass.
 //
-// Bound: HBM.  A row (or the share of one) sits in registers between the
-// reductions; TPR threads work on a row: one wave for up to 512 columns (no
+// Bound: HBM where y or dx is written; the statistics pass of the quantize, which
+// only reads, by vector instructions (k_norm).  A row (or the share of one) sits
+// in registers between the reductions; TPR threads work on a row: one wave for up to 512 columns (no
 // barrier, reductions by DPP), 128 to 1024 threads for more (with_shape).
 //
 // The quantize forms need y only as fp8 codes.  Per-token codes (no
@@ -334,9 +335,11 @@ constexpr int block_threads() {
 // the same number of rounds (a row past the end is computed on row rows - 1
 // and not stored).
 //
-// Measured, statistics and maxima of 8192 x 4096 bf16 (tensorwise): 17.3 us,
-// 3.9 TB/s (this card reads a large array at 4.0), with 256 threads a row and
-// 2048 workgroups; with 512 threads 19.3 us; earlier forms of this kernel with a
+// Measured, statistics and maxima of 8192 x 4096 bf16 (tensorwise): 17.1 us,
+// 3.9 TB/s, with 256 threads a row and 2048 workgroups.  A plain read of the same
+// 64 MiB takes 12.5 us from memory and 10.7 from the Infinity Cache; here a vector
+// instruction issues in 0.89 of the cycles (7.8M of them, 15 an element and lane).
+// With 512 threads 19.3 us; earlier forms of this kernel with a
 // wave a row 30 us (its w and b take 128 registers, or twice the traffic of x
 // when read per row: 29 us), two rows a round 17-21 against 16.6 side by side.
 template <class T, int LAY, int TPR, int CH, int MODE>
