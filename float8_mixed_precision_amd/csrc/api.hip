@@ -137,6 +137,32 @@ bool overlapping(const Span (&spans)[N], int outs) {
   return false;
 }
 
+bool bad_finite(float v) { return !(v >= -3.402823466e38f && v <= 3.402823466e38f); }
+
+// Checks of a residual norm's descriptor shared by its entry points, and the
+// launchers' form of it.
+int check_resnorm(const fp8l_resnorm *r, fp8l::ResIn &in) {
+  if (!r) return FP8L_EINVAL;
+  const int s = check_norm(r->rows, r->cols, r->kind, r->dtype, r->pdtype);
+  if (s != FP8L_OK) return s;
+  if ((r->norms & ~(FP8L_POST_NORM | FP8L_PRE_NORM)) || r->norms == 0) return FP8L_EINVAL;
+  if (bad_finite(r->alpha) || (r->rows > 0 && (!r->b || !r->s))) return FP8L_EINVAL;
+  const bool post = (r->norms & FP8L_POST_NORM) != 0, pre = (r->norms & FP8L_PRE_NORM) != 0;
+  const bool rms = r->kind == FP8L_RMSNORM;
+  in = {r->b, r->x, post ? r->post_w : nullptr, post ? r->post_b : nullptr,
+        pre ? r->pre_w : nullptr, pre ? r->pre_b : nullptr, r->gate, r->pdtype == FP8L_F32,
+        r->dtype == FP8L_F32, rms, post, pre, r->alpha, r->eps, r->rows, r->cols, r->s,
+        pre ? r->y : nullptr, post && !rms ? r->mean_post : nullptr,
+        post ? r->rstd_post : nullptr, pre && !rms ? r->mean_pre : nullptr,
+        pre ? r->rstd_pre : nullptr};
+  for (const void *p : {in.b, in.x, in.post_w, in.post_b, in.pre_w, in.pre_b, in.gate,
+                        (const void *)in.s, (const void *)in.y})
+    if (misaligned(p)) return FP8L_EALIGN;
+  for (const float *f : {in.mean_post, in.rstd_post, in.mean_pre, in.rstd_pre})
+    if (misaligned4(f)) return FP8L_EALIGN;
+  return FP8L_OK;
+}
+
 bool bad_eps(float eps) { return !(eps >= 0.f && eps <= 3.402823466e38f); }
 
 }  // namespace
@@ -568,6 +594,128 @@ int fp8_layernorm_bwd(const void *dy, const void *x, const void *weight, const f
   hipError_t e = fp8l::norm_bwd_launch(dy, in, dtype == FP8L_F32, mean, rstd, dx, dweight, dbias,
                                        workspace, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? FP8L_OK : FP8L_EHIP;
+}
+
+size_t fp8_resnorm_workspace_bytes(int64_t rows, int64_t cols, int scaling) {
+  if (check_norm(rows, cols, 0, 0, 0) != FP8L_OK || bad_scaling(scaling)) return 0;
+  return fp8l::resnorm_workspace_bytes(rows, cols, scaling);
+}
+
+int fp8_resnorm_fwd(const fp8l_resnorm *r, void *stream) {
+  fp8l::ResIn in;
+  const int s = check_resnorm(r, in);
+  if (s != FP8L_OK) return s;
+  if (bad_eps(r->eps) || (in.rows > 0 && (!in.x || (in.pre && !in.y)))) return FP8L_EINVAL;
+  const int64_t n = in.rows * in.cols, e = in.f32 ? 4 : 2, pb = in.cols * (in.wf32 ? 4 : 2);
+  const Span spans[] = {{in.s, e * n}, {in.y, 2 * n}, {in.mean_post, 4 * in.rows},
+                        {in.rstd_post, 4 * in.rows}, {in.mean_pre, 4 * in.rows},
+                        {in.rstd_pre, 4 * in.rows}, {in.b, 2 * n}, {in.x, e * n},
+                        {in.post_w, pb}, {in.post_b, pb}, {in.pre_w, pb}, {in.pre_b, pb},
+                        {in.gate, pb}};
+  if (overlapping(spans, 6)) return FP8L_EINVAL;
+  const hipError_t err = fp8l::resnorm_fwd_launch(in, static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? FP8L_OK : FP8L_EHIP;
+}
+
+int fp8_resnorm_quantize(const fp8l_resnorm *r, int scaling, void *q, void *qt, float *scale,
+                         float *scale_t, float *amax_out, void *workspace,
+                         size_t workspace_bytes, void *stream) {
+  fp8l::ResIn in;
+  const int s = check_resnorm(r, in);
+  if (s != FP8L_OK) return s;
+  if (scaling != FP8L_TENSORWISE && scaling != FP8L_ROWWISE) return FP8L_EINVAL;
+  if (bad_eps(r->eps) || !in.pre) return FP8L_EINVAL;
+  const bool rw = scaling == FP8L_ROWWISE;
+  const bool rows_only = rw && !qt && in.rows > 0;
+  if (in.cols % 16 != 0 || (!rows_only && in.rows % 16 != 0)) return FP8L_ESHAPE;
+  if (in.rows > 0 && (!in.x || !q || (!qt && !rows_only))) return FP8L_EINVAL;
+  // scale vectors may be NULL only where they have no entries
+  if (!scale && (!rw || in.rows > 0)) return FP8L_EINVAL;
+  if (!scale_t && (qt || !rw)) return FP8L_EINVAL;
+  if (!rows_only && in.rows > 0 && !in.y &&
+      (in.f32 || !in.rstd_pre || (!in.rms && !in.mean_pre)))
+    return FP8L_EINVAL;
+  if (misaligned(q) || misaligned(qt)) return FP8L_EALIGN;
+  if (misaligned4(scale) || misaligned4(scale_t) || misaligned4(amax_out)) return FP8L_EALIGN;
+  size_t need = 0;
+  if (!rows_only) {
+    if (rw && !scale_t) return FP8L_OK;          // no rows, no column scales wanted
+    if (!workspace) return FP8L_EINVAL;
+    need = fp8l::resnorm_workspace_bytes(in.rows, in.cols, scaling);
+    if (workspace_bytes < need) return FP8L_EWORKSPACE;
+    if (misaligned(workspace)) return FP8L_EALIGN;
+  }
+  const int64_t n = in.rows * in.cols, e = in.f32 ? 4 : 2, pb = in.cols * (in.wf32 ? 4 : 2);
+  const int64_t sr = rw ? 4 * in.rows : 4, sc = rows_only ? 0 : rw ? 4 * in.cols : 4;
+  const Span spans[] = {{in.s, e * n}, {in.y, 2 * n}, {q, n}, {qt, n}, {scale, sr},
+                        {scale_t, sc}, {amax_out, rw ? sr + sc : 4}, {workspace, (int64_t)need},
+                        {in.mean_post, 4 * in.rows}, {in.rstd_post, 4 * in.rows},
+                        {in.mean_pre, 4 * in.rows}, {in.rstd_pre, 4 * in.rows},
+                        {in.b, 2 * n}, {in.x, e * n}, {in.post_w, pb}, {in.post_b, pb},
+                        {in.pre_w, pb}, {in.pre_b, pb}, {in.gate, pb}};
+  if (overlapping(spans, 12)) return FP8L_EINVAL;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const hipError_t err =
+      rows_only ? fp8l::resnorm_rows_launch(in, q, scale, amax_out, st)
+                : fp8l::resnorm_quantize_launch(in, scaling, {q, qt, scale, scale_t, amax_out},
+                                                workspace, st);
+  return err == hipSuccess ? FP8L_OK : FP8L_EHIP;
+}
+
+int fp8_resnorm_bwd(const fp8l_resnorm *r, const void *dy, const void *ds,
+                    const fp8l_resnorm_grads *g, int scaling, void *q, void *qt, float *scale,
+                    float *scale_t, float *amax_out, void *workspace, size_t workspace_bytes,
+                    void *stream) {
+  fp8l::ResIn in;
+  const int s = check_resnorm(r, in);
+  if (s != FP8L_OK) return s;
+  if (!g || bad_scaling(scaling)) return FP8L_EINVAL;
+  const bool quant = q || qt || scale || scale_t || amax_out;
+  if (quant && (in.rows % 16 != 0 || in.cols % 16 != 0)) return FP8L_ESHAPE;
+  if (in.rows > 0) {
+    if (!g->db || !dy != !in.pre || (!ds && !in.pre)) return FP8L_EINVAL;
+    if ((in.post && (!in.rstd_post || (!in.rms && !in.mean_post))) ||
+        (in.pre && (!in.rstd_pre || (!in.rms && !in.mean_pre))))
+      return FP8L_EINVAL;
+  }
+  if ((!in.post && (g->dpost_w || g->dpost_b)) || (!in.pre && (g->dpre_w || g->dpre_b)) ||
+      (!in.gate && g->dgate))
+    return FP8L_EINVAL;
+  if (misaligned(dy) || misaligned(ds) || misaligned(g->dx) || misaligned(g->db))
+    return FP8L_EALIGN;
+  const bool wants = g->dgate || g->dpost_w || g->dpost_b || g->dpre_w || g->dpre_b;
+  for (const float *f : {g->dgate, g->dpost_w, g->dpost_b, g->dpre_w, g->dpre_b})
+    if (misaligned4(f)) return FP8L_EALIGN;
+  if (quant) {
+    const int e = check_quantize_args(g->db, in.rows, in.cols, scaling, q, qt, scale, scale_t,
+                                      amax_out);
+    if (e != FP8L_OK) return e;
+  }
+  size_t need = 0;
+  if (wants || quant) {
+    if (!workspace) return FP8L_EINVAL;
+    need = fp8l::resnorm_workspace_bytes(in.rows, in.cols, scaling);
+    if (workspace_bytes < need) return FP8L_EWORKSPACE;
+    if (misaligned(workspace)) return FP8L_EALIGN;
+  }
+  const int64_t n = in.rows * in.cols, e = in.f32 ? 4 : 2, pb = in.cols * (in.wf32 ? 4 : 2);
+  const int64_t cb = 4 * in.cols, rb = 4 * in.rows;
+  const bool rw = (scaling & FP8L_ROWWISE) != 0;
+  const int64_t sr = rw ? rb : 4, sc = rw ? cb : 4;
+  const Span spans[] = {{g->dx, e * n}, {g->db, 2 * n}, {g->dgate, cb}, {g->dpost_w, cb},
+                        {g->dpost_b, cb}, {g->dpre_w, cb}, {g->dpre_b, cb}, {q, n}, {qt, n},
+                        {scale, sr}, {scale_t, sc}, {amax_out, rw ? sr + sc : 4},
+                        {workspace, (int64_t)need}, {dy, 2 * n}, {ds, e * n}, {in.b, 2 * n},
+                        {in.s, e * n}, {in.post_w, pb}, {in.post_b, pb}, {in.pre_w, pb},
+                        {in.pre_b, pb}, {in.gate, pb}, {in.mean_post, rb}, {in.rstd_post, rb},
+                        {in.mean_pre, rb}, {in.rstd_pre, rb}};
+  if (overlapping(spans, 13)) return FP8L_EINVAL;
+  const fp8l::ResGrads gr = {g->dx, g->db, g->dgate, g->dpost_w, g->dpost_b, g->dpre_w,
+                             g->dpre_b};
+  const fp8l::Fp8Out o = {q, qt, scale, scale_t, amax_out};
+  const hipError_t err = fp8l::resnorm_bwd_launch(in, dy, ds, gr, scaling, quant ? &o : nullptr,
+                                                  workspace, static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? FP8L_OK : FP8L_EHIP;
 }
 
 int fp8_linear_encode_e4m3(const float *in, uint8_t *out, int64_t n, void *stream) {

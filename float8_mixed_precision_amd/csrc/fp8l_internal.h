@@ -212,6 +212,33 @@ hipError_t norm_bwd_launch(const void *dy, const NormIn &in, int f32, const floa
                            const float *rstd, void *dx, float *dw, float *db, void *workspace,
                            hipStream_t stream);
 
+// Residual norm (resnorm.h).  Parameters as above; post, pre: which norms there
+// are; f32: type of the stream (x, s, ds, dx).
+struct ResIn {
+  const void *b, *x;
+  const void *post_w, *post_b, *pre_w, *pre_b, *gate;
+  int wf32, f32, rms, post, pre;
+  float alpha, eps;
+  int64_t rows, cols;
+  void *s, *y;                 // y may be NULL
+  float *mean_post, *rstd_post, *mean_pre, *rstd_pre;
+};
+struct ResGrads {
+  void *dx, *db;               // dx may be NULL
+  float *dgate, *dpost_w, *dpost_b, *dpre_w, *dpre_b;   // each may be NULL
+};
+size_t resnorm_workspace_bytes(int64_t rows, int64_t cols, int scaling);
+hipError_t resnorm_fwd_launch(const ResIn &in, hipStream_t stream);
+hipError_t resnorm_rows_launch(const ResIn &in, void *q, float *scale, float *amax_out,
+                               hipStream_t stream);
+// y NULL: a bf16 stream, whose cast normalizes s again (mean_pre and rstd_pre
+// needed)
+hipError_t resnorm_quantize_launch(const ResIn &in, int scaling, const Fp8Out &o, void *workspace,
+                                   hipStream_t stream);
+// o NULL: db is not quantized
+hipError_t resnorm_bwd_launch(const ResIn &in, const void *dy, const void *ds, const ResGrads &gr,
+                              int scaling, const Fp8Out *o, void *workspace, hipStream_t stream);
+
 // SwiGLU producers (swiglu.hip): the elementwise pass writes its bf16
 // outputs with their amax partial maxima, then each output's quantize
 // finishes with quantize_finish_launch.  The workspace holds two shares,

@@ -14,6 +14,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -29,7 +30,8 @@ EXPORTS = ("fp8_linear_workspace_bytes", "fp8_linear_quantize",
            "fp8_linear_bwd_w_f32", "fp8_linear_bwd_x_acc", "fp8_linear_gemm_grouped",
            "fp8_gated_workspace_bytes", "fp8_gated_fwd", "fp8_gated_bwd",
            "fp8_layernorm_workspace_bytes", "fp8_layernorm_fwd", "fp8_layernorm_quantize",
-           "fp8_layernorm_bwd", "fp8_linear_encode_e4m3",
+           "fp8_layernorm_bwd", "fp8_resnorm_workspace_bytes", "fp8_resnorm_fwd",
+           "fp8_resnorm_quantize", "fp8_resnorm_bwd", "fp8_linear_encode_e4m3",
            "fp8_linear_encode_e5m2", "fp8_swiglu_workspace_bytes", "fp8_swiglu_fwd",
            "fp8_swiglu_bwd", "fp8_linear_status_string", "fp8_linear_version")
 
@@ -38,6 +40,7 @@ FP8L_MAX_GROUP = 4
 FP8L_LAYERNORM, FP8L_RMSNORM = 0, 1
 FP8L_BF16, FP8L_F32 = 0, 1
 FP8L_NORM_MAX_COLS = 16384
+FP8L_POST_NORM, FP8L_PRE_NORM = 1, 2
 
 
 class GemmProblem(ctypes.Structure):
@@ -111,6 +114,15 @@ def lib() -> ctypes.CDLL:
                                          + [P, ctypes.c_size_t, P])
     L.fp8_layernorm_bwd.restype = I
     L.fp8_layernorm_bwd.argtypes = ([P] * 5 + [i64, i64, I, I, I, P, P, P, P, ctypes.c_size_t, P])
+    S = ctypes.c_char_p          # a packed descriptor (_RESNORM, _RESNORM_GRADS)
+    L.fp8_resnorm_workspace_bytes.restype = ctypes.c_size_t
+    L.fp8_resnorm_workspace_bytes.argtypes = [i64, i64, I]
+    L.fp8_resnorm_fwd.restype = I
+    L.fp8_resnorm_fwd.argtypes = [S, P]
+    L.fp8_resnorm_quantize.restype = I
+    L.fp8_resnorm_quantize.argtypes = [S, I] + [P] * 5 + [P, ctypes.c_size_t, P]
+    L.fp8_resnorm_bwd.restype = I
+    L.fp8_resnorm_bwd.argtypes = [S, P, P, S, I] + [P] * 5 + [P, ctypes.c_size_t, P]
     L.fp8_linear_encode_e4m3.restype = I
     L.fp8_linear_encode_e4m3.argtypes = [P, P, i64, P]
     L.fp8_linear_encode_e5m2.restype = I
@@ -560,6 +572,246 @@ def fp8_layernorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.
             _DTYPES[xd], _DTYPES[pd], _a(dx), _a(dweight), _a(dbias), *_ws(workspace, dev),
             _stream(stream)), "fp8_layernorm_bwd")
     return dx, dweight, dbias
+
+
+# --------------------------------------------------------- residual norm --
+
+# fp8l_resnorm and fp8l_resnorm_grads of the C ABI (packing their fields into bytes
+# takes a third of the time that a ctypes structure's assignments take)
+_RESNORM = struct.Struct("@qqiiiiff13P")
+_RESNORM_GRADS = struct.Struct("@7P")
+
+
+class ResNormStats:
+    """Statistics of a residual norm, fp32 [rows] each: of the block's output
+    (post) and of the stream behind it (pre); None where there is no such norm
+    or, for the means, in the RMS form."""
+
+    __slots__ = ("mean_post", "rstd_post", "mean_pre", "rstd_pre")
+
+    def __init__(self, mean_post=None, rstd_post=None, mean_pre=None, rstd_pre=None):
+        self.mean_post, self.rstd_post = mean_post, rstd_post
+        self.mean_pre, self.rstd_pre = mean_pre, rstd_pre
+
+
+class ResNormGrads:
+    """Outputs of fp8_resnorm_bwd: dx in the stream's type, db bf16, the
+    parameters' gradients fp32 [cols]; None where not wanted."""
+
+    __slots__ = ("dx", "db", "dgate", "dpost_weight", "dpost_bias", "dpre_weight", "dpre_bias")
+
+    def __init__(self, dx=None, db=None, dgate=None, dpost_weight=None, dpost_bias=None,
+                 dpre_weight=None, dpre_bias=None):
+        self.dx, self.db, self.dgate = dx, db, dgate
+        self.dpost_weight, self.dpost_bias = dpost_weight, dpost_bias
+        self.dpre_weight, self.dpre_bias = dpre_weight, dpre_bias
+
+
+def alloc_resnorm_stats(rows: int, device, post: bool = True, pre: bool = True,
+                        rms: bool = False) -> ResNormStats:
+    new = lambda there: torch.empty(rows, dtype=torch.float32, device=device) if there else None
+    return ResNormStats(new(post and not rms), new(post), new(pre and not rms), new(pre))
+
+
+def fp8_resnorm_workspace_bytes(rows: int, cols: int, rowwise: bool = False) -> int:
+    return int(lib().fp8_resnorm_workspace_bytes(rows, cols, _scaling(rowwise)))
+
+
+def alloc_resnorm_workspace(rows: int, cols: int, device, rowwise: bool = False) -> torch.Tensor:
+    """Workspace of fp8_resnorm_quantize (with this scaling) and fp8_resnorm_bwd
+    for a stream of up to [rows, cols]; needs no clearing."""
+    return torch.empty(max(fp8_resnorm_workspace_bytes(rows, cols, rowwise), 256),
+                       dtype=torch.uint8, device=device)
+
+
+_NO_PAIR = (None, None)
+
+
+def _resnorm_params(b, post, pre, gate):
+    """Checked (post, pre, type of the parameters): each norm a (weight, bias)
+    pair, (None, None) where it is not there."""
+    if b.dim() != 2:
+        raise ValueError("b must be a [rows, cols] bf16 matrix")
+    if post is None and pre is None:
+        raise ValueError("post or pre must be a (weight, bias) pair")
+    pd = None
+    for pair in (post, pre, (gate,)):
+        for p in pair or ():
+            if p is not None:
+                if p.dtype not in _DTYPES or pd not in (None, p.dtype):
+                    raise ValueError("the parameters must be all bf16 or all fp32")
+                pd = p.dtype
+    return post or _NO_PAIR, pre or _NO_PAIR, pd or torch.bfloat16
+
+
+def _pack_resnorm(b, x, s, y, post, pre, gate, pd, xd, norms, alpha, eps, rms, st):
+    rows, cols = b.shape
+    a = lambda t: 0 if t is None else t.data_ptr()
+    return _RESNORM.pack(rows, cols, int(rms), norms, _DTYPES[xd], _DTYPES[pd], alpha, eps, a(b),
+                         a(x), a(post[0]), a(post[1]), a(pre[0]), a(pre[1]), a(gate), a(s), a(y),
+                         a(st.mean_post), a(st.rstd_post), a(st.mean_pre), a(st.rstd_pre))
+
+
+def _resnorm_forward(b, x, post, pre, gate, rms, s, y, stats):
+    """Checks shared by the forward calls: (post, pre, their norms flags, type of
+    the parameters)."""
+    norms = ((FP8L_POST_NORM if post is not None else 0)
+             | (FP8L_PRE_NORM if pre is not None else 0))
+    post, pre, pd = _resnorm_params(b, post, pre, gate)
+    rows, cols = b.shape
+    bf, f32, dev, xd = torch.bfloat16, torch.float32, b.device, x.dtype
+    if xd not in _DTYPES:
+        raise ValueError("x must be a bf16 or fp32 matrix")
+    _checked(dev, ("b", b, bf, b.shape), ("x", x, xd, b.shape), ("s", s, xd, b.shape),
+             ("y", y, bf, b.shape), ("post weight", post[0], pd, (cols,)),
+             ("post bias", post[1], pd, (cols,)), ("pre weight", pre[0], pd, (cols,)),
+             ("pre bias", pre[1], pd, (cols,)), ("gate", gate, pd, (cols,)))
+    if y is not None and not norms & FP8L_PRE_NORM:
+        raise ValueError("y must be None without a pre norm")
+    if stats is not None:
+        _checked(dev, ("mean_post", stats.mean_post, f32, (rows,)),
+                 ("rstd_post", stats.rstd_post, f32, (rows,)),
+                 ("mean_pre", stats.mean_pre, f32, (rows,)),
+                 ("rstd_pre", stats.rstd_pre, f32, (rows,)))
+    return post, pre, norms, pd
+
+
+_NO_STATS = ResNormStats()
+
+
+def fp8_resnorm_fwd(b: torch.Tensor, x: torch.Tensor, post=None, pre=None,
+                    gate: Optional[torch.Tensor] = None, alpha: float = 1.0, eps: float = 1e-5,
+                    rms: bool = False, s: Optional[torch.Tensor] = None,
+                    y: Optional[torch.Tensor] = None, stats: Optional[ResNormStats] = None,
+                    stream=None):
+    """(s, y, stats): s = alpha x + gate N(b; post) and y = N(s; pre) for a
+    block's output b [rows, cols] (bf16) and the residual stream x (bf16 or
+    fp32, s in its type).  post and pre are (weight, bias) pairs, each a tensor
+    or None, or None where there is no such norm (not both; without pre y is
+    None); gate [cols] or None.  Of given ``stats`` only the tensors in it are
+    written."""
+    post, pre, norms, pd = _resnorm_forward(b, x, post, pre, gate, rms, s, y, stats)
+    want_y = bool(norms & FP8L_PRE_NORM)
+    given = s is not None and stats is not None and (y is not None or not want_y)
+    dev = b.device
+    with _on_device(dev, None if given else stream):
+        if s is None:
+            s = torch.empty_like(x)
+        if y is None and want_y:
+            y = torch.empty_like(b)
+        if stats is None:
+            stats = alloc_resnorm_stats(b.shape[0], dev, bool(norms & FP8L_POST_NORM), want_y, rms)
+        _check(lib().fp8_resnorm_fwd(
+            _pack_resnorm(b, x, s, y, post, pre, gate, pd, x.dtype, norms, alpha, eps, rms, stats),
+            _stream(stream)), "fp8_resnorm_fwd")
+    return s, y, stats
+
+
+def fp8_resnorm_quantize(b: torch.Tensor, x: torch.Tensor, post=None, pre=_NO_PAIR,
+                         gate: Optional[torch.Tensor] = None, alpha: float = 1.0,
+                         eps: float = 1e-5, rms: bool = False, rowwise: bool = False,
+                         transposed: bool = True, s: Optional[torch.Tensor] = None,
+                         y: Optional[torch.Tensor] = None, out: Optional[Quantized] = None,
+                         stats: Optional[ResNormStats] = None,
+                         workspace: Optional[torch.Tensor] = None, want_stats: bool = True,
+                         stream=None):
+    """(s, Quantized, stats): fp8_resnorm_fwd with the E4M3 quantize of y.  y
+    itself is stored only if a tensor ``y`` is given for it, which an fp32
+    stream needs.  transposed=False (rowwise only) is the serving form: the codes
+    and scales of each row alone, any number of rows, with any stream; there
+    want_stats=False leaves the statistics out (None)."""
+    if pre is None:
+        raise ValueError("pre must be a (weight, bias) pair")
+    if not transposed and not rowwise:
+        raise ValueError("codes without their transposed copy are rowwise")
+    post, pre, norms, pd = _resnorm_forward(b, x, post, pre, gate, rms, s, y, stats)
+    rows, cols = b.shape
+    f32, u8, dev = torch.float32, torch.uint8, b.device
+    if out is not None:
+        if transposed:
+            # (without qt the library takes the call for the serving form)
+            if out.scale_t is None or (out.qt is None and rows > 0):
+                raise ValueError("out must have qt and scale_t unless transposed=False")
+            _checked(dev, *_quantized("y ", out, rows, cols, rowwise))
+        else:
+            _checked(dev, ("q", out.q, u8, (rows, cols)), ("scale", out.scale, f32, (rows,)),
+                     ("amax", out.amax, f32, (rows,)))
+    if transposed and y is None and x.dtype is f32:
+        raise ValueError("y must be a tensor where the stream is fp32 and qt is wanted")
+    want_stats = stats is None and (want_stats or transposed)
+    given = (s is not None and out is not None and not want_stats
+             and (workspace is not None or not transposed))
+    with _on_device(dev, None if given else stream):
+        if s is None:
+            s = torch.empty_like(x)
+        if out is None:
+            out = (alloc_quantized(rows, cols, rowwise, dev) if transposed else
+                   Quantized(torch.empty((rows, cols), dtype=u8, device=dev), None,
+                             torch.empty(rows, dtype=f32, device=dev), None,
+                             torch.empty(rows, dtype=f32, device=dev)))
+        if want_stats:
+            stats = alloc_resnorm_stats(rows, dev, bool(norms & FP8L_POST_NORM), True, rms)
+        if transposed and workspace is None:
+            workspace = alloc_resnorm_workspace(rows, cols, dev, rowwise)
+        _check(lib().fp8_resnorm_quantize(
+            _pack_resnorm(b, x, s, y, post, pre, gate, pd, x.dtype, norms, alpha, eps, rms,
+                          stats or _NO_STATS),
+            _scaling(rowwise), _a(out.q), _a(out.qt) if transposed else None, _a(out.scale),
+            _a(out.scale_t) if transposed else None, _a(out.amax), *_ws(workspace, dev),
+            _stream(stream)), "fp8_resnorm_quantize")
+    return s, out, stats
+
+
+def fp8_resnorm_bwd(dy: Optional[torch.Tensor], ds: Optional[torch.Tensor], b: torch.Tensor,
+                    s: torch.Tensor, stats: ResNormStats, post=None, pre=None,
+                    gate: Optional[torch.Tensor] = None, alpha: float = 1.0, rms: bool = False,
+                    grads: Optional[ResNormGrads] = None, out: Optional[Quantized] = None,
+                    rowwise: bool = False, e5m2: bool = False,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> ResNormGrads:
+    """Gradients of fp8_resnorm_fwd from dy (of y, bf16; None without a pre norm)
+    and ds (of s from elsewhere, or None): dx, db and those of the parameters
+    that are tensors.  With ``grads`` given its tensors are written and nothing
+    else; with ``out`` given db is quantized into it (E5M2 when e5m2)."""
+    norms = ((FP8L_POST_NORM if post is not None else 0)
+             | (FP8L_PRE_NORM if pre is not None else 0))
+    post, pre, pd = _resnorm_params(b, post, pre, gate)
+    rows, cols = b.shape
+    bf, f32, dev, xd = torch.bfloat16, torch.float32, b.device, s.dtype
+    if xd not in _DTYPES:
+        raise ValueError("s must be a bf16 or fp32 matrix")
+    _checked(dev, ("b", b, bf, b.shape), ("s", s, xd, b.shape), ("dy", dy, bf, b.shape),
+             ("ds", ds, xd, b.shape), ("post weight", post[0], pd, (cols,)),
+             ("post bias", post[1], pd, (cols,)), ("pre weight", pre[0], pd, (cols,)),
+             ("pre bias", pre[1], pd, (cols,)), ("gate", gate, pd, (cols,)),
+             ("mean_post", stats.mean_post, f32, (rows,)),
+             ("rstd_post", stats.rstd_post, f32, (rows,)),
+             ("mean_pre", stats.mean_pre, f32, (rows,)),
+             ("rstd_pre", stats.rstd_pre, f32, (rows,)))
+    if grads is not None:
+        _checked(dev, ("dx", grads.dx, xd, b.shape), ("db", grads.db, bf, b.shape),
+                 *((n, getattr(grads, n), f32, (cols,)) for n in ResNormGrads.__slots__[2:]))
+    if out is not None:
+        # (without any of them the library takes the call for one that wants no codes)
+        if out.q is None or out.qt is None or out.scale is None or out.scale_t is None:
+            raise ValueError("out must have q, qt, scale and scale_t")
+        _checked(dev, *_quantized("db", out, rows, cols, rowwise))
+    z = out if out is not None else _NO_CODES
+    given = grads is not None and workspace is not None
+    with _on_device(dev, None if given else stream):
+        if grads is None:
+            new = lambda p: torch.empty(cols, dtype=f32, device=dev) if p is not None else None
+            grads = ResNormGrads(torch.empty_like(s), torch.empty_like(b), new(gate), new(post[0]),
+                                 new(post[1]), new(pre[0]), new(pre[1]))
+        if workspace is None:
+            workspace = alloc_resnorm_workspace(rows, cols, dev, rowwise)
+        g = _RESNORM_GRADS.pack(*(0 if v is None else v.data_ptr() for v in (
+            grads.dx, grads.db, grads.dgate, grads.dpost_weight, grads.dpost_bias,
+            grads.dpre_weight, grads.dpre_bias)))
+        _check(lib().fp8_resnorm_bwd(
+            _pack_resnorm(b, None, s, None, post, pre, gate, pd, xd, norms, alpha, 0.0, rms, stats),
+            _a(dy), _a(ds), g, _scaling(rowwise, e5m2), _a(z.q), _a(z.qt), _a(z.scale),
+            _a(z.scale_t), _a(z.amax), *_ws(workspace, dev), _stream(stream)), "fp8_resnorm_bwd")
+    return grads
 
 
 # ---------------------------------------------------- gated feed-forward --

@@ -506,6 +506,112 @@ FP8L_API int fp8_layernorm_bwd(const void *dy, const void *x, const void *weight
                                void *stream);
 
 /*
+ * Residual norm: what lies between two blocks of a residual stream.  The norm
+ * behind a block, its gate, the residual and the norm in front of the next block,
+ * as the producer of that block's fp8 operand, and their backward as the producer
+ * of the first block's fp8 output gradient.  With N the norm above (its kind and
+ * eps; each norm with its own weight and bias):
+ *
+ *   t = N(b; post_w, post_b)          (b itself without FP8L_POST_NORM)
+ *   s = alpha x + gate t              (rounded once to the stream's type)
+ *   y = N(s; pre_w, pre_b)            (bf16; none without FP8L_PRE_NORM)
+ *
+ * in fp32; y is the norm of s as it is stored.
+ *
+ *   rows, cols  any rows >= 0 and 1 <= cols <= FP8L_NORM_MAX_COLS; multiples of
+ *             16 where codes are written (below)
+ *   kind      FP8L_LAYERNORM or FP8L_RMSNORM, of both norms
+ *   norms     FP8L_POST_NORM, FP8L_PRE_NORM or both
+ *   dtype     FP8L_BF16 or FP8L_F32: type of the stream x, s (and ds, dx);
+ *             b and y (and db, dy) are bf16
+ *   pdtype    FP8L_BF16 or FP8L_F32: type of the parameters
+ *   alpha     finite; eps finite, >= 0
+ *   b [rows, cols], x [rows, cols]    (read)
+ *   post_w, post_b, pre_w, pre_b, gate  [cols], or NULL for 1 (biases: 0); those
+ *             of a norm that is not there are not read
+ *   s [rows, cols] (written), y [rows, cols] bf16 (written) or NULL
+ *   mean_*, rstd_*  [rows] fp32, the statistics of b and of s (written; each may
+ *             be NULL; those of a norm that is not there, and the means of
+ *             FP8L_RMSNORM, are not written)
+ *
+ * Non-finite values, 16-byte alignment, overlaps and the order of additions as
+ * for the norm above.
+ */
+#define FP8L_POST_NORM 1
+#define FP8L_PRE_NORM  2
+typedef struct fp8l_resnorm {
+    int64_t rows, cols;
+    int kind, norms, dtype, pdtype;
+    float alpha, eps;
+    const void *b, *x;
+    const void *post_w, *post_b, *pre_w, *pre_b, *gate;
+    void *s, *y;
+    float *mean_post, *rstd_post, *mean_pre, *rstd_pre;
+} fp8l_resnorm;
+
+/* Bytes of device workspace of fp8_resnorm_quantize with this scaling and of
+ * fp8_resnorm_bwd (one size serves both, and every smaller number of rows); 0
+ * for invalid arguments. */
+FP8L_API size_t fp8_resnorm_workspace_bytes(int64_t rows, int64_t cols, int scaling);
+
+/* s, y and the statistics.  (r is read during the call only.) */
+FP8L_API int fp8_resnorm_fwd(const fp8l_resnorm *r, void *stream);
+
+/*
+ * The same with fp8_linear_quantize's definition applied to y: codes E4M3,
+ * scaling FP8L_TENSORWISE or FP8L_ROWWISE.  norms has FP8L_PRE_NORM.
+ *
+ *   q, qt, scale, scale_t, amax_out  as fp8_linear_quantize's for x = y; rows and
+ *        cols are multiples of 16
+ *   y    NULL where only the codes are wanted: the cast then normalizes s again,
+ *        so the stream is bf16, and rstd_pre (and mean_pre, FP8L_LAYERNORM) must be
+ *        given.  An fp32 stream needs y.
+ *   qt = NULL (FP8L_ROWWISE only): no transposed copy and no scale_t, for
+ *        serving; amax_out is then [rows], any number of rows is valid, the
+ *        workspace is not used (it may be NULL), and y and the statistics are
+ *        optional whatever the stream
+ * The workspace's contents are undefined on entry and exit, not shared by calls
+ * in flight together.
+ */
+FP8L_API int fp8_resnorm_quantize(const fp8l_resnorm *r, int scaling, void *q, void *qt,
+                                  float *scale, float *scale_t, float *amax_out,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients, from the forward pass's b, s, parameters and statistics in r (x, y
+ * and eps are not used; means of FP8L_RMSNORM and statistics of a norm that is
+ * not there are not read).  xh_post = (b - mean_post) rstd_post, xh_pre = (s -
+ * mean_pre) rstd_pre, N' the norm's backward (dx of fp8_layernorm_bwd):
+ *
+ *   dT = ds + N'(dy; s, pre_w)              fp32, not rounded
+ *   dx = alpha dT                           (the stream's type)
+ *   db = N'(gate dT; b, post_w)             (bf16; gate dT without a post norm)
+ *   dgate = sum_r dT t,  dpost_w = sum_r gate dT xh_post,  dpost_b = sum_r gate dT,
+ *   dpre_w = sum_r dy xh_pre,  dpre_b = sum_r dy                      (fp32 [cols])
+ *
+ *   dy [rows, cols] bf16: the gradient of y; NULL exactly without FP8L_PRE_NORM
+ *   ds [rows, cols] of the stream's type: the gradient of s from elsewhere, or NULL
+ *      for 0 (FP8L_PRE_NORM only)
+ *   g  db must be given; dx and the parameters' gradients may each be NULL, and
+ *      those of a norm that is not there must be
+ *   q, qt, scale, scale_t, amax_out  the quantize of db (scaling as for
+ *      fp8_swiglu_bwd; rows and cols multiples of 16); all NULL: db is not
+ *      quantized
+ * The workspace is needed where a parameter's gradient or the codes are wanted.
+ * The order of the sums over rows is fixed: equal calls give equal bits.  With no
+ * rows they are zeros.
+ */
+typedef struct fp8l_resnorm_grads {
+    void *dx, *db;
+    float *dgate, *dpost_w, *dpost_b, *dpre_w, *dpre_b;
+} fp8l_resnorm_grads;
+
+FP8L_API int fp8_resnorm_bwd(const fp8l_resnorm *r, const void *dy, const void *ds,
+                             const fp8l_resnorm_grads *g, int scaling, void *q, void *qt,
+                             float *scale, float *scale_t, float *amax_out, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/*
  * The element conversion the quantize kernels use, exposed for testing it on
  * every fp32 input: out[i] = e4m3_sat_rne(in[i]) (definition above; a NaN
  * input gives a NaN code).  in: n fp32, out: n bytes, both device pointers.
