@@ -34,7 +34,8 @@ PEAK_HBM_GBS = 8000.0         # MI355X HBM3E
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "gemm_traffic.json")
 # gemm.hip and every file of this library that it includes
 GEMM_SOURCES = [os.path.join(ROOT, "float8_mixed_precision_amd", "csrc", f)
-                for f in ("gemm.hip", "fp8l_internal.h", "gemm_schedule.h", "gated.h")]
+                for f in ("gemm.hip", "fp8l_internal.h", "gemm_schedule.h", "gated.h", "act.h",
+                          "linear_act.h")]
 
 
 def parse():

@@ -137,6 +137,10 @@ bool overlapping(const Span (&spans)[N], int outs) {
   return false;
 }
 
+bool bad_act(int act, int pdtype) {
+  return act < FP8L_ACT_NONE || act > FP8L_ACT_RELU2 || (pdtype != FP8L_BF16 && pdtype != FP8L_F32);
+}
+
 bool bad_finite(float v) { return !(v >= -3.402823466e38f && v <= 3.402823466e38f); }
 
 // Checks of a residual norm's descriptor shared by its entry points, and the
@@ -482,6 +486,127 @@ int fp8_gated_bwd(const void *dyq, const float *sdy, const void *w2tq, const flo
       static_cast<const uint8_t *>(dyq), sdy, static_cast<const uint8_t *>(w2tq), sw2t,
       static_cast<const uint16_t *>(a), static_cast<const uint16_t *>(b), M, H, D, scaling,
       static_cast<uint16_t *>(da), static_cast<uint16_t *>(db), qa, qb, workspace,
+      static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FP8L_OK : FP8L_EHIP;
+}
+
+size_t fp8_linear_act_workspace_bytes(int64_t M, int64_t N, int scaling) {
+  if (M < 0 || M > (int64_t)1 << 30 || bad_dim(N) || bad_scaling(scaling)) return 0;
+  return fp8l::linear_act_workspace_bytes(M, N, scaling);
+}
+
+int fp8_linear_act_fwd(const void *xq, const float *sx, const void *wq, const float *sw,
+                       int64_t M, int64_t N, int64_t K, int scaling, const void *bias, int pdtype,
+                       int act, const void *residual, void *z, void *y, void *q, void *qt,
+                       float *scale, float *scale_t, float *amax_out, void *workspace,
+                       size_t workspace_bytes, void *stream) {
+  if (scaling != FP8L_TENSORWISE && scaling != FP8L_ROWWISE) return FP8L_EINVAL;
+  if (bad_act(act, pdtype)) return FP8L_EINVAL;
+  if (M < 0 || M > (int64_t)1 << 30 || bad_dim(N) || bad_dim(K)) return FP8L_ESHAPE;
+  if (bad_gemm_sizes(M, N, K)) return FP8L_ESHAPE;
+  const bool rw = scaling == FP8L_ROWWISE;
+  const bool quant = q || qt || scale || scale_t || amax_out;
+  const bool rows_only = quant && rw && !qt && !scale_t;
+  if (quant && !rows_only && M % 16 != 0) return FP8L_ESHAPE;
+  // y may be left out where z and its codes are written
+  if (M * N > 0 && !y && (!z || !quant || residual)) return FP8L_EINVAL;
+  int s = check_gemm_operands(xq, sx, wq, sw, y ? y : z, M, N, K);
+  if (s != FP8L_OK) return s;
+  if (misaligned(bias) || misaligned(residual) || misaligned(z)) return FP8L_EALIGN;
+  if (quant) {
+    if (rows_only) {
+      if (M * N > 0 && !q) return FP8L_EINVAL;
+      if (M > 0 && !scale) return FP8L_EINVAL;
+      if (misaligned(q)) return FP8L_EALIGN;
+      if (misaligned4(scale) || misaligned4(amax_out)) return FP8L_EALIGN;
+    } else {
+      s = check_quantize_args(y ? y : z, M, N, scaling, q, qt, scale, scale_t, amax_out);
+      if (s != FP8L_OK) return s;
+    }
+  }
+  if (!workspace) return FP8L_EINVAL;
+  const size_t need = fp8l::linear_act_workspace_bytes(M, N, scaling);
+  if (workspace_bytes < need) return FP8L_EWORKSPACE;
+  if (misaligned(workspace)) return FP8L_EALIGN;
+  const int64_t mn = M * N;
+  const int64_t sm = rw ? 4 * M : 4, sn = rw ? 4 * N : 4, st = rows_only ? 0 : sn;
+  const Span spans[] = {{z, 2 * mn}, {y, 2 * mn}, {q, mn}, {qt, mn}, {scale, sm}, {scale_t, st},
+                        {amax_out, rw ? sm + st : 4}, {workspace, (int64_t)need}, {xq, M * K},
+                        {wq, N * K}, {sx, sm}, {sw, sn},
+                        {bias, N * (pdtype == FP8L_F32 ? 4 : 2)},
+                        {residual == y ? nullptr : residual, 2 * mn}};
+  if (overlapping(spans, 8)) return FP8L_EINVAL;
+  const fp8l::LinearActIn in = {static_cast<const uint8_t *>(xq), static_cast<const uint8_t *>(wq),
+                                sx, sw, M, N, K, bias, pdtype == FP8L_F32, act,
+                                static_cast<const uint16_t *>(residual),
+                                static_cast<uint16_t *>(z), static_cast<uint16_t *>(y)};
+  const fp8l::Fp8Out o = {q, qt, scale, scale_t, amax_out};
+  const hipError_t e = fp8l::linear_act_fwd_launch(in, scaling, quant ? &o : nullptr, workspace,
+                                                   static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FP8L_OK : FP8L_EHIP;
+}
+
+int fp8_linear_act_bwd(const void *dyq, const float *sdy, const void *wtq, const float *swt,
+                       const void *z, int64_t M, int64_t H, int64_t D, int scaling, int act,
+                       void *dz, void *q, void *qt, float *scale, float *scale_t, float *amax_out,
+                       void *dbias, int pdtype, void *workspace, size_t workspace_bytes,
+                       void *stream) {
+  if (bad_scaling(scaling) || bad_act(act, pdtype)) return FP8L_EINVAL;
+  if (bad_dim(M) || bad_dim(H) || bad_dim(D)) return FP8L_ESHAPE;
+  if (bad_gemm_sizes(M, H, D)) return FP8L_ESHAPE;
+  int s = check_gemm_operands(dyq, sdy, wtq, swt, dz, M, H, D);
+  if (s == FP8L_OK) s = check_quantize_args(dz, M, H, scaling, q, qt, scale, scale_t, amax_out);
+  if (s != FP8L_OK) return s;
+  if (act == FP8L_ACT_NONE) z = nullptr;
+  else if (M * H > 0 && !z) return FP8L_EINVAL;
+  if (misaligned(z) || misaligned(dbias)) return FP8L_EALIGN;
+  if (!workspace) return FP8L_EINVAL;
+  const size_t need = fp8l::linear_act_workspace_bytes(M, H, scaling);
+  if (workspace_bytes < need) return FP8L_EWORKSPACE;
+  if (misaligned(workspace)) return FP8L_EALIGN;
+  const int64_t mh = M * H;
+  const bool rw = (scaling & FP8L_ROWWISE) != 0;
+  const int64_t sm = rw ? 4 * M : 4, sh = rw ? 4 * H : 4;
+  const Span spans[] = {{dz, 2 * mh}, {q, mh}, {qt, mh}, {scale, sm}, {scale_t, sh},
+                        {amax_out, rw ? sm + sh : 4}, {dbias, H * (pdtype == FP8L_F32 ? 4 : 2)},
+                        {workspace, (int64_t)need}, {dyq, M * D}, {wtq, H * D}, {sdy, sm},
+                        {swt, sh}, {z, 2 * mh}};
+  if (overlapping(spans, 8)) return FP8L_EINVAL;
+  const hipError_t e = fp8l::linear_act_bwd_launch(
+      static_cast<const uint8_t *>(dyq), sdy, static_cast<const uint8_t *>(wtq), swt,
+      static_cast<const uint16_t *>(z), act, M, H, D, scaling, static_cast<uint16_t *>(dz), dbias,
+      pdtype == FP8L_F32, {q, qt, scale, scale_t, amax_out}, workspace,
+      static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FP8L_OK : FP8L_EHIP;
+}
+
+int fp8_bias_act_bwd(const void *dy, const void *z, int64_t M, int64_t N, int scaling, int act,
+                     void *dz, void *q, void *qt, float *scale, float *scale_t, float *amax_out,
+                     void *dbias, int pdtype, void *workspace, size_t workspace_bytes,
+                     void *stream) {
+  if (bad_scaling(scaling) || bad_act(act, pdtype)) return FP8L_EINVAL;
+  int s = check_quantize_args(dy, M, N, scaling, q, qt, scale, scale_t, amax_out);
+  if (s != FP8L_OK) return s;
+  // (tiles of the pass and their column sums are counted in 32 bits)
+  if (M * N > (int64_t)1 << 38) return FP8L_ESHAPE;
+  if (act == FP8L_ACT_NONE) z = nullptr;
+  else if (M * N > 0 && (!z || !dz)) return FP8L_EINVAL;
+  if (misaligned(z) || misaligned(dz) || misaligned(dbias)) return FP8L_EALIGN;
+  if (!workspace) return FP8L_EINVAL;
+  const size_t need = fp8l::linear_act_workspace_bytes(M, N, scaling);
+  if (workspace_bytes < need) return FP8L_EWORKSPACE;
+  if (misaligned(workspace)) return FP8L_EALIGN;
+  const int64_t mn = M * N;
+  const bool rw = (scaling & FP8L_ROWWISE) != 0;
+  const int64_t sm = rw ? 4 * M : 4, sn = rw ? 4 * N : 4;
+  const Span spans[] = {{dz, 2 * mn}, {q, mn}, {qt, mn}, {scale, sm}, {scale_t, sn},
+                        {amax_out, rw ? sm + sn : 4}, {dbias, N * (pdtype == FP8L_F32 ? 4 : 2)},
+                        {workspace, (int64_t)need}, {dy, 2 * mn}, {z, 2 * mn}};
+  if (overlapping(spans, 8)) return FP8L_EINVAL;
+  const size_t maxima = fp8l::linear_act_maxima_bytes(M, N, scaling);
+  const hipError_t e = fp8l::bias_act_bwd_launch(
+      dy, z, act, M, N, scaling, dz, dbias, pdtype == FP8L_F32, {q, qt, scale, scale_t, amax_out},
+      workspace, reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + maxima),
       static_cast<hipStream_t>(stream));
   return e == hipSuccess ? FP8L_OK : FP8L_EHIP;
 }

@@ -186,8 +186,9 @@ struct CastSource {
   int nparts;
   const uint16_t *rowpart, *colpart;
   int row_slices, col_slices;
+  int act;                     // FP8L_ACT_*: quantized is act(x), rounded to bf16 (E4M3)
 };
-// count (1, or 2 without rstd) tensors of one shape and one count of partials, in
+// count (1, or 2 with neither rstd nor act) tensors of one shape and one count of partials, in
 // the same launches.
 hipError_t quantize_cast_launch(const CastSource *src, int count, int64_t rows, int64_t cols,
                                 int scaling, const Fp8Out *o, hipStream_t stream);
@@ -211,6 +212,45 @@ hipError_t norm_quantize_launch(const NormIn &in, int scaling, void *y, float *m
 hipError_t norm_bwd_launch(const void *dy, const NormIn &in, int f32, const float *mean,
                            const float *rstd, void *dx, float *dw, float *db, void *workspace,
                            hipStream_t stream);
+
+// Linear with its epilogue (linear_act.h).  y NULL: not stored (z is then); z
+// NULL: not stored.  o NULL: y is not quantized; o->qt NULL (rowwise): each row
+// alone, any M.
+struct LinearActIn {
+  const uint8_t *xq, *wq;
+  const float *sx, *sw;
+  int64_t M, N, K;
+  const void *bias;
+  int bias_f32, act;
+  const uint16_t *residual;
+  uint16_t *z, *y;
+};
+size_t linear_act_workspace_bytes(int64_t M, int64_t N, int scaling);
+// the part of it in front of the column sums
+size_t linear_act_maxima_bytes(int64_t M, int64_t N, int scaling);
+hipError_t linear_act_fwd_launch(const LinearActIn &in, int scaling, const Fp8Out *o,
+                                 void *workspace, hipStream_t stream);
+hipError_t linear_act_bwd_launch(const uint8_t *dyq, const float *sdy, const uint8_t *wtq,
+                                 const float *swt, const uint16_t *z, int act, int64_t M,
+                                 int64_t H, int64_t D, int scaling, uint16_t *dz, void *dbias,
+                                 int dbias_f32, const Fp8Out &o, void *workspace,
+                                 hipStream_t stream);
+
+// Elementwise passes around it (bias_act.h).  dz NULL: without an activation, not
+// stored.  maxima: bias_act_maxima_bytes; sums: fp32 [rows / AM_TR, rounded up][cols].
+size_t bias_act_maxima_bytes(int64_t rows, int64_t cols, int scaling);
+hipError_t bias_act_bwd_launch(const void *dy, const void *z, int act, int64_t rows, int64_t cols,
+                               int scaling, void *dz, void *dbias, int dbias_f32, const Fp8Out &o,
+                               void *maxima, float *sums, hipStream_t stream);
+// Sums of the columns of part[slices][cols], in a fixed order, to fp32 or bf16.
+hipError_t column_sums_launch(const float *part, int slices, int64_t cols, void *out, int f32,
+                              hipStream_t stream);
+// E4M3 quantize of act(x): of each row alone, and as quantize_launch's (workspace:
+// bias_act_maxima_bytes and quantize_workspace_bytes at least).
+hipError_t quantize_rows_launch(const void *x, int act, int64_t rows, int64_t cols,
+                                const Fp8Out &o, hipStream_t stream);
+hipError_t quantize_act_launch(const void *x, int act, int64_t rows, int64_t cols, int scaling,
+                               const Fp8Out &o, void *workspace, hipStream_t stream);
 
 // Residual norm (resnorm.h).  Parameters as above; post, pre: which norms there
 // are; f32: type of the stream (x, s, ds, dx).

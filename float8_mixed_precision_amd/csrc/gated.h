@@ -185,9 +185,11 @@ constexpr int T_STAGE = (TM + TB) * BK;            // 24 KB
 constexpr int T_STAGES = 3;
 
 template <int EPI, int FA, bool RW>
-__global__ __launch_bounds__(256) void k_gate_tile(GateArgs g) {
+__global__ __launch_bounds__(256) void k_gate_tile(typename ArgsOf<EPI>::type g) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[T_STAGES * T_STAGE];
-  constexpr bool GATE = EPI != EPI_DGATE;
+  constexpr bool GATE = is_gate(EPI);
+  constexpr bool ACT = is_act(EPI), DACT = is_dact(EPI);
+  constexpr int NOUT = EPI == EPI_DGATE ? 2 : 1;   // tensors that are quantized
   constexpr int TN = GATE ? TB / 2 : TB;           // output columns of the tile
   constexpr int WC = TN / 2;                       // of a wave
   constexpr int NJ = WC / FR;                      // output blocks of a wave along n
@@ -247,7 +249,30 @@ __global__ __launch_bounds__(256) void k_gate_tile(GateArgs g) {
   const int mrow = m0 + wm * 32 + l16;
   const int ncol = n0 + wn * WC + g4 * 4;
   uint2 ga[GATE ? 1 : NJ][2], gb[GATE ? 1 : NJ][2];
-  if constexpr (!GATE) {
+  float bias[ACT ? NJ : 1][4];
+  if constexpr (ACT || DACT) {
+    // the residual or z, and the bias
+    const uint16_t *in = ACT ? g.res : g.act.act != FP8L_ACT_NONE ? g.a : nullptr;
+    if (in) {                                      // uniform
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          ga[j][i] = *reinterpret_cast<const uint2 *>(
+              in + (size_t)min(mrow + i * FR, M - 1) * N + min(ncol + j * FR, N - 4));
+    }
+    if constexpr (ACT) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          const float2 b = bias_pair(g, ncol + j * FR + e);
+          bias[j][e] = b.x;
+          bias[j][e + 1] = b.y;
+        }
+    }
+  }
+  if constexpr (EPI == EPI_DGATE) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -266,7 +291,7 @@ __global__ __launch_bounds__(256) void k_gate_tile(GateArgs g) {
     for (int e = 0; e < 4; ++e) {
       const int at = RW ? min(ncol + j * FR + e, N - 1) : 0;
       ib[j][e] = g.sb[0][at];
-      ib2[j][e] = GATE ? g.sb2[at] : 1.f;
+      if constexpr (GATE) ib2[j][e] = g.sb2[at];
     }
   fill(0);
   if (nk > 1) fill(1);
@@ -300,6 +325,7 @@ __global__ __launch_bounds__(256) void k_gate_tile(GateArgs g) {
   uint16_t *C = static_cast<uint16_t *>(g.C[0]);
   uint32_t rm[2][2] = {};                          // [output][i]: row maxima (u16 pairs)
   uint2 cm[2][NJ] = {};                            // [output][j]: column maxima
+  float cs[DACT ? NJ : 1][4] = {};                 // column sums
 #pragma unroll
   for (int i = 0; i < 2; ++i) ia[i] = 1.0f / ia[i];
 #pragma unroll
@@ -319,7 +345,7 @@ __global__ __launch_bounds__(256) void k_gate_tile(GateArgs g) {
       const uint2 pa =
           make_uint2(bf16x2_bits((p[0] * ia[i]) * ib[j][0], (p[1] * ia[i]) * ib[j][1]),
                      bf16x2_bits((p[2] * ia[i]) * ib[j][2], (p[3] * ia[i]) * ib[j][3]));
-      uint2 o[2];
+      uint2 o[2] = {};
       if constexpr (GATE) {
         const v4f r = acc[j + NJ][i];
         const uint2 pb =
@@ -331,6 +357,30 @@ __global__ __launch_bounds__(256) void k_gate_tile(GateArgs g) {
         }
         o[0] = make_uint2(gate_fwd2(pa.x, pb.x), gate_fwd2(pa.y, pb.y));
         if (ok) *reinterpret_cast<uint2 *>(C + at) = o[0];
+      } else if constexpr (ACT) {
+        float f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = add32((p[e] * ia[i]) * ib[j][e], bias[j][e]);
+        const uint2 r = g.res ? ga[j][i] : make_uint2(0u, 0u);
+        uint2 z;
+        o[0] = act_out4<EPI - EPI_ACT>(g.act, f, g.res != nullptr, r, z);
+        if (ok && g.a) *reinterpret_cast<uint2 *>(g.a + at) = z;
+        if (ok && C) *reinterpret_cast<uint2 *>(C + at) = o[0];
+      } else if constexpr (DACT) {
+        float f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = (p[e] * ia[i]) * ib[j][e];
+        if (g.act.act != FP8L_ACT_NONE) {          // uniform
+          const float z[4] = {bf16_lo(ga[j][i].x), bf16_hi(ga[j][i].x), bf16_lo(ga[j][i].y),
+                              bf16_hi(ga[j][i].y)};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[e] *= act_slope<EPI - EPI_DACT>(g.act, z[e]);
+        }
+        o[0] = make_uint2(bf16x2_bits(f[0], f[1]), bf16x2_bits(f[2], f[3]));
+        if (ok) *reinterpret_cast<uint2 *>(C + at) = o[0];
+        // (a row past M repeats the last one)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) cs[j][e] += ok ? f[e] : 0.f;
       } else {
         gate_bwd2(pa.x, ga[j][i].x, gb[j][i].x, o[0].x, o[1].x);
         gate_bwd2(pa.y, ga[j][i].y, gb[j][i].y, o[0].y, o[1].y);
@@ -341,16 +391,33 @@ __global__ __launch_bounds__(256) void k_gate_tile(GateArgs g) {
       }
       const uint32_t keep = ok ? 0x7FFF7FFFu : 0u;
 #pragma unroll
-      for (int k = 0; k < (GATE ? 1 : 2); ++k) {
+      for (int k = 0; k < NOUT; ++k) {
         const uint32_t v0 = o[k].x & keep, v1 = o[k].y & keep;
         rm[k][i] = pk_max(rm[k][i], pk_max(v0, v1));
         if (RW) cm[k][j] = make_uint2(pk_max(cm[k][j].x, v0), pk_max(cm[k][j].y, v1));
       }
     }
   }
+  if constexpr (DACT) {
+    if (g.colsum) {                                // uniform
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        // the 16 rows of a block add up in a fixed order
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+#pragma unroll
+          for (int w = 1; w < 16; w <<= 1) cs[j][e] += __shfl_xor(cs[j][e], w);
+        }
+        const int n = ncol + j * FR;
+        if (l16 == 0 && n < N)
+          *reinterpret_cast<v4f *>(g.colsum + (size_t)(m0 / TM * 2 + wm) * N + n) =
+              (v4f){cs[j][0], cs[j][1], cs[j][2], cs[j][3]};
+      }
+    }
+  }
   if (!g.maxima) return;                           // uniform
 #pragma unroll
-  for (int k = 0; k < (GATE ? 1 : 2); ++k) {
+  for (int k = 0; k < NOUT; ++k) {
     if (RW) {
       const int tile_n = n0 / TN, tile_m = m0 / TM;
 #pragma unroll

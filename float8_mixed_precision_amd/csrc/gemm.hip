@@ -78,8 +78,11 @@
 // precision.  The result therefore differs from a sequential fp32 sum by
 // more than rounding order where a group holds products 14 or more binades
 // apart; the parity tests bound that difference per element.
+#include "act.h"
 #include "fp8l_internal.h"
 #include "gemm_schedule.h"
+
+#include <type_traits>
 
 namespace fp8l {
 #ifdef FP8L_PHASE_TIMING
@@ -204,14 +207,26 @@ static_assert(sizeof(GemmGroup) <= 4096, "kernel arguments");
 //             bf16, as the plain GEMM writes it) and the forward pass's a and
 //             b read where the tile is finished, C receives
 //             da = dh * b * silu'(a), C2 receives db = dh * silu(a).
-// Both forms take the amax partial maxima of what they write (of h, or of da
+//  EPI_ACT + form   a linear with its epilogue (linear_act.h): z = A B^T + bias,
+//             C receives y = act(z) + residual (either optional), `a` receives z.
+//             act applies to the bf16 z; without one z is not rounded first.  C may
+//             be NULL (y is then only measured).
+//  EPI_DACT + form  its backward behind the next linear's product: with dh = A
+//             B^T (not rounded) and z read from `a` where the tile is finished, C
+//             receives dz = dh act'(z), colsum the sums of the unrounded dz over
+//             each wave's rows, [slice][N].
+//             (form: ACT_PW, ACT_SIG or ACT_ERF of act.h)
+// The gate's forms take the amax partial maxima of what they write (of h, or of da
 // and db) where `maxima` is set: tensorwise one u32 per wave of the launch in
 // part[o], rowwise the row maxima over each wave's columns in
 // rowpart[o][slice][M] and the column maxima over its rows in
 // colpart[o][slice][N], one slice per wave column / wave row of the tiles
-// (EPI_DGATE takes them always).
+// (EPI_DGATE takes them always).  EPI_ACT (of y) and EPI_DACT (of dz) do likewise.
 constexpr int EPI_NONE = 0, EPI_GATE = 1, EPI_GATE_AB = 2, EPI_DGATE = 3;
+constexpr int EPI_ACT = 4, EPI_DACT = 8;
 constexpr bool is_gate(int epi) { return epi == EPI_GATE || epi == EPI_GATE_AB; }
+constexpr bool is_act(int epi) { return epi >= EPI_ACT && epi < EPI_ACT + 3; }
+constexpr bool is_dact(int epi) { return epi >= EPI_DACT && epi < EPI_DACT + 3; }
 struct GateArgs : GemmGroup {
   const uint8_t *B2;           // is_gate(EPI)
   const float *sb2;
@@ -221,13 +236,18 @@ struct GateArgs : GemmGroup {
   uint32_t *part[2];
   uint16_t *rowpart[2], *colpart[2];
 };
+struct ActArgs : GateArgs {    // a: z
+  const void *bias;            // [N], fp32 with bias_f32, else bf16; NULL: none
+  int bias_f32;
+  const uint16_t *res;         // residual [M, N], or NULL
+  ActConsts act;
+  float *colsum;               // EPI_DACT; NULL: not wanted
+};
 template <int EPI>
 struct ArgsOf {
-  typedef GateArgs type;
-};
-template <>
-struct ArgsOf<EPI_NONE> {
-  typedef GemmGroup type;
+  typedef typename std::conditional<
+      EPI == EPI_NONE, GemmGroup,
+      typename std::conditional<is_act(EPI) || is_dact(EPI), ActArgs, GateArgs>::type>::type type;
 };
 
 // silu(x) = x s and silu'(x) = s + x s (1 - s), s = 1 / (1 + e^-x), in fp32
@@ -444,6 +464,29 @@ __device__ __forceinline__ void store_colmax(const uint32_t (&cm)[4], int lane, 
   if (lane < LANES && col_ok) *reinterpret_cast<v4u *>(dst) = r;
 }
 
+// Two bias values from column n (even) on, clamped into the vector (the outputs
+// past it are not stored).
+__device__ __forceinline__ float2 bias_pair(const ActArgs &g, int n) {
+  if (!g.bias) return make_float2(0.f, 0.f);      // uniform
+  n = min(n, g.N[0] - 2);
+  if (g.bias_f32) return *reinterpret_cast<const float2 *>(static_cast<const float *>(g.bias) + n);
+  const uint32_t w = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(g.bias) + n);
+  return make_float2(bf16_lo(w), bf16_hi(w));
+}
+
+// eight bf16 values
+__device__ __forceinline__ void unpack8(float (&f)[8], v4u w) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    f[2 * d] = bf16_lo(w[d]);
+    f[2 * d + 1] = bf16_hi(w[d]);
+  }
+}
+__device__ __forceinline__ v4u pack8(const float (&f)[8]) {
+  return (v4u){bf16x2_bits(f[0], f[1]), bf16x2_bits(f[2], f[3]), bf16x2_bits(f[4], f[5]),
+               bf16x2_bits(f[6], f[7])};
+}
+
 // KFULL: K % 128 == 0 (no K tail, no per-chunk K check).  RW: rowwise
 // scales (sa[M], sb[N]) instead of one scale per operand.  F32: fp32 output
 // (the scaled value before bf16 rounding) instead of bf16.  FA: code format
@@ -464,7 +507,9 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
   // stores every lane has certainly issued after an epilogue began, which the
   // next tile's first wait may leave in flight; 48 of EPI_DGATE's 64 (the
   // counter has 6 bits)
-  constexpr int IN_FLIGHT = EPI == EPI_GATE ? 16 : EPI == EPI_NONE ? EPI_STORES : 48;
+  // (EPI_ACT: y's or z's 32, EPI_DACT: dz's)
+  constexpr int IN_FLIGHT = EPI == EPI_GATE ? 16
+                            : EPI == EPI_NONE || is_act(EPI) || is_dact(EPI) ? EPI_STORES : 48;
   // columns of the output per tile
   constexpr int TN = is_gate(EPI) ? BN / 2 : BN;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[EPI_OFF + EPI_BYTES];
@@ -733,6 +778,12 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
   // pairs per lane) wait in its staging, which frees their registers for the
   // main loop
 #define FP8P_TMAX() (reinterpret_cast<uint2 *>(epi) + hw_lane())
+  // EPI_ACT: the bias of the wave's 128 columns, fp32.  Rowwise it takes the part
+  // of the tile's scale table that holds the other waves' rows (a wave reads its
+  // own 128 rows and columns there, and the table fills again only after this
+  // tile's epilogue); tensorwise the second KB.
+#define FP8P_BIAS_TAB(TILE)                                                       \
+  reinterpret_cast<float2 *>(epi + (RW ? ((TILE) & 1) * SCALE_BYTES + (1 - wm) * WM * 4 : 1024))
   if (EPI != EPI_NONE && !RW) *FP8P_TMAX() = make_uint2(0u, 0u);
   int st = 0;          // stage of the current unit
   for (int tile = 0;; ++tile) {
@@ -795,6 +846,9 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
       sn_ = gate_scales(g, hw_lane(), m0 + wm * WM, n0 + wn * (WN / 2));          \
       rn_ = reinterpret_cast<v4f *>(epi) + hw_lane();                             \
     }                                                                             \
+    float2 bias_ = {};                                                            \
+    if constexpr (is_act(EPI))                                                    \
+      bias_ = bias_pair(g, n0 + wn * WN + hw_lane() * 2);                         \
     FP8P_H1(st, MF)                                                               \
     if (nk == 1 && !F32 && !RW)                                                   \
       wait_vmcnt<IN_FLIGHT>();                                                    \
@@ -806,6 +860,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
       rn_ = FP8P_RCP_AT((tile + 1) & 1);                                          \
       sn_ = *rn_;                                                                 \
     }                                                                             \
+    if constexpr (is_act(EPI)) FP8P_BIAS_TAB(tile)[hw_lane()] = bias_;            \
     FP8P_H2D(st, MF, if (RW) sn_ = recip4(sn_), if (RW) *rn_ = sn_)               \
     FP8P_DADV();                                                                  \
     st ^= 1;                                                                      \
@@ -855,8 +910,9 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
     // ---- epilogue: scale, round, stage 32 rows of the wave's 128 x 128 tile
     // at a time in the wave's 8 KB (row r's 16-byte chunk c at c ^ (r % 16),
     // its 8-byte halves swapped where r % 16 >= 8), write whole rows
+    // (EPI_ACT without a y: stores to an empty buffer are dropped)
     const __amdgpu_buffer_rsrc_t rsC = __builtin_amdgcn_make_buffer_rsrc(
-        pick(g.C, pi), (short)0, M * N * (F32 ? 4 : 2), 0x00020000);
+        pick(g.C, pi), (short)0, is_act(EPI) && !g.C[0] ? 0 : M * N * (F32 ? 4 : 2), 0x00020000);
     const int lane_e = hw_lane();
     const int ml16 = lane_e & 15;                 // row within a 16-row block
     const int nq = (lane_e >> 4) * 4;             // first of the lane's 4 columns in a block
@@ -1101,6 +1157,168 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
         store_colmax<16>(cm[0], lane_e, col_ok, g.colpart[0] + at);
         store_colmax<16>(cm[1], lane_e, col_ok, g.colpart[1] + at);
       }
+    } else if constexpr (is_act(EPI) || is_dact(EPI)) {
+      // The tile's columns in two halves of 64, one 16-row block per pass, staged
+      // as fp32 in 4 KB (16 rows x 256 B, row r's 16-byte chunk c at c ^ r) and
+      // taken up by rows: lane l has columns 8 (l % 8) .. + 7 of rows l / 8 and
+      // l / 8 + 8.  The next pass is staged and read back, and its part of the
+      // residual or of z loaded, before this one is computed.
+      constexpr bool ACT = is_act(EPI);
+      constexpr int FORM = EPI - (ACT ? EPI_ACT : EPI_DACT);
+      uint8_t *sf = epi + RW_STAGE_OFF;
+      const bool has_z = ACT ? g.a != nullptr : g.act.act != FP8L_ACT_NONE;
+      const bool has_in = ACT ? g.res != nullptr : has_z;     // uniform
+      const __amdgpu_buffer_rsrc_t rsZ =
+          __builtin_amdgcn_make_buffer_rsrc(g.a, (short)0, g.a ? M * N * 2 : 0, 0x00020000);
+      const __amdgpu_buffer_rsrc_t rsIn =
+          ACT ? __builtin_amdgcn_make_buffer_rsrc((void *)g.res, (short)0,
+                                                  g.res ? M * N * 2 : 0, 0x00020000)
+              : rsZ;
+      const __amdgpu_buffer_rsrc_t rsRow = __builtin_amdgcn_make_buffer_rsrc(
+          RW ? g.rowpart[0] + (size_t)((n0 / BN) * 2 + wn) * M : nullptr, (short)0,
+          RW && g.maxima ? M * 2 : 0, 0x00020000);
+      const int r8 = lane_e >> 3;
+      const int row0 = m0 + wm * WM + r8;
+      // (the whole offset is checked against the resource, which drops rows past M)
+      const uint32_t row_at = (lane_e & 7) == 0 ? (uint32_t)row0 * 2 : OOB_C;
+      uint32_t tmax = RW ? 0u : FP8P_TMAX()->x;
+      // row maxima of the left half wait here for the right one's
+      uint32_t rmax[RW ? NF : 1][2];
+#pragma unroll
+      for (int jh = 0; jh < 2; ++jh) {
+        const int scol = n0 + wn * WN + jh * 64 + (lane_e & 7) * 8;
+        const bool col_ok = scol < N;
+        const uint32_t off0 = ((uint32_t)row0 * (uint32_t)N + (uint32_t)scol) * 2u;
+        const int rows_left = col_ok ? M - row0 : 0;
+        auto offset = [&](int i, int u) { return i * FR + u * 8 < rows_left ? off0 : OOB_C; };
+        auto row_off = [&](int i, int u) { return (uint32_t)(i * FR + u * 8) * (uint32_t)N * 2u; };
+        v4u in[2][2];
+        v4f v[2][2][2];
+        auto load_in = [&](int i) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            in[i & 1][u] =
+                __builtin_amdgcn_raw_buffer_load_b128(rsIn, offset(i, u), row_off(i, u), 0);
+        };
+        auto stage = [&](int i) {
+          const float ia = RW ? tab[wm * WM + i * FR + ml16] : inv_ar[i];
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj) {
+            const int j = jh * 4 + jj;
+            const v4f ib = RW ? *reinterpret_cast<const v4f *>(tab + BM + wn * WN + j * FR + nq)
+                              : inv_br[j];
+            const v4f x = acc[j][i];
+            *reinterpret_cast<v4f *>(sf + ml16 * 256 + ((jj * 4 + (nq >> 2)) ^ ml16) * 16) =
+                (v4f){(x[0] * ia) * ib[0], (x[1] * ia) * ib[1], (x[2] * ia) * ib[2],
+                      (x[3] * ia) * ib[3]};
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int r = u * 8 + r8;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              v[i & 1][u][e] = *reinterpret_cast<const v4f *>(
+                  sf + r * 256 + ((2 * (lane_e & 7) + e) ^ r) * 16);
+          }
+        };
+        if (has_in) load_in(0);
+        stage(0);
+        float bias[8];
+        if (ACT) {
+          const v4f *bt = reinterpret_cast<const v4f *>(FP8P_BIAS_TAB(tile)) + jh * 16 +
+                          (lane_e & 7) * 2;
+          const v4f b0 = bt[0], b1 = bt[1];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            bias[e] = b0[e];
+            bias[4 + e] = b1[e];
+          }
+        }
+        uint32_t cm[4] = {0, 0, 0, 0};
+        float cs[8] = {};
+#pragma unroll
+        for (int i = 0; i < NF; ++i) {
+          if (i + 1 < NF) {
+            if (has_in) load_in(i + 1);
+            stage(i + 1);
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t off = offset(i, u);
+            const uint32_t keep = off != OOB_C ? 0x7FFF7FFFu : 0u;
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = v[i & 1][u][e >> 2][e & 3];
+            v4u y;
+            if constexpr (ACT) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) f[e] = add32(f[e], bias[e]);
+              y = pack8(f);                       // z
+              if (has_z)
+                __builtin_amdgcn_raw_buffer_store_b128(y, rsZ, off, row_off(i, u), C_STORE_AUX);
+              if (FORM != ACT_PW || g.act.act != FP8L_ACT_NONE) {
+                unpack8(f, y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = act_value<FORM>(g.act, f[e]);
+                if (!has_in) y = pack8(f);
+              }
+              if (has_in) {
+                float r[8];
+                unpack8(r, in[i & 1][u]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = add32(f[e], r[e]);
+                y = pack8(f);
+              }
+            } else {
+              if (has_in) {
+                float z[8];
+                unpack8(z, in[i & 1][u]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] *= act_slope<FORM>(g.act, z[e]);
+              }
+              y = pack8(f);
+              // (a row past M has no scale)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) cs[e] += keep ? f[e] : 0.f;
+            }
+            __builtin_amdgcn_raw_buffer_store_b128(y, rsC, off, row_off(i, u), C_STORE_AUX);
+            uint32_t rm = 0;
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+              const uint32_t x = y[d] & keep;
+              rm = pk_max(rm, x);
+              if (RW) cm[d] = pk_max(cm[d], x);
+            }
+            if (!RW) tmax = pk_max(tmax, rm);
+            if (RW) {
+              if (jh == 0) {
+                rmax[i][u] = rm;
+              } else {
+                rm = lanes_max<8>(hmax16(pk_max(rm, rmax[i][u])));
+                __builtin_amdgcn_raw_buffer_store_b16((unsigned short)rm, rsRow,
+                                                      row_at + (i * FR + u * 8) * 2, 0, 0);
+              }
+            }
+          }
+        }
+        if (RW && g.maxima)
+          store_colmax<8>(cm, lane_e, col_ok,
+                          g.colpart[0] + (size_t)((m0 / BM) * 2 + wm) * N + scol);
+        if (!ACT && g.colsum) {
+          // the lanes of a column add up in a fixed order
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+#pragma unroll
+            for (int o = 8; o < 64; o <<= 1) cs[e] += __shfl_xor(cs[e], o);
+          }
+          if (lane_e < 8 && col_ok) {
+            v4f *dst = reinterpret_cast<v4f *>(g.colsum + (size_t)((m0 / BM) * 2 + wm) * N + scol);
+            dst[0] = (v4f){cs[0], cs[1], cs[2], cs[3]};
+            dst[1] = (v4f){cs[4], cs[5], cs[6], cs[7]};
+          }
+        }
+      }
+      if (!RW) FP8P_TMAX()->x = tmax;
     } else if (RW && F32) {
       // rowwise fp32: the tile's columns in two halves of 64, one 16-row
       // block per pass: 16 rows x 256 B (row r's 16-byte chunk c at
@@ -1312,6 +1530,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
       }
     }
   }
+#undef FP8P_BIAS_TAB
 #undef FP8P_TMAX
 #undef FP8P_H2D
 #undef FP8P_H2
@@ -1478,6 +1697,7 @@ hipError_t gemm_f32_launch(const uint8_t *A, const float *sa, const uint8_t *B,
 }  // namespace fp8l
 
 #include "gated.h"
+#include "linear_act.h"
 
 #ifdef FP8L_PHASE_TIMING
 // Copies the first `bytes` of the timestamp array (8 u64 per workgroup:

@@ -1,0 +1,278 @@
+// A Float8 linear with its epilogue on gfx950: bias, activation and residual where
+// the output tile is finished, and the gradient through the activation where the
+// next linear's product is.
+//
+//   z = x W^T + bias,  y = act(z) + residual        (act of the bf16 z)
+//   dz = (dy W2) act'(z),  dbias = sum_m dz
+//
+// Large M: the persistent GEMM with EPI_ACT / EPI_DACT (gemm.hip).  Where its tiles
+// are too few, the small tiles of gated.h with the same forms.  Few tokens: below.
+// The activations: act.h.
+//
+// Part of gemm.hip (included at its end).
+#pragma once
+
+namespace fp8l {
+namespace {
+
+// ---------------------------------------------------------- few tokens --
+//
+// As k_gated_skinny with one weight: a workgroup owns 16 columns of y, its 8
+// waves split the contraction and join through LDS, weights go straight from
+// memory to the matrix instruction's operands.
+struct ActSkinnyArgs {
+  const uint8_t *x, *w;
+  const float *sx, *sw;
+  ActArgs e;                   // bias, res, act, a (z), C[0] (y), N[0]
+  int M, N, K, rowwise;
+};
+
+template <bool KFULL, int FORM>
+__global__ __launch_bounds__(64 * SK_WAVES) void k_act_skinny(ActSkinnyArgs p) {
+  __shared__ v4f red[SK_WAVES][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6;
+  const int n0 = blockIdx.x * 16;
+  const int K = p.K;
+  const int nk = (K + BK - 1) / BK;
+  const int kl = (lane >> 4) * 16;
+  const uint8_t *rw = p.w + (size_t)(n0 + (lane & 15)) * K;
+  const uint8_t *rx = p.x + (size_t)min(lane & 15, p.M - 1) * K;
+  v4f acc = {0.f, 0.f, 0.f, 0.f};
+  for (int t0 = wave; t0 < nk; t0 += SK_WAVES * SK_UNROLL) {
+    v4u fw[SK_UNROLL][2], fx[SK_UNROLL][2];
+#pragma unroll
+    for (int u = 0; u < SK_UNROLL; ++u) {
+      const int t = t0 + u * SK_WAVES;            // past the end: loaded again, not used
+      const int k = (t < nk ? t : t0) * BK + kl;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        fw[u][e] = row_chunk<KFULL>(rw, k + e * 64, K);
+        fx[u][e] = row_chunk<KFULL>(rx, k + e * 64, K);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < SK_UNROLL; ++u)
+      if (t0 + u * SK_WAVES < nk)                 // wave-uniform
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            frag(fw[u][0], fw[u][1]), frag(fx[u][0], fx[u][1]), acc, 0, 0, 0, 0, 0, 0);
+  }
+  red[wave][lane] = acc;
+  __syncthreads();
+  // lane l of the first wave: token l % 16, columns n0 + 4 (l / 16) ...
+  const int m = lane & 15;
+  const int n = n0 + (lane >> 4) * 4;
+  if (wave > 0 || m >= p.M) return;
+  v4f a = red[0][lane];
+#pragma unroll
+  for (int w = 1; w < SK_WAVES; ++w) a += red[w][lane];
+  const float ia = 1.0f / p.sx[p.rowwise ? m : 0];
+  const size_t at = (size_t)m * p.N + n;
+  float f[4];
+#pragma unroll
+  for (int j = 0; j < 4; j += 2) {
+    const float2 b = bias_pair(p.e, n + j);
+    f[j] = add32((a[j] * ia) * (1.0f / p.sw[p.rowwise ? n + j : 0]), b.x);
+    f[j + 1] = add32((a[j + 1] * ia) * (1.0f / p.sw[p.rowwise ? n + j + 1 : 0]), b.y);
+  }
+  uint2 r = make_uint2(0u, 0u), z;
+  if (p.e.res) r = *reinterpret_cast<const uint2 *>(p.e.res + at);
+  const uint2 y = act_out4<FORM>(p.e.act, f, p.e.res != nullptr, r, z);
+  if (p.e.a) *reinterpret_cast<uint2 *>(p.e.a + at) = z;
+  if (p.e.C[0]) *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.e.C[0]) + at) = y;
+}
+
+bool act_few_tokens(int64_t M, int64_t N) { return few_tokens(M, N); }
+
+template <int FORM>
+hipError_t act_skinny_launch(const ActSkinnyArgs &p, hipStream_t stream) {
+  const dim3 grid((unsigned)(p.N / 16)), block(64 * SK_WAVES);
+  if (p.K % BK == 0)
+    hipLaunchKernelGGL((k_act_skinny<true, FORM>), grid, block, 0, stream, p);
+  else
+    hipLaunchKernelGGL((k_act_skinny<false, FORM>), grid, block, 0, stream, p);
+  return hipGetLastError();
+}
+
+// An empty contraction: z = bias (EPI_ACT).  One thread per 8 values.
+template <int FORM>
+__global__ __launch_bounds__(256) void k_act_k0(ActArgs g, int64_t n8) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n8) return;
+  const int n = (int)(i * 8 % g.N[0]);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float2 b0 = bias_pair(g, n + 4 * h), b1 = bias_pair(g, n + 4 * h + 2);
+    const float f[4] = {b0.x, b0.y, b1.x, b1.y};
+    const size_t at = (size_t)i * 8 + 4 * h;
+    uint2 r = make_uint2(0u, 0u), z;
+    if (g.res) r = *reinterpret_cast<const uint2 *>(g.res + at);
+    const uint2 y = act_out4<FORM>(g.act, f, g.res != nullptr, r, z);
+    if (g.a) *reinterpret_cast<uint2 *>(g.a + at) = z;
+    if (g.C[0]) *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(g.C[0]) + at) = y;
+  }
+}
+
+// ------------------------------------------------------------- launches --
+
+// f(form) for an activation
+template <class F>
+hipError_t with_form(int act, F f) {
+  switch (act_form(act)) {
+    case ACT_SIG: return f(std::integral_constant<int, ACT_SIG>());
+    case ACT_ERF: return f(std::integral_constant<int, ACT_ERF>());
+    default: return f(std::integral_constant<int, ACT_PW>());
+  }
+}
+
+// Slices of the column sums that a call's kernel writes.
+int act_slices(int64_t M, int64_t N) { return (int)col_slices(small_tiles(M, N, BN), M); }
+
+// One problem, as launch_gate.
+template <int EPI, int FA>
+hipError_t launch_act(ActArgs &g, bool rowwise, int *nparts, hipStream_t stream) {
+  g.count = 1;
+  if (small_tiles(g.M[0], g.N[0], BN)) {
+    g.tiles_m[0] = (int)tiles(g.M[0], TM);
+    g.tiles_n[0] = (int)tiles(g.N[0], TB);
+    g.total = *nparts = g.tiles_m[0] * g.tiles_n[0];
+    if (rowwise)
+      hipLaunchKernelGGL((k_gate_tile<EPI, FA, true>), dim3((unsigned)g.total), dim3(256), 0,
+                         stream, g);
+    else
+      hipLaunchKernelGGL((k_gate_tile<EPI, FA, false>), dim3((unsigned)g.total), dim3(256), 0,
+                         stream, g);
+    return hipGetLastError();
+  }
+  g.tiles_m[0] = (int)tiles(g.M[0], BM);
+  g.tiles_n[0] = (int)tiles(g.N[0], BN);
+  g.total = g.tiles_m[0] * g.tiles_n[0];
+  constexpr int kComputeUnits = 256;
+  const int blocks = g.total < kComputeUnits ? g.total : kComputeUnits;
+  *nparts = blocks * 4;                           // one per wave
+  const bool kfull = g.K[0] % BK == 0;
+  auto kern = rowwise ? (kfull ? k_gemm_fp8_pers<true, true, false, FA, false, EPI>
+                               : k_gemm_fp8_pers<false, true, false, FA, false, EPI>)
+                      : (kfull ? k_gemm_fp8_pers<true, false, false, FA, false, EPI>
+                               : k_gemm_fp8_pers<false, false, false, FA, false, EPI>);
+  hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(THREADS), 0, stream, g);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// The workspace: the maxima (this kernel's, or those of a pass of its own), then
+// the column sums.
+size_t linear_act_maxima_bytes(int64_t M, int64_t N, int scaling) {
+  size_t b = gate_share_bytes(M, N, (scaling & FP8L_ROWWISE) != 0, BN);
+  for (const size_t q : {quantize_workspace_bytes((M + 15) / 16 * 16, N, scaling),
+                         bias_act_maxima_bytes(M, N, scaling)})
+    if (b < q) b = q;
+  return (b + 255) & ~(size_t)255;
+}
+
+size_t linear_act_workspace_bytes(int64_t M, int64_t N, int scaling) {
+  // column sums: a slice per 32 rows at most (small tiles)
+  const size_t sums = (size_t)(2 * tiles(M, TM)) * (size_t)N * sizeof(float);
+  return linear_act_maxima_bytes(M, N, scaling) + ((sums + 255) & ~(size_t)255);
+}
+
+hipError_t linear_act_fwd_launch(const LinearActIn &in, int scaling, const Fp8Out *o,
+                                 void *workspace, hipStream_t stream) {
+  const bool rw = (scaling & FP8L_ROWWISE) != 0;
+  const int64_t M = in.M, N = in.N, K = in.K;
+  // (what is quantized: z stands for y where there is no activation)
+  const void *y = in.y ? in.y : in.z;
+  const int cast_act = in.y ? FP8L_ACT_NONE : in.act;
+  ActArgs g = {};
+  g.A[0] = in.xq;
+  g.sa[0] = in.sx;
+  g.B[0] = in.wq;
+  g.sb[0] = in.sw;
+  g.C[0] = in.y;
+  g.M[0] = (int)M;
+  g.N[0] = (int)N;
+  g.K[0] = (int)K;
+  g.a = in.z;
+  g.bias = in.bias;
+  g.bias_f32 = in.bias_f32;
+  g.res = in.residual;
+  g.act = act_consts(in.act);
+  CastSource src = {};
+  src.x = y;
+  src.act = cast_act;
+  bool measured = false;                          // the maxima are there
+  if (M * N > 0) {
+    const hipError_t e = with_form(in.act, [&](auto form) {
+      constexpr int FORM = decltype(form)::value;
+      if (K == 0) {
+        const int64_t n8 = M * N / 8;
+        hipLaunchKernelGGL((k_act_k0<FORM>), dim3((unsigned)((n8 + 255) / 256)), dim3(256), 0,
+                           stream, g, n8);
+        return hipGetLastError();
+      }
+      if (act_few_tokens(M, N)) {
+        const ActSkinnyArgs p = {in.xq, in.wq, in.sx, in.sw, g, (int)M, (int)N, (int)K, rw};
+        return act_skinny_launch<FORM>(p, stream);
+      }
+      measured = o && o->qt;
+      g.maxima = measured;
+      if (measured) set_partials(g, 0, src, workspace, rw, BN);
+      return launch_act<EPI_ACT + FORM, 0>(g, rw, &src.nparts, stream);
+    });
+    if (e != hipSuccess) return e;
+  }
+  if (!o) return hipSuccess;
+  if (!o->qt && rw && M > 0) return quantize_rows_launch(y, cast_act, M, N, *o, stream);
+  if (measured) return quantize_cast_launch(&src, 1, M, N, scaling, o, stream);
+  return quantize_act_launch(y, cast_act, M, N, scaling, *o, workspace, stream);
+}
+
+hipError_t linear_act_bwd_launch(const uint8_t *dyq, const float *sdy, const uint8_t *wtq,
+                                 const float *swt, const uint16_t *z, int act, int64_t M,
+                                 int64_t H, int64_t D, int scaling, uint16_t *dz, void *dbias,
+                                 int dbias_f32, const Fp8Out &o, void *workspace,
+                                 hipStream_t stream) {
+  const bool rw = (scaling & FP8L_ROWWISE) != 0;
+  float *sums = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) +
+                                          linear_act_maxima_bytes(M, H, scaling));
+  if (M * H == 0 || D == 0) {                     // dz is empty or zero
+    if (M * H > 0) {
+      const hipError_t e = fill_zero(dz, 2 * M * H, stream);
+      if (e != hipSuccess) return e;
+    }
+    if (dbias) {
+      const hipError_t e = column_sums_launch(nullptr, 0, H, dbias, dbias_f32, stream);
+      if (e != hipSuccess) return e;
+    }
+    return quantize_launch(dz, M, H, scaling, o.q, o.qt, o.scale, o.scale_t, o.amax, workspace,
+                           stream);
+  }
+  ActArgs g = {};
+  g.A[0] = dyq;
+  g.sa[0] = sdy;
+  g.B[0] = wtq;
+  g.sb[0] = swt;
+  g.C[0] = dz;
+  g.M[0] = (int)M;
+  g.N[0] = (int)H;
+  g.K[0] = (int)D;
+  g.a = const_cast<uint16_t *>(z);
+  g.act = act_consts(act);
+  g.maxima = 1;
+  g.colsum = dbias ? sums : nullptr;
+  CastSource src = {};
+  src.x = dz;
+  set_partials(g, 0, src, workspace, rw, BN);
+  hipError_t e = with_form(act, [&](auto form) {
+    constexpr int EPI = EPI_DACT + decltype(form)::value;
+    return (scaling & FP8L_E5M2) ? launch_act<EPI, 1>(g, rw, &src.nparts, stream)
+                                 : launch_act<EPI, 0>(g, rw, &src.nparts, stream);
+  });
+  if (e == hipSuccess && dbias)
+    e = column_sums_launch(sums, act_slices(M, H), H, dbias, dbias_f32, stream);
+  if (e != hipSuccess) return e;
+  return quantize_cast_launch(&src, 1, M, H, scaling, &o, stream);
+}
+
+}  // namespace fp8l

@@ -21,6 +21,7 @@
 // non-negative values the bit order is the value order, and NaN patterns
 // (exponent all ones, mantissa non-zero) sort above +inf, so a NaN anywhere
 // makes the amax NaN without a floating-point compare.
+#include "act.h"
 #include "fp8l_internal.h"
 
 namespace fp8l {
@@ -324,13 +325,20 @@ __device__ __forceinline__ void load_param8(float (&f)[8], const void *p, int wf
     f[6] = bf16_to_f32(v.w & 0xFFFFu); f[7] = bf16_to_f32(v.w >> 16);
   }
 }
-template <int MODE, int FMT, bool NORM>
+// What is quantized: x itself, its norm (CastNorm), or an activation of it.
+constexpr int SRC_X = 0, SRC_NORM = 1, SRC_ACT = 2;
+struct CastAct {
+  ActConsts c;
+  int form;
+};
+template <int MODE, int FMT, int SRC>
 __device__ __forceinline__ void cast_tile(
     const uint16_t *__restrict__ x, int rows, int cols, int tiles_c,
     float *__restrict__ scale, float *__restrict__ scale_t,
     const uint32_t *__restrict__ part, int nparts, float *__restrict__ amax_out,
     uint8_t *__restrict__ q, uint8_t *__restrict__ qt, const CastNorm &nm,
-    const RowParts &rp) {
+    const RowParts &rp, const CastAct &ca) {
+  constexpr bool NORM = SRC == SRC_NORM;
   __shared__ __attribute__((aligned(16))) uint8_t lds[CT_T * CT_T];
   const int tid = threadIdx.x;
   // block -> (tile_r, tile_c): groups of CT_GROUP row tiles (the last one
@@ -464,6 +472,15 @@ __device__ __forceinline__ void cast_tile(
             f[e + 1] = bf16_to_f32(y >> 16);
           }
         }
+        if (SRC == SRC_ACT) {
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const uint32_t y = bf16x2_bits(act_value_any(ca.c, ca.form, f[e]),
+                                           act_value_any(ca.c, ca.form, f[e + 1]));
+            f[e] = bf16_to_f32(y & 0xFFFFu);
+            f[e + 1] = bf16_to_f32(y >> 16);
+          }
+        }
         const float s = srs[j];
         const uint32_t q0 = fp8x4<FMT>(f[0] * s, f[1] * s, f[2] * s, f[3] * s);
         const uint32_t q1 = fp8x4<FMT>(f[4] * s, f[5] * s, f[6] * s, f[7] * s);
@@ -530,14 +547,14 @@ __device__ __forceinline__ void cast_tile(
   }
 }
 
-template <int MODE, int FMT, bool NORM = false>
+template <int MODE, int FMT, int SRC = SRC_X>
 __global__ __launch_bounds__(CT_THREADS) void k_cast_transpose(
     const uint16_t *__restrict__ x, int rows, int cols, int tiles_c,
     float *__restrict__ scale, float *__restrict__ scale_t,
     const uint32_t *__restrict__ part, int nparts, float *__restrict__ amax_out,
-    uint8_t *__restrict__ q, uint8_t *__restrict__ qt, CastNorm nm, RowParts rp) {
-  cast_tile<MODE, FMT, NORM>(x, rows, cols, tiles_c, scale, scale_t, part, nparts, amax_out, q,
-                             qt, nm, rp);
+    uint8_t *__restrict__ q, uint8_t *__restrict__ qt, CastNorm nm, RowParts rp, CastAct ca) {
+  cast_tile<MODE, FMT, SRC>(x, rows, cols, tiles_c, scale, scale_t, part, nparts, amax_out, q,
+                            qt, nm, rp, ca);
 }
 
 // Two tensors of one shape (and one count of partials) in one launch: grid
@@ -555,11 +572,11 @@ template <int MODE, int FMT>
 __global__ __launch_bounds__(CT_THREADS) void k_cast_pair(CastJob a, CastJob b, int rows, int cols,
                                                           int tiles_c, int nparts) {
   if (blockIdx.y == 0)
-    cast_tile<MODE, FMT, false>(a.x, rows, cols, tiles_c, a.scale, a.scale_t, a.part, nparts,
-                                a.amax_out, a.q, a.qt, CastNorm{}, a.rp);
+    cast_tile<MODE, FMT, SRC_X>(a.x, rows, cols, tiles_c, a.scale, a.scale_t, a.part, nparts,
+                                a.amax_out, a.q, a.qt, CastNorm{}, a.rp, CastAct{});
   else
-    cast_tile<MODE, FMT, false>(b.x, rows, cols, tiles_c, b.scale, b.scale_t, b.part, nparts,
-                                b.amax_out, b.q, b.qt, CastNorm{}, b.rp);
+    cast_tile<MODE, FMT, SRC_X>(b.x, rows, cols, tiles_c, b.scale, b.scale_t, b.part, nparts,
+                                b.amax_out, b.q, b.qt, CastNorm{}, b.rp, CastAct{});
 }
 
 // --------------------------------------------------------------- encode --
@@ -627,11 +644,12 @@ bool scales_in_cast(const CastSource &s, int64_t rows, int64_t cols) {
          t * (s.row_slices + s.col_slices) <= 48 << 10;
 }
 
-template <int FMT, bool NORM>
+template <int FMT, int SRC>
 hipError_t cast_fmt(const CastSource *src, int count, int64_t rows, int64_t cols, bool rowwise,
                     const Fp8Out *o, hipStream_t stream) {
   const int R = (int)rows, C = (int)cols, l = count - 1;   // l: the last tensor
   const CastNorm nm = {src->w, src->b, src->wf32, src->mean, src->rstd};
+  const CastAct ca = {act_consts(src->act), act_form(src->act)};
   const bool in_cast = rowwise && scales_in_cast(*src, rows, cols);
   if (rowwise && !in_cast) {
     const int64_t nbr = cdiv(rows, FR_OUT), nbc = cdiv(cols, FR_OUT);
@@ -669,17 +687,17 @@ hipError_t cast_fmt(const CastSource *src, int count, int64_t rows, int64_t cols
         hipLaunchKernelGGL((k_cast_pair<MODE_TW, FMT>), dim3(nb, 2), dim3(CT_THREADS), 0, stream,
                            j, job(1), R, C, (int)ct_c, src->nparts);
     } else if (!rowwise) {
-      hipLaunchKernelGGL((k_cast_transpose<MODE_TW, FMT, NORM>), dim3(nb), dim3(CT_THREADS), 0,
+      hipLaunchKernelGGL((k_cast_transpose<MODE_TW, FMT, SRC>), dim3(nb), dim3(CT_THREADS), 0,
                          stream, j.x, R, C, (int)ct_c, j.scale, j.scale_t, j.part, src->nparts,
-                         j.amax_out, j.q, j.qt, nm, j.rp);
+                         j.amax_out, j.q, j.qt, nm, j.rp, ca);
     } else if (in_cast) {
-      hipLaunchKernelGGL((k_cast_transpose<MODE_RP, FMT, NORM>), dim3(nb), dim3(CT_THREADS), 0,
+      hipLaunchKernelGGL((k_cast_transpose<MODE_RP, FMT, SRC>), dim3(nb), dim3(CT_THREADS), 0,
                          stream, j.x, R, C, (int)ct_c, j.scale, j.scale_t, nullptr, 0, j.amax_out,
-                         j.q, j.qt, nm, j.rp);
+                         j.q, j.qt, nm, j.rp, ca);
     } else {
-      hipLaunchKernelGGL((k_cast_transpose<MODE_RW, FMT, NORM>), dim3(nb), dim3(CT_THREADS), 0,
+      hipLaunchKernelGGL((k_cast_transpose<MODE_RW, FMT, SRC>), dim3(nb), dim3(CT_THREADS), 0,
                          stream, j.x, R, C, (int)ct_c, j.scale, j.scale_t, nullptr, 0, nullptr,
-                         j.q, j.qt, nm, j.rp);
+                         j.q, j.qt, nm, j.rp, ca);
     }
   }
   return hipGetLastError();
@@ -705,7 +723,7 @@ hipError_t finish_fmt(const void *x, int64_t rows, int64_t cols, bool rowwise, i
     src.nparts = nparts;
   }
   const Fp8Out o = {q, qt, scale, scale_t, amax_out};
-  return cast_fmt<FMT, false>(&src, 1, rows, cols, rowwise, &o, stream);
+  return cast_fmt<FMT, SRC_X>(&src, 1, rows, cols, rowwise, &o, stream);
 }
 
 // first pass (amax partial maxima of x), then the second half
@@ -789,16 +807,17 @@ hipError_t quantize_scaled_launch(const void *x, int64_t rows, int64_t cols,
                        dim3(CT_THREADS), 0, stream, static_cast<const uint16_t *>(x), (int)rows,
                        (int)cols, (int)ct_c, const_cast<float *>(scale), nullptr, nullptr, 0,
                        nullptr, static_cast<uint8_t *>(q), static_cast<uint8_t *>(qt),
-                       CastNorm{}, RowParts{});
+                       CastNorm{}, RowParts{}, CastAct{});
   return hipGetLastError();
 }
 
 hipError_t quantize_cast_launch(const CastSource *src, int count, int64_t rows, int64_t cols,
                                 int scaling, const Fp8Out *o, hipStream_t stream) {
   const bool rw = (scaling & FP8L_ROWWISE) != 0;
-  if (src->rstd) return cast_fmt<0, true>(src, count, rows, cols, rw, o, stream);  // E4M3 only
-  if (scaling & FP8L_E5M2) return cast_fmt<1, false>(src, count, rows, cols, rw, o, stream);
-  return cast_fmt<0, false>(src, count, rows, cols, rw, o, stream);
+  if (src->rstd) return cast_fmt<0, SRC_NORM>(src, count, rows, cols, rw, o, stream);  // E4M3 only
+  if (src->act) return cast_fmt<0, SRC_ACT>(src, count, rows, cols, rw, o, stream);    // E4M3 only
+  if (scaling & FP8L_E5M2) return cast_fmt<1, SRC_X>(src, count, rows, cols, rw, o, stream);
+  return cast_fmt<0, SRC_X>(src, count, rows, cols, rw, o, stream);
 }
 
 hipError_t encode_launch(const float *in, uint8_t *out, int64_t n, int fmt,
@@ -817,3 +836,4 @@ hipError_t encode_launch(const float *in, uint8_t *out, int64_t n, int fmt,
 
 #include "norm.h"
 #include "resnorm.h"
+#include "bias_act.h"

@@ -31,7 +31,9 @@ EXPORTS = ("fp8_linear_workspace_bytes", "fp8_linear_quantize",
            "fp8_gated_workspace_bytes", "fp8_gated_fwd", "fp8_gated_bwd",
            "fp8_layernorm_workspace_bytes", "fp8_layernorm_fwd", "fp8_layernorm_quantize",
            "fp8_layernorm_bwd", "fp8_resnorm_workspace_bytes", "fp8_resnorm_fwd",
-           "fp8_resnorm_quantize", "fp8_resnorm_bwd", "fp8_linear_encode_e4m3",
+           "fp8_resnorm_quantize", "fp8_resnorm_bwd", "fp8_linear_act_workspace_bytes",
+           "fp8_linear_act_fwd", "fp8_linear_act_bwd", "fp8_bias_act_bwd",
+           "fp8_linear_encode_e4m3",
            "fp8_linear_encode_e5m2", "fp8_swiglu_workspace_bytes", "fp8_swiglu_fwd",
            "fp8_swiglu_bwd", "fp8_linear_status_string", "fp8_linear_version")
 
@@ -41,6 +43,8 @@ FP8L_LAYERNORM, FP8L_RMSNORM = 0, 1
 FP8L_BF16, FP8L_F32 = 0, 1
 FP8L_NORM_MAX_COLS = 16384
 FP8L_POST_NORM, FP8L_PRE_NORM = 1, 2
+(FP8L_ACT_NONE, FP8L_ACT_RELU, FP8L_ACT_GELU, FP8L_ACT_GELU_TANH, FP8L_ACT_SILU,
+ FP8L_ACT_RELU2) = range(6)
 
 
 class GemmProblem(ctypes.Structure):
@@ -114,6 +118,17 @@ def lib() -> ctypes.CDLL:
                                          + [P, ctypes.c_size_t, P])
     L.fp8_layernorm_bwd.restype = I
     L.fp8_layernorm_bwd.argtypes = ([P] * 5 + [i64, i64, I, I, I, P, P, P, P, ctypes.c_size_t, P])
+    L.fp8_linear_act_workspace_bytes.restype = ctypes.c_size_t
+    L.fp8_linear_act_workspace_bytes.argtypes = [i64, i64, I]
+    L.fp8_linear_act_fwd.restype = I
+    L.fp8_linear_act_fwd.argtypes = ([P] * 4 + [i64, i64, i64, I, P, I, I] + [P] * 8
+                                     + [P, ctypes.c_size_t, P])
+    L.fp8_linear_act_bwd.restype = I
+    L.fp8_linear_act_bwd.argtypes = ([P] * 5 + [i64, i64, i64, I, I] + [P] * 7 + [I]
+                                     + [P, ctypes.c_size_t, P])
+    L.fp8_bias_act_bwd.restype = I
+    L.fp8_bias_act_bwd.argtypes = ([P, P, i64, i64, I, I] + [P] * 7 + [I]
+                                   + [P, ctypes.c_size_t, P])
     S = ctypes.c_char_p          # a packed descriptor (_RESNORM, _RESNORM_GRADS)
     L.fp8_resnorm_workspace_bytes.restype = ctypes.c_size_t
     L.fp8_resnorm_workspace_bytes.argtypes = [i64, i64, I]
@@ -908,6 +923,161 @@ def fp8_gated_bwd(dyq: torch.Tensor, sdy: torch.Tensor, w2tq: torch.Tensor, sw2t
             _a(qb.q), _a(qb.qt), _a(qb.scale), _a(qb.scale_t), _a(qb.amax),
             *_ws(workspace, dev), _stream(stream)), "fp8_gated_bwd")
     return da, db, qa, qb
+
+
+# ---------------------------------------------- linear with its epilogue --
+
+ACTS = {"none": FP8L_ACT_NONE, "relu": FP8L_ACT_RELU, "gelu": FP8L_ACT_GELU,
+        "gelu_tanh": FP8L_ACT_GELU_TANH, "silu": FP8L_ACT_SILU, "relu2": FP8L_ACT_RELU2}
+
+
+def _act(act: str) -> int:
+    if act not in ACTS:
+        raise ValueError("act must be a name in %s, not %r" % (tuple(ACTS), act))
+    return ACTS[act]
+
+
+def fp8_linear_act_workspace_bytes(M: int, N: int, rowwise: bool = False) -> int:
+    return int(lib().fp8_linear_act_workspace_bytes(M, N, _scaling(rowwise)))
+
+
+def alloc_linear_act_workspace(M: int, N: int, rowwise: bool, device) -> torch.Tensor:
+    """Workspace of fp8_linear_act_fwd, fp8_linear_act_bwd and fp8_bias_act_bwd for
+    outputs of up to [M, N]; needs no clearing."""
+    return torch.empty(max(fp8_linear_act_workspace_bytes(M, N, rowwise), 256), dtype=torch.uint8,
+                       device=device)
+
+
+def fp8_linear_act_fwd(xq: torch.Tensor, sx: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor,
+                       bias: Optional[torch.Tensor] = None, act: str = "none",
+                       residual: Optional[torch.Tensor] = None, rowwise: bool = False,
+                       y: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                       out: Optional[Quantized] = None, transposed: bool = True,
+                       workspace: Optional[torch.Tensor] = None, stream=None):
+    """y [M, N] bf16 = act(x W^T + bias) + residual from the fp8 copies of x [M, K]
+    (any M) and of W [N, K]; bias [N] bf16 or fp32, act a name in ``ACTS``,
+    residual [M, N] bf16 (y itself: added in place).  With a tensor z given the
+    pre-activation is stored there for the backward; with ``out`` given y is
+    quantized into it (M a multiple of 16), or with transposed=False (rowwise
+    only) each of its rows alone (any M).  Where z and ``out`` are given and y is
+    not, y is not stored and None returned."""
+    (M, K), N = xq.shape, wq.shape[0]
+    bf, f32, u8, dev = torch.bfloat16, torch.float32, torch.uint8, xq.device
+    code = _act(act)
+    pd = bias.dtype if bias is not None else bf
+    if pd not in _DTYPES:
+        raise ValueError("bias must be bf16 or fp32")
+    _checked(dev, *_operand("xq", xq, sx, M, K, rowwise), *_operand("wq", wq, sw, N, K, rowwise),
+             ("bias", bias, pd, (N,)), ("residual", residual, bf, (M, N)), ("y", y, bf, (M, N)),
+             ("z", z, bf, (M, N)))
+    q = out if out is not None else _NO_CODES
+    if out is not None:
+        if transposed:
+            # (without qt and scale_t the library takes the call for the serving form)
+            if out.q is None or out.qt is None or out.scale is None or out.scale_t is None:
+                raise ValueError("out must have q, qt, scale and scale_t unless transposed=False")
+            _checked(dev, *_quantized("y ", out, M, N, rowwise))
+        else:
+            if not rowwise:
+                raise ValueError("codes without their transposed copy are rowwise")
+            if out.q is None or out.scale is None:
+                raise ValueError("out must have q and scale")
+            _checked(dev, ("q", out.q, u8, (M, N)), ("scale", out.scale, f32, (M,)),
+                     ("amax", out.amax, f32, (M,)))
+    want_y = y is None and (out is None or z is None or residual is not None)
+    with _on_device(dev, None if workspace is not None and not want_y else stream):
+        if want_y:
+            y = torch.empty((M, N), dtype=bf, device=dev)
+        if workspace is None:
+            workspace = alloc_linear_act_workspace(M, N, rowwise, dev)
+        _check(lib().fp8_linear_act_fwd(
+            _a(xq), _a(sx), _a(wq), _a(sw), M, N, K, _scaling(rowwise), _a(bias), _DTYPES[pd],
+            code, _a(residual), _a(z), _a(y), _a(q.q), _a(q.qt) if transposed else None,
+            _a(q.scale), _a(q.scale_t) if transposed else None, _a(q.amax), *_ws(workspace, dev),
+            _stream(stream)), "fp8_linear_act_fwd")
+    return y
+
+
+def _bias_type(dbias, want):
+    """Type of a bias's gradient: a given tensor's, else the wanted one."""
+    pd = dbias.dtype if dbias is not None else want if want is not None else torch.float32
+    if pd not in _DTYPES:
+        raise ValueError("dbias must be bf16 or fp32")
+    return pd
+
+
+def fp8_linear_act_bwd(dyq: torch.Tensor, sdy: torch.Tensor, wtq: torch.Tensor, swt: torch.Tensor,
+                       z: Optional[torch.Tensor], act: str = "none", rowwise: bool = False,
+                       e5m2: bool = False, dz: Optional[torch.Tensor] = None,
+                       out: Optional[Quantized] = None, dbias: Optional[torch.Tensor] = None,
+                       bias_dtype: Optional[torch.dtype] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None):
+    """(dz, quantize of dz, dbias) of a linear y = act(z), z = x W1^T + bias,
+    whose y is the input of a next linear: dz = (dY W2) act'(z) from the fp8 copies
+    of dY [M, D] and of W2^T [H, D] (codes of dY and dz E5M2 when e5m2).  dbias is
+    computed where a tensor is given for it or ``bias_dtype`` names its type."""
+    (M, D), H = dyq.shape, wtq.shape[0]
+    bf, dev = torch.bfloat16, dyq.device
+    code, pd = _act(act), _bias_type(dbias, bias_dtype)
+    if z is None and code != FP8L_ACT_NONE:
+        raise ValueError("z must be a tensor where there is an activation")
+    _checked(dev, *_operand("dyq", dyq, sdy, M, D, rowwise), *_operand("wtq", wtq, swt, H, D, rowwise),
+             ("z", z, bf, (M, H)), ("dz", dz, bf, (M, H)),
+             ("dbias", dbias, pd, (H,)))
+    if out is not None:
+        _checked(dev, *_quantized("dz ", out, M, H, rowwise))
+    given = (dz is not None and out is not None and workspace is not None
+             and (dbias is not None or bias_dtype is None))
+    with _on_device(dev, None if given else stream):
+        if dbias is None and bias_dtype is not None:
+            dbias = torch.empty(H, dtype=pd, device=dev)
+        dz = torch.empty((M, H), dtype=bf, device=dev) if dz is None else dz
+        out = alloc_quantized(M, H, rowwise, dev) if out is None else out
+        if workspace is None:
+            workspace = alloc_linear_act_workspace(M, H, rowwise, dev)
+        _check(lib().fp8_linear_act_bwd(
+            _a(dyq), _a(sdy), _a(wtq), _a(swt), _a(z), M, H, D, _scaling(rowwise, e5m2), code,
+            _a(dz), _a(out.q), _a(out.qt), _a(out.scale), _a(out.scale_t), _a(out.amax), _a(dbias),
+            _DTYPES[pd], *_ws(workspace, dev), _stream(stream)), "fp8_linear_act_bwd")
+    return dz, out, dbias
+
+
+def fp8_bias_act_bwd(dy: torch.Tensor, z: Optional[torch.Tensor] = None, act: str = "none",
+                     rowwise: bool = False, e5m2: bool = False,
+                     dz: Optional[torch.Tensor] = None, out: Optional[Quantized] = None,
+                     dbias: Optional[torch.Tensor] = None,
+                     bias_dtype: Optional[torch.dtype] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """(dz, quantize of dz, dbias) of y = act(z) for a gradient dy [M, N] bf16 that is
+    there: dz = dy act'(z).  Without an activation dz is dy itself: not written
+    (None) unless a tensor is given for it."""
+    if dy.dim() != 2:
+        raise ValueError("dy must be a [M, N] bf16 matrix")
+    M, N = dy.shape
+    bf, dev = torch.bfloat16, dy.device
+    code, pd = _act(act), _bias_type(dbias, bias_dtype)
+    if z is None and code != FP8L_ACT_NONE:
+        raise ValueError("z must be a tensor where there is an activation")
+    _checked(dev, ("dy", dy, bf, (M, N)), ("z", z, bf, (M, N)), ("dz", dz, bf, (M, N)),
+             ("dbias", dbias, pd, (N,)))
+    if out is not None:
+        _checked(dev, *_quantized("dz ", out, M, N, rowwise))
+    given = (out is not None and workspace is not None
+             and (dz is not None or code == FP8L_ACT_NONE)
+             and (dbias is not None or bias_dtype is None))
+    with _on_device(dev, None if given else stream):
+        if dbias is None and bias_dtype is not None:
+            dbias = torch.empty(N, dtype=pd, device=dev)
+        if dz is None and code != FP8L_ACT_NONE:
+            dz = torch.empty((M, N), dtype=bf, device=dev)
+        out = alloc_quantized(M, N, rowwise, dev) if out is None else out
+        if workspace is None:
+            workspace = alloc_linear_act_workspace(M, N, rowwise, dev)
+        _check(lib().fp8_bias_act_bwd(
+            _a(dy), _a(z), M, N, _scaling(rowwise, e5m2), code, _a(dz), _a(out.q), _a(out.qt),
+            _a(out.scale), _a(out.scale_t), _a(out.amax), _a(dbias), _DTYPES[pd],
+            *_ws(workspace, dev), _stream(stream)), "fp8_bias_act_bwd")
+    return dz, out, dbias
 
 
 def fp8_linear_encode_e4m3(x: torch.Tensor, out: Optional[torch.Tensor] = None,

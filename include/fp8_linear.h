@@ -418,6 +418,104 @@ FP8L_API int fp8_gated_bwd(const void *dyq, const float *sdy, const void *w2tq,
                            void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * A Float8 linear with its epilogue: bias, activation and residual where the
+ * product's output is finished, in one kernel, and the gradient through them as
+ * the producer of the linear's fp8 output gradient.
+ *
+ *   z = fl32( p + bias[n] ),   p = fl32(fl32(acc * (1/sx)) * (1/sw))
+ *                              (fp8_linear_fwd's value before it is rounded)
+ *   FP8L_ACT_NONE:             y = bf16( fl32( z + residual ) )
+ *   the others, with zb = bf16(z):
+ *                              y = bf16( fl32( act(zb) + residual ) )
+ *
+ *   FP8L_ACT_RELU max(z, 0), FP8L_ACT_GELU z P(z) (P the normal distribution
+ *   function), FP8L_ACT_GELU_TANH z s(2 sqrt(2/pi) (z + 0.044715 z^3)), FP8L_ACT_SILU
+ *   z s(z), s(v) = 1 / (1 + e^-v), FP8L_ACT_RELU2 max(z, 0)^2.  act(+inf) = +inf,
+ *   act(-inf) = 0; act of a NaN is NaN.  Computed in fp32, over every finite z, with v
+ *   the exponent's argument (z; 2 sqrt(2/pi) (...); z^2 / 2): act with a relative error
+ *   of at most (3 |v| + 8) 2^-24 (FP8L_ACT_GELU: 2^-18 more) where its exact value is
+ *   2^-100 or more, below that an absolute one of 2^-100; act' with an absolute one
+ *   of at most 2^-21 (FP8L_ACT_GELU: 2^-19); none for the activations without an
+ *   exponent but the rounding of fp32.
+ */
+#define FP8L_ACT_NONE      0
+#define FP8L_ACT_RELU      1
+#define FP8L_ACT_GELU      2
+#define FP8L_ACT_GELU_TANH 3
+#define FP8L_ACT_SILU      4
+#define FP8L_ACT_RELU2     5
+
+/*
+ * Bytes of device workspace that the three entry points below need for outputs of
+ * [M, N] with this scaling (with or without FP8L_E5M2); does not fall as M or N
+ * grows: one for the largest batch serves the smaller ones.  0 for invalid
+ * arguments.
+ */
+FP8L_API size_t fp8_linear_act_workspace_bytes(int64_t M, int64_t N, int scaling);
+
+/*
+ *   xq [M, K], sx;  wq [N, K], sw   as fp8_linear_fwd's operands; M is any number of
+ *           tokens >= 0 unless qt is written
+ *   bias    [N], bf16 or fp32 (pdtype FP8L_BF16 or FP8L_F32), or NULL for 0
+ *   act     FP8L_ACT_*
+ *   residual [M, N] bf16, or NULL for 0; may be y itself (added in place)
+ *   z       [M, N] bf16 (written: what fp8_linear_act_bwd and fp8_bias_act_bwd
+ *           need), or NULL
+ *   y       [M, N] bf16 (written), or NULL where only z and the codes are wanted
+ *           (without a residual)
+ *   q, qt, scale, scale_t, amax_out  the E4M3 quantize of y, as
+ *           fp8_linear_quantize's outputs for x = y; all NULL: y is not quantized.
+ *           qt = NULL (FP8L_ROWWISE, scale_t = NULL): each row alone, for serving;
+ *           amax_out is then [M] and M any number
+ *   scaling FP8L_TENSORWISE or FP8L_ROWWISE, of the operands and of q
+ * N and K are multiples of 16, and M where qt is written; sizes as for
+ * fp8_linear_fwd.  The order of the fp32 additions depends on M, N and K; equal
+ * calls give equal bits.  The workspace's contents are undefined on entry and exit,
+ * not shared by calls in flight together.  Outputs and the workspace must not
+ * overlap inputs (apart from residual = y) or one another (FP8L_EINVAL).
+ */
+FP8L_API int fp8_linear_act_fwd(const void *xq, const float *sx, const void *wq, const float *sw,
+                                int64_t M, int64_t N, int64_t K, int scaling, const void *bias,
+                                int pdtype, int act, const void *residual, void *z, void *y,
+                                void *q, void *qt, float *scale, float *scale_t,
+                                float *amax_out, void *workspace, size_t workspace_bytes,
+                                void *stream);
+
+/*
+ * The gradient through a linear's epilogue where it is the input of a next linear,
+ * behind that linear's product: with dh = fp8_linear_bwd's grad_x for (dyq, wtq)
+ * before it is rounded,
+ *
+ *   dz = bf16( fl32( dh * act'(z) ) ),   dbias = sum_m fl32( dh * act'(z) )
+ *
+ *   dyq [M, D] (q of the next linear's output gradient), sdy
+ *   wtq [H, D] (qt of the next linear's weight [D, H]), swt
+ *   z   [M, H] bf16 (read): fp8_linear_act_fwd's; may be NULL for FP8L_ACT_NONE
+ *   dz  [M, H] bf16 (written); q, qt, scale, scale_t, amax_out its quantize, as for
+ *       fp8_swiglu_bwd
+ *   dbias [H] of type pdtype (written), or NULL; its sum is fp32 in a fixed order,
+ *       rounded once
+ *   scaling FP8L_TENSORWISE or FP8L_ROWWISE, optionally | FP8L_E5M2 (dyq and the
+ *       codes of dz)
+ * M, H and D are multiples of 16.  Workspace and overlaps as above.
+ */
+FP8L_API int fp8_linear_act_bwd(const void *dyq, const float *sdy, const void *wtq,
+                                const float *swt, const void *z, int64_t M, int64_t H, int64_t D,
+                                int scaling, int act, void *dz, void *q, void *qt, float *scale,
+                                float *scale_t, float *amax_out, void *dbias, int pdtype,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The same of an output gradient that is there (a linear whose output is the
+ * residual stream's): dz and dbias with dh = dy [M, N] bf16.  dz may be NULL for
+ * FP8L_ACT_NONE: it equals dy, whose codes are written.
+ */
+FP8L_API int fp8_bias_act_bwd(const void *dy, const void *z, int64_t M, int64_t N, int scaling,
+                              int act, void *dz, void *q, void *qt, float *scale, float *scale_t,
+                              float *amax_out, void *dbias, int pdtype, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/*
  * Layer norm, and its RMS form: the norm in front of the feed-forward block,
  * as the producer of the fp8 operand that the block's first linears read.
  *
