@@ -184,11 +184,15 @@ constexpr int TB = 128;                            // rows of the B slab
 constexpr int T_STAGE = (TM + TB) * BK;            // 24 KB
 constexpr int T_STAGES = 3;
 
+// k-tiles of a part of a split contraction
+__device__ __forceinline__ int part_kt(const ActArgs &g) { return g.part_kt; }
+__device__ __forceinline__ int part_kt(const GateArgs &) { return 0; }
+
 template <int EPI, int FA, bool RW>
 __global__ __launch_bounds__(256) void k_gate_tile(typename ArgsOf<EPI>::type g) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[T_STAGES * T_STAGE];
   constexpr bool GATE = is_gate(EPI);
-  constexpr bool ACT = is_act(EPI), DACT = is_dact(EPI);
+  constexpr bool ACT = is_act(EPI), DACT = is_dact(EPI), SPLIT = EPI == EPI_SPLIT;
   constexpr int NOUT = EPI == EPI_DGATE ? 2 : 1;   // tensors that are quantized
   constexpr int TN = GATE ? TB / 2 : TB;           // output columns of the tile
   constexpr int WC = TN / 2;                       // of a wave
@@ -197,7 +201,9 @@ __global__ __launch_bounds__(256) void k_gate_tile(typename ArgsOf<EPI>::type g)
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   const int M = g.M[0], N = g.N[0], K = g.K[0];
-  const int nk = (K + BK - 1) / BK;
+  // (EPI_SPLIT: the k-tiles of this part)
+  const int first_kt = SPLIT ? (int)blockIdx.y * part_kt(g) : 0;
+  const int nk = SPLIT ? min(part_kt(g), (K + BK - 1) / BK - first_kt) : (K + BK - 1) / BK;
   // workgroups are dealt to the XCDs round-robin; each XCD takes a contiguous
   // share of the tiles, rows fastest, so that it reads its own rows of B
   const int x = blockIdx.x % NUM_XCD, total = g.total;
@@ -222,7 +228,7 @@ __global__ __launch_bounds__(256) void k_gate_tile(typename ArgsOf<EPI>::type g)
   const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void *)lds;
   const int lr = lane >> 3;
   auto fill = [&](int t) {
-    const int k0 = t * BK;
+    const int k0 = (first_kt + t) * BK;
     const uint32_t st = base + (uint32_t)(t % T_STAGES * T_STAGE);
 #pragma unroll
     for (int i = 0; i < 6; ++i) {
@@ -284,9 +290,9 @@ __global__ __launch_bounds__(256) void k_gate_tile(typename ArgsOf<EPI>::type g)
   }
   float ia[2], ib[NJ][4], ib2[NJ][4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) ia[i] = g.sa[0][RW ? min(mrow + i * FR, M - 1) : 0];
+  for (int i = 0; i < 2 && !SPLIT; ++i) ia[i] = g.sa[0][RW ? min(mrow + i * FR, M - 1) : 0];
 #pragma unroll
-  for (int j = 0; j < NJ; ++j)
+  for (int j = 0; j < NJ && !SPLIT; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int at = RW ? min(ncol + j * FR + e, N - 1) : 0;
@@ -322,6 +328,17 @@ __global__ __launch_bounds__(256) void k_gate_tile(typename ArgsOf<EPI>::type g)
 
   // ---- epilogue: lane l holds columns 4 (l / 16) .. + 3 of row l % 16 of its
   // blocks
+  if constexpr (SPLIT) {
+    float *dst = g.partial + (size_t)blockIdx.y * M * N;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int m = mrow + i * FR, n = ncol + j * FR;
+        if (m < M && n < N) *reinterpret_cast<v4f *>(dst + (size_t)m * N + n) = acc[j][i];
+      }
+    return;
+  }
   uint16_t *C = static_cast<uint16_t *>(g.C[0]);
   uint32_t rm[2][2] = {};                          // [output][i]: row maxima (u16 pairs)
   uint2 cm[2][NJ] = {};                            // [output][j]: column maxima

@@ -216,6 +216,8 @@ static_assert(sizeof(GemmGroup) <= 4096, "kernel arguments");
 //             receives dz = dh act'(z), colsum the sums of the unrounded dz over
 //             each wave's rows, [slice][N].
 //             (form: ACT_PW, ACT_SIG or ACT_ERF of act.h)
+//  EPI_SPLIT  (small tiles only) one part of the contraction: its unscaled fp32 sums
+//             go to partial[part][M][N].
 // The gate's forms take the amax partial maxima of what they write (of h, or of da
 // and db) where `maxima` is set: tensorwise one u32 per wave of the launch in
 // part[o], rowwise the row maxima over each wave's columns in
@@ -223,7 +225,7 @@ static_assert(sizeof(GemmGroup) <= 4096, "kernel arguments");
 // colpart[o][slice][N], one slice per wave column / wave row of the tiles
 // (EPI_DGATE takes them always).  EPI_ACT (of y) and EPI_DACT (of dz) do likewise.
 constexpr int EPI_NONE = 0, EPI_GATE = 1, EPI_GATE_AB = 2, EPI_DGATE = 3;
-constexpr int EPI_ACT = 4, EPI_DACT = 8;
+constexpr int EPI_ACT = 4, EPI_DACT = 8, EPI_SPLIT = 12;
 constexpr bool is_gate(int epi) { return epi == EPI_GATE || epi == EPI_GATE_AB; }
 constexpr bool is_act(int epi) { return epi >= EPI_ACT && epi < EPI_ACT + 3; }
 constexpr bool is_dact(int epi) { return epi >= EPI_DACT && epi < EPI_DACT + 3; }
@@ -242,12 +244,15 @@ struct ActArgs : GateArgs {    // a: z
   const uint16_t *res;         // residual [M, N], or NULL
   ActConsts act;
   float *colsum;               // EPI_DACT; NULL: not wanted
+  float *partial;              // EPI_SPLIT
+  int part_kt;                 // EPI_SPLIT: k-tiles of a part
 };
 template <int EPI>
 struct ArgsOf {
   typedef typename std::conditional<
       EPI == EPI_NONE, GemmGroup,
-      typename std::conditional<is_act(EPI) || is_dact(EPI), ActArgs, GateArgs>::type>::type type;
+      typename std::conditional<is_act(EPI) || is_dact(EPI) || EPI == EPI_SPLIT, ActArgs,
+                                GateArgs>::type>::type type;
 };
 
 // silu(x) = x s and silu'(x) = s + x s (1 - s), s = 1 / (1 + e^-x), in fp32
@@ -1184,6 +1189,24 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
       uint32_t tmax = RW ? 0u : FP8P_TMAX()->x;
       // row maxima of the left half wait here for the right one's
       uint32_t rmax[RW ? NF : 1][2];
+      auto row_off = [&](int i, int u) { return (uint32_t)(i * FR + u * 8) * (uint32_t)N * 2u; };
+      // The residual or z: all of a half's loads in flight together, the right half's
+      // each as soon as its registers fall free (a wave alone on its SIMD covers no
+      // trip to memory but by loads of its own: with one pass ahead, 8 KB a compute
+      // unit, z cost 46 us of 8192 x 14336)
+      v4u in[NF][2];
+      auto load_in = [&](int jh, int i) {
+        const int col = n0 + wn * WN + jh * 64 + (lane_e & 7) * 8;
+        const uint32_t at = ((uint32_t)row0 * (uint32_t)N + (uint32_t)col) * 2u;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          in[i][u] = __builtin_amdgcn_raw_buffer_load_b128(
+              rsIn, col < N && i * FR + u * 8 < M - row0 ? at : OOB_C, row_off(i, u), 0);
+      };
+      if (has_in) {
+#pragma unroll
+        for (int i = 0; i < NF; ++i) load_in(0, i);
+      }
 #pragma unroll
       for (int jh = 0; jh < 2; ++jh) {
         const int scol = n0 + wn * WN + jh * 64 + (lane_e & 7) * 8;
@@ -1191,15 +1214,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
         const uint32_t off0 = ((uint32_t)row0 * (uint32_t)N + (uint32_t)scol) * 2u;
         const int rows_left = col_ok ? M - row0 : 0;
         auto offset = [&](int i, int u) { return i * FR + u * 8 < rows_left ? off0 : OOB_C; };
-        auto row_off = [&](int i, int u) { return (uint32_t)(i * FR + u * 8) * (uint32_t)N * 2u; };
-        v4u in[2][2];
         v4f v[2][2][2];
-        auto load_in = [&](int i) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-            in[i & 1][u] =
-                __builtin_amdgcn_raw_buffer_load_b128(rsIn, offset(i, u), row_off(i, u), 0);
-        };
         auto stage = [&](int i) {
           const float ia = RW ? tab[wm * WM + i * FR + ml16] : inv_ar[i];
 #pragma unroll
@@ -1221,7 +1236,6 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
                   sf + r * 256 + ((2 * (lane_e & 7) + e) ^ r) * 16);
           }
         };
-        if (has_in) load_in(0);
         stage(0);
         float bias[8];
         if (ACT) {
@@ -1238,10 +1252,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
         float cs[8] = {};
 #pragma unroll
         for (int i = 0; i < NF; ++i) {
-          if (i + 1 < NF) {
-            if (has_in) load_in(i + 1);
-            stage(i + 1);
-          }
+          if (i + 1 < NF) stage(i + 1);
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const uint32_t off = offset(i, u);
@@ -1264,7 +1275,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
               }
               if (has_in) {
                 float r[8];
-                unpack8(r, in[i & 1][u]);
+                unpack8(r, in[i][u]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) f[e] = add32(f[e], r[e]);
                 y = pack8(f);
@@ -1272,7 +1283,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
             } else {
               if (has_in) {
                 float z[8];
-                unpack8(z, in[i & 1][u]);
+                unpack8(z, in[i][u]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) f[e] *= act_slope<FORM>(g.act, z[e]);
               }
@@ -1300,6 +1311,8 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
               }
             }
           }
+          if (jh == 0 && has_in) load_in(1, i);
+          FP8P_E()                                // (mixed passes spill)
         }
         if (RW && g.maxima)
           store_colmax<8>(cm, lane_e, col_ok,

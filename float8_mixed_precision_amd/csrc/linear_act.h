@@ -27,45 +27,58 @@ struct ActSkinnyArgs {
   int M, N, K, rowwise;
 };
 
-template <bool KFULL, int FORM>
+// CB: blocks of 16 columns a workgroup owns.  Two of them keep twice the loads in
+// flight and read x half as often.
+template <bool KFULL, int FORM, int CB>
 __global__ __launch_bounds__(64 * SK_WAVES) void k_act_skinny(ActSkinnyArgs p) {
-  __shared__ v4f red[SK_WAVES][64];
+  __shared__ v4f red[SK_WAVES][CB][64];
   const int lane = threadIdx.x & 63;
   const int wave = threadIdx.x >> 6;
-  const int n0 = blockIdx.x * 16;
+  const int n0 = blockIdx.x * 16 * CB;
   const int K = p.K;
   const int nk = (K + BK - 1) / BK;
   const int kl = (lane >> 4) * 16;
-  const uint8_t *rw = p.w + (size_t)(n0 + (lane & 15)) * K;
+  const uint8_t *rw[CB];
+#pragma unroll
+  for (int c = 0; c < CB; ++c)                    // (past N: the last row, not stored)
+    rw[c] = p.w + (size_t)min(n0 + c * 16 + (lane & 15), p.N - 1) * K;
   const uint8_t *rx = p.x + (size_t)min(lane & 15, p.M - 1) * K;
-  v4f acc = {0.f, 0.f, 0.f, 0.f};
+  v4f acc[CB];
+#pragma unroll
+  for (int c = 0; c < CB; ++c) acc[c] = (v4f){0.f, 0.f, 0.f, 0.f};
   for (int t0 = wave; t0 < nk; t0 += SK_WAVES * SK_UNROLL) {
-    v4u fw[SK_UNROLL][2], fx[SK_UNROLL][2];
+    v4u fw[SK_UNROLL][CB][2], fx[SK_UNROLL][2];
 #pragma unroll
     for (int u = 0; u < SK_UNROLL; ++u) {
       const int t = t0 + u * SK_WAVES;            // past the end: loaded again, not used
       const int k = (t < nk ? t : t0) * BK + kl;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        fw[u][e] = row_chunk<KFULL>(rw, k + e * 64, K);
+#pragma unroll
+        for (int c = 0; c < CB; ++c) fw[u][c][e] = row_chunk<KFULL>(rw[c], k + e * 64, K);
         fx[u][e] = row_chunk<KFULL>(rx, k + e * 64, K);
       }
     }
 #pragma unroll
     for (int u = 0; u < SK_UNROLL; ++u)
-      if (t0 + u * SK_WAVES < nk)                 // wave-uniform
-        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            frag(fw[u][0], fw[u][1]), frag(fx[u][0], fx[u][1]), acc, 0, 0, 0, 0, 0, 0);
-  }
-  red[wave][lane] = acc;
-  __syncthreads();
-  // lane l of the first wave: token l % 16, columns n0 + 4 (l / 16) ...
-  const int m = lane & 15;
-  const int n = n0 + (lane >> 4) * 4;
-  if (wave > 0 || m >= p.M) return;
-  v4f a = red[0][lane];
+      if (t0 + u * SK_WAVES < nk) {               // wave-uniform
+        const v8i ax = frag(fx[u][0], fx[u][1]);
 #pragma unroll
-  for (int w = 1; w < SK_WAVES; ++w) a += red[w][lane];
+        for (int c = 0; c < CB; ++c)
+          acc[c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              frag(fw[u][c][0], fw[u][c][1]), ax, acc[c], 0, 0, 0, 0, 0, 0);
+      }
+  }
+#pragma unroll
+  for (int c = 0; c < CB; ++c) red[wave][c][lane] = acc[c];
+  __syncthreads();
+  // wave c finishes column block c: lane l has token l % 16, columns 4 (l / 16) ...
+  const int m = lane & 15;
+  const int n = n0 + wave * 16 + (lane >> 4) * 4;
+  if (wave >= CB || m >= p.M || n >= p.N) return;
+  v4f a = red[0][wave][lane];
+#pragma unroll
+  for (int w = 1; w < SK_WAVES; ++w) a += red[w][wave][lane];
   const float ia = 1.0f / p.sx[p.rowwise ? m : 0];
   const size_t at = (size_t)m * p.N + n;
   float f[4];
@@ -82,15 +95,95 @@ __global__ __launch_bounds__(64 * SK_WAVES) void k_act_skinny(ActSkinnyArgs p) {
   if (p.e.C[0]) *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.e.C[0]) + at) = y;
 }
 
-bool act_few_tokens(int64_t M, int64_t N) { return few_tokens(M, N); }
+bool act_few_tokens(int64_t M, int64_t N) { return M <= SKINNY_M; }
 
 template <int FORM>
 hipError_t act_skinny_launch(const ActSkinnyArgs &p, hipStream_t stream) {
-  const dim3 grid((unsigned)(p.N / 16)), block(64 * SK_WAVES);
-  if (p.K % BK == 0)
-    hipLaunchKernelGGL((k_act_skinny<true, FORM>), grid, block, 0, stream, p);
-  else
-    hipLaunchKernelGGL((k_act_skinny<false, FORM>), grid, block, 0, stream, p);
+  const dim3 block(64 * SK_WAVES);
+  const bool wide = p.N >= 2 * 16 * 256;
+  const dim3 grid((unsigned)((p.N + (wide ? 31 : 15)) / (wide ? 32 : 16)));
+  const bool kfull = p.K % BK == 0;
+  auto kern = wide ? (kfull ? k_act_skinny<true, FORM, 2> : k_act_skinny<false, FORM, 2>)
+                   : (kfull ? k_act_skinny<true, FORM, 1> : k_act_skinny<false, FORM, 1>);
+  hipLaunchKernelGGL(kern, grid, block, 0, stream, p);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------- split contraction --
+//
+// Where one small tile per output leaves most of the compute units idle and the
+// contraction is long, its k-tiles go to several workgroups (EPI_SPLIT), whose fp32
+// sums this kernel adds in order and finishes.  A thread has 8 columns of a row.
+struct ActJoinArgs {
+  ActArgs e;
+  const float *sx, *sw;
+  int parts, rowwise;
+};
+template <int FORM>
+__global__ __launch_bounds__(256) void k_act_join(ActJoinArgs p, int64_t n8) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n8) return;
+  const int N = p.e.N[0];
+  const int m = (int)(i * 8 / N), n = (int)(i * 8 % N);
+  const size_t mn = (size_t)p.e.M[0] * N;
+  const v4f *src = reinterpret_cast<const v4f *>(p.e.partial + (size_t)i * 8);
+  v4f a[2] = {src[0], src[1]};
+  for (int s = 1; s < p.parts; ++s) {
+    a[0] += src[(size_t)s * (mn / 4)];
+    a[1] += src[(size_t)s * (mn / 4) + 1];
+  }
+  const float ia = 1.0f / p.sx[p.rowwise ? m : 0];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = n + 4 * h;
+    float f[4];
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      const float2 b = bias_pair(p.e, c + j);
+      f[j] = add32((a[h][j] * ia) * (1.0f / p.sw[p.rowwise ? c + j : 0]), b.x);
+      f[j + 1] = add32((a[h][j + 1] * ia) * (1.0f / p.sw[p.rowwise ? c + j + 1 : 0]), b.y);
+    }
+    const size_t at = (size_t)i * 8 + 4 * h;
+    uint2 r = make_uint2(0u, 0u), z;
+    if (p.e.res) r = *reinterpret_cast<const uint2 *>(p.e.res + at);
+    const uint2 y = act_out4<FORM>(p.e.act, f, p.e.res != nullptr, r, z);
+    if (p.e.a) *reinterpret_cast<uint2 *>(p.e.a + at) = z;
+    if (p.e.C[0]) *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.e.C[0]) + at) = y;
+  }
+}
+
+// Parts of the contraction of an [M, N] output; 1: not split.
+constexpr int64_t SPLIT_TILES = 512;              // workgroups: two a compute unit
+#ifndef FP8L_SPLIT_KT
+#define FP8L_SPLIT_KT 4
+#endif
+int act_parts(int64_t M, int64_t N, int64_t K, int *part_kt) {
+  const int64_t t = tiles(M, TM) * tiles(N, TB), nk = tiles(K, BK);
+  int64_t s = SPLIT_TILES / t;
+  if (s > nk / FP8L_SPLIT_KT) s = nk / FP8L_SPLIT_KT;
+  if (t > 128 || s < 2) return 1;
+  *part_kt = (int)tiles(nk, s);
+  return (int)tiles(nk, *part_kt);
+}
+size_t act_split_bytes(int64_t M, int64_t N) {
+  // at most SPLIT_TILES tiles of partial sums
+  size_t b = (size_t)SPLIT_TILES * TM * TB * sizeof(float);
+  const size_t all = (size_t)(SPLIT_TILES * M * N) * sizeof(float);
+  return b < all ? b : all;
+}
+
+template <int FORM>
+hipError_t act_split_launch(ActArgs &g, const float *sx, const float *sw, bool rw, int parts,
+                            hipStream_t stream) {
+  g.tiles_m[0] = (int)tiles(g.M[0], TM);
+  g.tiles_n[0] = (int)tiles(g.N[0], TB);
+  g.total = g.tiles_m[0] * g.tiles_n[0];
+  hipLaunchKernelGGL((k_gate_tile<EPI_SPLIT, 0, false>), dim3((unsigned)g.total, (unsigned)parts),
+                     dim3(256), 0, stream, g);
+  const ActJoinArgs p = {g, sx, sw, parts, rw};
+  const int64_t n8 = (int64_t)g.M[0] * g.N[0] / 8;
+  hipLaunchKernelGGL((k_act_join<FORM>), dim3((unsigned)((n8 + 255) / 256)), dim3(256), 0, stream,
+                     p, n8);
   return hipGetLastError();
 }
 
@@ -172,8 +265,11 @@ size_t linear_act_maxima_bytes(int64_t M, int64_t N, int scaling) {
 }
 
 size_t linear_act_workspace_bytes(int64_t M, int64_t N, int scaling) {
-  // column sums: a slice per 32 rows at most (small tiles)
-  const size_t sums = (size_t)(2 * tiles(M, TM)) * (size_t)N * sizeof(float);
+  // column sums: a slice per 32 rows at most (small tiles); or the partial sums of a
+  // split contraction
+  size_t sums = (size_t)(2 * tiles(M, TM)) * (size_t)N * sizeof(float);
+  const size_t split = act_split_bytes(M, N);
+  if (sums < split) sums = split;
   return linear_act_maxima_bytes(M, N, scaling) + ((sums + 255) & ~(size_t)255);
 }
 
@@ -214,6 +310,12 @@ hipError_t linear_act_fwd_launch(const LinearActIn &in, int scaling, const Fp8Ou
       if (act_few_tokens(M, N)) {
         const ActSkinnyArgs p = {in.xq, in.wq, in.sx, in.sw, g, (int)M, (int)N, (int)K, rw};
         return act_skinny_launch<FORM>(p, stream);
+      }
+      const int parts = act_parts(M, N, K, &g.part_kt);
+      if (parts > 1) {
+        g.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) +
+                                              linear_act_maxima_bytes(M, N, scaling));
+        return act_split_launch<FORM>(g, in.sx, in.sw, rw, parts, stream);
       }
       measured = o && o->qt;
       g.maxima = measured;

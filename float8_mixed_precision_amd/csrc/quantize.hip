@@ -454,9 +454,16 @@ __device__ __forceinline__ void cast_tile(
           for (int j = 0; j < 4; ++j) srs[j] = scale[r + j];
         }
       }
+      // (with an activation, whose code is not one block, the loads come first, or
+      // each row's would wait for the row before)
+      U4 vs[4];
+      if (SRC == SRC_ACT) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) vs[j] = load16(x + (size_t)(r + j) * cols + c);
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const U4 v = load16(x + (size_t)(r + j) * cols + c);
+        const U4 v = SRC == SRC_ACT ? vs[j] : load16(x + (size_t)(r + j) * cols + c);
         float f[8];
         f[0] = bf16_to_f32(v.x & 0xFFFFu); f[1] = bf16_to_f32(v.x >> 16);
         f[2] = bf16_to_f32(v.y & 0xFFFFu); f[3] = bf16_to_f32(v.y >> 16);
