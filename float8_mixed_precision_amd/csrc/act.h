@@ -6,8 +6,9 @@
 //       s(v) = 1 / (1 + e^-v)
 //   gelu(z) = z P(z), P the normal distribution function
 //
-// in three forms of code:
-//  ACT_PW    none, relu, relu2
+// in four forms of code:
+//  ACT_ID    none
+//  ACT_RELUS relu and relu2
 //  ACT_SIG   silu and gelu_tanh: v = z (c1 + c3 z^2) with c1 and c3 from the call
 //  ACT_ERF   gelu: P(-t) = e^(-t^2/2) m(u), t = |z|, u = 1 / (1 + 0.3 t), m a
 //            polynomial of degree 6: the scaled tail e^(t^2/2) P(-t) is smooth in u
@@ -29,11 +30,12 @@
 namespace fp8l {
 namespace {
 
-constexpr int ACT_PW = 0, ACT_SIG = 1, ACT_ERF = 2;
+constexpr int ACT_ID = 0, ACT_RELUS = 1, ACT_SIG = 2, ACT_ERF = 3, ACT_FORMS = 4;
 
 constexpr int act_form(int act) {
   return act == FP8L_ACT_GELU ? ACT_ERF
-         : act == FP8L_ACT_GELU_TANH || act == FP8L_ACT_SILU ? ACT_SIG : ACT_PW;
+         : act == FP8L_ACT_GELU_TANH || act == FP8L_ACT_SILU ? ACT_SIG
+         : act == FP8L_ACT_NONE ? ACT_ID : ACT_RELUS;
 }
 
 // What the forms need of the activation, worked out on the host.
@@ -95,9 +97,9 @@ __device__ __forceinline__ float act_value(const ActConsts &c, float z) {
     const float n = normal_tail(t, e);
     return __builtin_fmaf(-t, n, max_nan(z, 0.f));
   }
-  if (c.act == FP8L_ACT_NONE) return z;           // uniform
+  if (FORM == ACT_ID) return z;
   const float m = max_nan(z, 0.f);
-  return c.act == FP8L_ACT_RELU ? m : m * m;
+  return m * (c.act == FP8L_ACT_RELU ? 1.f : m);
 }
 
 template <int FORM>
@@ -118,9 +120,8 @@ __device__ __forceinline__ float act_slope(const ActConsts &c, float z) {
     const float cdf = z >= 0.f ? 1.0f - n : n;
     return __builtin_fmaf(__builtin_copysignf(t, z), e * 0.39894228040143268f, cdf);
   }
-  if (c.act == FP8L_ACT_NONE) return 1.f;         // uniform
-  const float m = max_nan(z, 0.f);
-  return c.act == FP8L_ACT_RELU ? (z <= 0.f ? 0.f : 1.f) : 2.f * m;
+  if (FORM == ACT_ID) return 1.f;
+  return z <= 0.f ? 0.f : c.act == FP8L_ACT_RELU ? 1.f : 2.f * z;
 }
 
 // A sum with a rounding of its own: the compiler would fuse a product in front of it
@@ -137,7 +138,7 @@ __device__ __forceinline__ uint2 act_out4(const ActConsts &c, const float (&f)[4
                                           uint2 r, uint2 &z) {
   z = make_uint2(bf16x2_bits(f[0], f[1]), bf16x2_bits(f[2], f[3]));
   float v[4] = {f[0], f[1], f[2], f[3]};
-  if (FORM != ACT_PW || c.act != FP8L_ACT_NONE) {
+  if (FORM != ACT_ID) {
     const float b[4] = {bf16_to_f32(z.x & 0xFFFFu), __uint_as_float(z.x & 0xFFFF0000u),
                         bf16_to_f32(z.y & 0xFFFFu), __uint_as_float(z.y & 0xFFFF0000u)};
 #pragma unroll
@@ -152,15 +153,16 @@ __device__ __forceinline__ uint2 act_out4(const ActConsts &c, const float (&f)[4
   return make_uint2(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]));
 }
 
-// The form chosen at run time (kernels that memory bounds).
+// The form of an activation (not ACT_ID) chosen at run time, in kernels that memory
+// bounds.
 __device__ __forceinline__ float act_value_any(const ActConsts &c, int form, float z) {
   return form == ACT_SIG ? act_value<ACT_SIG>(c, z)
-         : form == ACT_ERF ? act_value<ACT_ERF>(c, z) : act_value<ACT_PW>(c, z);
+         : form == ACT_ERF ? act_value<ACT_ERF>(c, z) : act_value<ACT_RELUS>(c, z);
 }
 
 __device__ __forceinline__ float act_slope_any(const ActConsts &c, int form, float z) {
   return form == ACT_SIG ? act_slope<ACT_SIG>(c, z)
-         : form == ACT_ERF ? act_slope<ACT_ERF>(c, z) : act_slope<ACT_PW>(c, z);
+         : form == ACT_ERF ? act_slope<ACT_ERF>(c, z) : act_slope<ACT_RELUS>(c, z);
 }
 
 }  // namespace

@@ -258,7 +258,7 @@ __global__ __launch_bounds__(256) void k_gate_tile(typename ArgsOf<EPI>::type g)
   float bias[ACT ? NJ : 1][4];
   if constexpr (ACT || DACT) {
     // the residual or z, and the bias
-    const uint16_t *in = ACT ? g.res : g.act.act != FP8L_ACT_NONE ? g.a : nullptr;
+    const uint16_t *in = ACT ? g.res : EPI != EPI_DACT + ACT_ID ? g.a : nullptr;
     if (in) {                                      // uniform
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
@@ -387,7 +387,7 @@ __global__ __launch_bounds__(256) void k_gate_tile(typename ArgsOf<EPI>::type g)
         float f[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) f[e] = (p[e] * ia[i]) * ib[j][e];
-        if (g.act.act != FP8L_ACT_NONE) {          // uniform
+        if constexpr (EPI != EPI_DACT + ACT_ID) {
           const float z[4] = {bf16_lo(ga[j][i].x), bf16_hi(ga[j][i].x), bf16_lo(ga[j][i].y),
                               bf16_hi(ga[j][i].y)};
 #pragma unroll

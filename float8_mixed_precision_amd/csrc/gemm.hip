@@ -215,7 +215,7 @@ static_assert(sizeof(GemmGroup) <= 4096, "kernel arguments");
 //             B^T (not rounded) and z read from `a` where the tile is finished, C
 //             receives dz = dh act'(z), colsum the sums of the unrounded dz over
 //             each wave's rows, [slice][N].
-//             (form: ACT_PW, ACT_SIG or ACT_ERF of act.h)
+//             (form: ACT_ID, ACT_RELUS, ACT_SIG or ACT_ERF of act.h)
 //  EPI_SPLIT  (small tiles only) one part of the contraction: its unscaled fp32 sums
 //             go to partial[part][M][N].
 // The gate's forms take the amax partial maxima of what they write (of h, or of da
@@ -227,8 +227,8 @@ static_assert(sizeof(GemmGroup) <= 4096, "kernel arguments");
 constexpr int EPI_NONE = 0, EPI_GATE = 1, EPI_GATE_AB = 2, EPI_DGATE = 3;
 constexpr int EPI_ACT = 4, EPI_DACT = 8, EPI_SPLIT = 12;
 constexpr bool is_gate(int epi) { return epi == EPI_GATE || epi == EPI_GATE_AB; }
-constexpr bool is_act(int epi) { return epi >= EPI_ACT && epi < EPI_ACT + 3; }
-constexpr bool is_dact(int epi) { return epi >= EPI_DACT && epi < EPI_DACT + 3; }
+constexpr bool is_act(int epi) { return epi >= EPI_ACT && epi < EPI_ACT + ACT_FORMS; }
+constexpr bool is_dact(int epi) { return epi >= EPI_DACT && epi < EPI_DACT + ACT_FORMS; }
 struct GateArgs : GemmGroup {
   const uint8_t *B2;           // is_gate(EPI)
   const float *sb2;
@@ -303,6 +303,23 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
   return v;
 }
 
+// Sum, and maxima of u16 pairs, over the lanes l, l ^ 8, l ^ 16, ... of a wave, in all
+// of them: a rotation by half a row of 16 lanes, then exchanges of rows and of halves.
+__device__ __forceinline__ float lanes_sum8(float v) {
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xF, 0xF, true));
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+__device__ __forceinline__ uint32_t lanes_pk_max8(uint32_t v) {
+  v = pk_max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, true));
+  auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = pk_max(a[0], a[1]);
+  auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return pk_max(b[0], b[1]);
+}
+
 // element i of a kernel-argument array for a wave-uniform i (selects, so the
 // array is never copied to private memory)
 template <class T>
@@ -343,6 +360,10 @@ constexpr int EPI_STORES = 32;
 // become reciprocals between the MFMAs of the last k-tile of the tile
 // before it.
 constexpr int SCALE_DMAS = 2;
+#ifndef FP8L_IN_AHEAD
+#define FP8L_IN_AHEAD 2
+#endif
+constexpr int IN_AHEAD = FP8L_IN_AHEAD;
 constexpr int RW_STAGE_OFF = EPI_WAVE_BYTES / 2;
 static_assert(2 * SCALE_BYTES <= RW_STAGE_OFF, "two scale tables below the rowwise staging");
 static_assert(EPI_WAVE_BYTES == 64 * BK, "a wave's staging is at its operand offset + EPI_OFF");
@@ -1171,7 +1192,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
       constexpr bool ACT = is_act(EPI);
       constexpr int FORM = EPI - (ACT ? EPI_ACT : EPI_DACT);
       uint8_t *sf = epi + RW_STAGE_OFF;
-      const bool has_z = ACT ? g.a != nullptr : g.act.act != FP8L_ACT_NONE;
+      const bool has_z = ACT ? g.a != nullptr : FORM != ACT_ID;
       const bool has_in = ACT ? g.res != nullptr : has_z;     // uniform
       const __amdgpu_buffer_rsrc_t rsZ =
           __builtin_amdgcn_make_buffer_rsrc(g.a, (short)0, g.a ? M * N * 2 : 0, 0x00020000);
@@ -1190,22 +1211,20 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
       // row maxima of the left half wait here for the right one's
       uint32_t rmax[RW ? NF : 1][2];
       auto row_off = [&](int i, int u) { return (uint32_t)(i * FR + u * 8) * (uint32_t)N * 2u; };
-      // The residual or z: all of a half's loads in flight together, the right half's
-      // each as soon as its registers fall free (a wave alone on its SIMD covers no
-      // trip to memory but by loads of its own: with one pass ahead, 8 KB a compute
-      // unit, z cost 46 us of 8192 x 14336)
-      v4u in[NF][2];
-      auto load_in = [&](int jh, int i) {
+      // the residual or z of pass jh 8 + i, IN_AHEAD passes ahead
+      v4u in[IN_AHEAD + 1][2];
+      auto load_in = [&](int pass) {
+        const int jh = pass / NF, i = pass % NF;
         const int col = n0 + wn * WN + jh * 64 + (lane_e & 7) * 8;
         const uint32_t at = ((uint32_t)row0 * (uint32_t)N + (uint32_t)col) * 2u;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-          in[i][u] = __builtin_amdgcn_raw_buffer_load_b128(
+          in[pass % (IN_AHEAD + 1)][u] = __builtin_amdgcn_raw_buffer_load_b128(
               rsIn, col < N && i * FR + u * 8 < M - row0 ? at : OOB_C, row_off(i, u), 0);
       };
       if (has_in) {
 #pragma unroll
-        for (int i = 0; i < NF; ++i) load_in(0, i);
+        for (int i = 0; i < IN_AHEAD; ++i) load_in(i);
       }
 #pragma unroll
       for (int jh = 0; jh < 2; ++jh) {
@@ -1252,6 +1271,8 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
         float cs[8] = {};
 #pragma unroll
         for (int i = 0; i < NF; ++i) {
+          const int pass = jh * NF + i;
+          if (has_in && pass + IN_AHEAD < 2 * NF) load_in(pass + IN_AHEAD);
           if (i + 1 < NF) stage(i + 1);
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
@@ -1267,7 +1288,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
               y = pack8(f);                       // z
               if (has_z)
                 __builtin_amdgcn_raw_buffer_store_b128(y, rsZ, off, row_off(i, u), C_STORE_AUX);
-              if (FORM != ACT_PW || g.act.act != FP8L_ACT_NONE) {
+              if (FORM != ACT_ID) {
                 unpack8(f, y);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) f[e] = act_value<FORM>(g.act, f[e]);
@@ -1275,7 +1296,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
               }
               if (has_in) {
                 float r[8];
-                unpack8(r, in[i][u]);
+                unpack8(r, in[pass % (IN_AHEAD + 1)][u]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) f[e] = add32(f[e], r[e]);
                 y = pack8(f);
@@ -1283,7 +1304,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
             } else {
               if (has_in) {
                 float z[8];
-                unpack8(z, in[i][u]);
+                unpack8(z, in[pass % (IN_AHEAD + 1)][u]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) f[e] *= act_slope<FORM>(g.act, z[e]);
               }
@@ -1311,19 +1332,19 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
               }
             }
           }
-          if (jh == 0 && has_in) load_in(1, i);
           FP8P_E()                                // (mixed passes spill)
         }
-        if (RW && g.maxima)
-          store_colmax<8>(cm, lane_e, col_ok,
-                          g.colpart[0] + (size_t)((m0 / BM) * 2 + wm) * N + scol);
+        if (RW && g.maxima) {
+          v4u r;
+#pragma unroll
+          for (int d = 0; d < 4; ++d) r[d] = lanes_pk_max8(cm[d]);
+          if (lane_e < 8 && col_ok)
+            *reinterpret_cast<v4u *>(g.colpart[0] + (size_t)((m0 / BM) * 2 + wm) * N + scol) = r;
+        }
         if (!ACT && g.colsum) {
           // the lanes of a column add up in a fixed order
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-#pragma unroll
-            for (int o = 8; o < 64; o <<= 1) cs[e] += __shfl_xor(cs[e], o);
-          }
+          for (int e = 0; e < 8; ++e) cs[e] = lanes_sum8(cs[e]);
           if (lane_e < 8 && col_ok) {
             v4f *dst = reinterpret_cast<v4f *>(g.colsum + (size_t)((m0 / BM) * 2 + wm) * N + scol);
             dst[0] = (v4f){cs[0], cs[1], cs[2], cs[3]};

@@ -212,9 +212,10 @@ __global__ __launch_bounds__(256) void k_act_k0(ActArgs g, int64_t n8) {
 template <class F>
 hipError_t with_form(int act, F f) {
   switch (act_form(act)) {
+    case ACT_RELUS: return f(std::integral_constant<int, ACT_RELUS>());
     case ACT_SIG: return f(std::integral_constant<int, ACT_SIG>());
     case ACT_ERF: return f(std::integral_constant<int, ACT_ERF>());
-    default: return f(std::integral_constant<int, ACT_PW>());
+    default: return f(std::integral_constant<int, ACT_ID>());
   }
 }
 
