@@ -41,6 +41,7 @@ constexpr int act_form(int act) {
 // What the forms need of the activation, worked out on the host.
 struct ActConsts {
   int act;
+  uint32_t peak;               // |z| in bf16 where |act| is largest for z < 0, twice
   float c1, c3;                // ACT_SIG: e^-v = 2^(z (c1 + c3 z^2))
   float d1, d3;                // ACT_SIG: dv/dz = d1 + d3 z^2
 };
@@ -49,6 +50,9 @@ inline ActConsts act_consts(int act) {
   constexpr float L = 1.44269504088896341f, K = 1.59576912160573071f;   // log2 e, 2 sqrt(2/pi)
   ActConsts c = {};
   c.act = act;
+  // gelu -0.7518, gelu_tanh -0.7525, silu -1.2785 (the others are 0 for z < 0)
+  c.peak = act == FP8L_ACT_SILU ? 0x3FA43FA4u : act == FP8L_ACT_GELU_TANH ? 0x3F413F41u
+                                                                          : 0x3F403F40u;
   if (act == FP8L_ACT_SILU) {
     c.c1 = -L;
     c.d1 = 1.f;
@@ -151,6 +155,52 @@ __device__ __forceinline__ uint2 act_out4(const ActConsts &c, const float (&f)[4
     v[3] = add32(v[3], __uint_as_float(r.y & 0xFFFF0000u));
   }
   return make_uint2(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]));
+}
+
+// The largest |act(z)| of many bf16 z without evaluating act at each: act grows for z
+// >= 0, and for z < 0 |act| grows up to one peak (the derivative's zero) and falls
+// beyond it, so one of four z decides: the largest, the negative ones nearest the peak
+// on either side, and a NaN of negative sign.  (fp32 errors of act do not matter:
+// around the peak all z have one bf16 value, and elsewhere neighbours differ by 2^-9
+// relatively or more.)  Found on bit patterns, two z a register, in 3 instructions an
+// element where evaluating takes 11 to 18:
+//   top     signed maximum: the largest z >= 0, or a NaN of positive sign
+//   below   unsigned minimum of d = (z ^ sign) - peak: z <= peak nearest to it
+//   above   unsigned maximum of d: peak < z < 0 nearest to it (d wraps around)
+//   neg     unsigned maximum of z: a NaN of negative sign sorts above all others
+// A z of +0 changes none of them.
+struct ActKeys {
+  uint32_t top, below, above, neg;
+};
+__device__ __forceinline__ void act_keys_add(ActKeys &k, uint32_t z, uint32_t peak) {
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  typedef short i16x2 __attribute__((ext_vector_type(2)));
+#define FP8L_U2(v) __builtin_bit_cast(u16x2, v)
+#define FP8L_I2(v) __builtin_bit_cast(i16x2, v)
+  const u16x2 d = FP8L_U2(z ^ 0x80008000u) - FP8L_U2(peak);
+  k.top = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(FP8L_I2(k.top), FP8L_I2(z)));
+  k.below = __builtin_bit_cast(uint32_t, __builtin_elementwise_min(FP8L_U2(k.below), d));
+  k.above = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(FP8L_U2(k.above), d));
+  k.neg = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(FP8L_U2(k.neg), FP8L_U2(z)));
+#undef FP8L_U2
+#undef FP8L_I2
+}
+// The u16 bits of the largest |bf16(act(z))| of a wave's keys, in every lane.
+template <int FORM>
+__device__ __forceinline__ uint32_t act_keys_amax(const ActConsts &c, const ActKeys &k) {
+  const uint32_t peak = c.peak & 0xFFFFu;
+  auto of = [&](uint32_t z16) {
+    return bf16x2_bits(act_value<FORM>(c, __uint_as_float(z16 << 16)), 0.f) & 0x7FFFu;
+  };
+  const uint32_t top = wave_max(hmax16(k.top ^ 0x80008000u)) ^ 0x8000u;
+  const uint32_t below = 0xFFFFu - wave_max(hmax16(~k.below));
+  const uint32_t above = wave_max(hmax16(k.above));
+  const uint32_t neg = wave_max(hmax16(k.neg));
+  uint32_t m = of(top);
+  if (below < 0x8000u - peak) m = max(m, of((below + peak) | 0x8000u));
+  if (above >= 0x10000u - peak) m = max(m, of(((above + peak) & 0x7FFFu) | 0x8000u));
+  if (neg > 0xFF80u) m = max(m, of(neg));
+  return m;
 }
 
 // The form of an activation (not ACT_ID) chosen at run time, in kernels that memory

@@ -153,33 +153,8 @@ __global__ __launch_bounds__(AM_THREADS) void k_fold_maxima(const uint32_t *part
   if (threadIdx.x == 0) out[blockIdx.x] = max(max(red[0], red[1]), max(red[2], red[3]));
 }
 
-// Sums of the columns of part[slices][cols], to fp32 or bf16.  Workgroup: 64
-// columns, 16 slices of the partial rows joined in LDS in slice order.
-// slices = 0 gives zeros.
-__global__ __launch_bounds__(64 * FIN_SLICES) void k_column_sums(const float *__restrict__ part,
-                                                                 int slices, int cols, void *out,
-                                                                 int f32) {
-  const int c = (int)blockIdx.x * 64 + (threadIdx.x & 63);
-  const int sl = threadIdx.x >> 6;
-  const int cc = min(c, cols - 1);
-  float s = 0.f;
-  for (int i0 = sl; i0 < slices; i0 += FIN_SLICES * 8) {
-    float v[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      v[u] = part[(size_t)min(i0 + FIN_SLICES * u, slices - 1) * cols + cc];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) s += i0 + FIN_SLICES * u < slices ? v[u] : 0.f;
-  }
-  __shared__ float red[FIN_SLICES][64];
-  red[sl][threadIdx.x & 63] = s;
-  __syncthreads();
-  if (sl == 0 && c < cols) {
-#pragma unroll
-    for (int i = 1; i < FIN_SLICES; ++i) s += red[i][threadIdx.x];
-    if (f32) static_cast<float *>(out)[c] = s;
-    else static_cast<uint16_t *>(out)[c] = (uint16_t)bf16x2_bits(s, 0.f);
-  }
+__global__ __launch_bounds__(64 * FIN_SLICES) void k_column_sums(CastSums s) {
+  column_sums<FIN_SLICES>(s, (int)blockIdx.x);
 }
 
 // ----------------------------------------------------------- rows alone --
@@ -237,12 +212,12 @@ __global__ __launch_bounds__(1024) void k_quantize_rows(const uint16_t *__restri
 // ------------------------------------------------------------- launches --
 
 // The pass, its maxima where a quantize of [rows, cols] expects them in `ws`, and
-// the cast of `cast` (an activation `act` applied there, or none).
+// the cast of `cast` (an activation `act` applied there, or none) with the column sums
+// that src names.
 template <bool BWD>
 hipError_t bias_act_pass(BiasActArgs a, const void *cast, int cast_act, int scaling,
-                         const Fp8Out &o, void *ws, hipStream_t stream) {
+                         const Fp8Out &o, void *ws, CastSource src, hipStream_t stream) {
   const bool rw = (scaling & FP8L_ROWWISE) != 0;
-  CastSource src = {};
   src.x = cast;
   src.act = cast_act;
   if (rw) quantize_rowwise_partials(ws, a.rows, a.cols, &a.rowpart, &a.colpart);
@@ -284,7 +259,7 @@ hipError_t column_sums_launch(const float *part, int slices, int64_t cols, void 
                               hipStream_t stream) {
   if (cols > 0)
     hipLaunchKernelGGL(k_column_sums, dim3((unsigned)cdiv(cols, 64)), dim3(64 * FIN_SLICES), 0,
-                       stream, part, slices, (int)cols, out, f32);
+                       stream, CastSums{part, slices, (int)cols, f32, 0, out});
   return hipGetLastError();
 }
 
@@ -308,7 +283,7 @@ hipError_t quantize_act_launch(const void *x, int act, int64_t rows, int64_t col
   a.form = act_form(act);
   a.rows = (int)rows;
   a.cols = (int)cols;
-  return bias_act_pass<false>(a, x, act, scaling, o, workspace, stream);
+  return bias_act_pass<false>(a, x, act, scaling, o, workspace, CastSource{}, stream);
 }
 
 hipError_t bias_act_bwd_launch(const void *dy, const void *z, int act, int64_t rows, int64_t cols,
@@ -323,10 +298,15 @@ hipError_t bias_act_bwd_launch(const void *dy, const void *z, int act, int64_t r
   a.form = act_form(act);
   a.rows = (int)rows;
   a.cols = (int)cols;
+  CastSource src = {};
+  src.sums = a.sums;
+  src.slices = (int)cdiv(rows, AM_TR);
+  src.sums_f32 = dbias_f32;
+  src.sums_out = dbias;
   const hipError_t e =
-      bias_act_pass<true>(a, dz ? dz : dy, FP8L_ACT_NONE, scaling, o, maxima, stream);
-  if (e != hipSuccess || !dbias) return e;
-  return column_sums_launch(sums, (int)cdiv(rows, AM_TR), cols, dbias, dbias_f32, stream);
+      bias_act_pass<true>(a, dz ? dz : dy, FP8L_ACT_NONE, scaling, o, maxima, src, stream);
+  if (e != hipSuccess || !dbias || rows > 0) return e;
+  return column_sums_launch(nullptr, 0, cols, dbias, dbias_f32, stream);
 }
 
 }  // namespace fp8l

@@ -187,8 +187,13 @@ struct CastSource {
   const uint16_t *rowpart, *colpart;
   int row_slices, col_slices;
   int act;                     // FP8L_ACT_*: quantized is act(x), rounded to bf16 (E4M3)
+  // column sums to finish beside the cast, from sums[slices][cols] to fp32 or bf16
+  // (x itself is quantized; NULL: none)
+  const float *sums;
+  int slices, sums_f32;
+  void *sums_out;
 };
-// count (1, or 2 with neither rstd nor act) tensors of one shape and one count of partials, in
+// count (1, or 2 with none of rstd, act and sums) tensors of one shape and one count of partials, in
 // the same launches.
 hipError_t quantize_cast_launch(const CastSource *src, int count, int64_t rows, int64_t cols,
                                 int scaling, const Fp8Out *o, hipStream_t stream);

@@ -380,7 +380,7 @@ __global__ __launch_bounds__(256) void k_gate_tile(typename ArgsOf<EPI>::type g)
         for (int e = 0; e < 4; ++e) f[e] = add32((p[e] * ia[i]) * ib[j][e], bias[j][e]);
         const uint2 r = g.res ? ga[j][i] : make_uint2(0u, 0u);
         uint2 z;
-        o[0] = act_out4<EPI - EPI_ACT>(g.act, f, g.res != nullptr, r, z);
+        o[0] = act_out4<form_of(EPI)>(g.act, f, g.res != nullptr, r, z);
         if (ok && g.a) *reinterpret_cast<uint2 *>(g.a + at) = z;
         if (ok && C) *reinterpret_cast<uint2 *>(C + at) = o[0];
       } else if constexpr (DACT) {
@@ -391,7 +391,7 @@ __global__ __launch_bounds__(256) void k_gate_tile(typename ArgsOf<EPI>::type g)
           const float z[4] = {bf16_lo(ga[j][i].x), bf16_hi(ga[j][i].x), bf16_lo(ga[j][i].y),
                               bf16_hi(ga[j][i].y)};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) f[e] *= act_slope<EPI - EPI_DACT>(g.act, z[e]);
+          for (int e = 0; e < 4; ++e) f[e] *= act_slope<form_of(EPI)>(g.act, z[e]);
         }
         o[0] = make_uint2(bf16x2_bits(f[0], f[1]), bf16x2_bits(f[2], f[3]));
         if (ok) *reinterpret_cast<uint2 *>(C + at) = o[0];

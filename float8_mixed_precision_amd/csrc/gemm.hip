@@ -225,10 +225,22 @@ static_assert(sizeof(GemmGroup) <= 4096, "kernel arguments");
 // colpart[o][slice][N], one slice per wave column / wave row of the tiles
 // (EPI_DGATE takes them always).  EPI_ACT (of y) and EPI_DACT (of dz) do likewise.
 constexpr int EPI_NONE = 0, EPI_GATE = 1, EPI_GATE_AB = 2, EPI_DGATE = 3;
-constexpr int EPI_ACT = 4, EPI_DACT = 8, EPI_SPLIT = 12;
+// (EPI_ACT_RES: EPI_ACT with a residual, in the large tiles, whose waits for it count
+// stores that must not be conditional)
+constexpr int EPI_ACT = 4, EPI_DACT = 8, EPI_SPLIT = 12, EPI_ACT_RES = 16;
 constexpr bool is_gate(int epi) { return epi == EPI_GATE || epi == EPI_GATE_AB; }
-constexpr bool is_act(int epi) { return epi >= EPI_ACT && epi < EPI_ACT + ACT_FORMS; }
+constexpr bool is_act_res(int epi) { return epi >= EPI_ACT_RES && epi < EPI_ACT_RES + ACT_FORMS; }
+constexpr bool is_act(int epi) {
+  return (epi >= EPI_ACT && epi < EPI_ACT + ACT_FORMS) || is_act_res(epi);
+}
 constexpr bool is_dact(int epi) { return epi >= EPI_DACT && epi < EPI_DACT + ACT_FORMS; }
+constexpr int form_of(int epi) {
+  return epi - (is_act_res(epi) ? EPI_ACT_RES : is_act(epi) ? EPI_ACT : EPI_DACT);
+}
+// whether a kernel may take the maximum of an unstored y from keys of z
+constexpr bool may_key(int epi, bool rowwise) {
+  return is_act(epi) && !is_act_res(epi) && !rowwise && form_of(epi) != ACT_ID;
+}
 struct GateArgs : GemmGroup {
   const uint8_t *B2;           // is_gate(EPI)
   const float *sb2;
@@ -243,6 +255,8 @@ struct ActArgs : GateArgs {    // a: z
   int bias_f32;
   const uint16_t *res;         // residual [M, N], or NULL
   ActConsts act;
+  int keys;                    // EPI_ACT, tensorwise: y is not stored, its maximum
+                               // comes from the keys of z (act.h)
   float *colsum;               // EPI_DACT; NULL: not wanted
   float *partial;              // EPI_SPLIT
   int part_kt;                 // EPI_SPLIT: k-tiles of a part
@@ -811,6 +825,11 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
 #define FP8P_BIAS_TAB(TILE)                                                       \
   reinterpret_cast<float2 *>(epi + (RW ? ((TILE) & 1) * SCALE_BYTES + (1 - wm) * WM * 4 : 1024))
   if (EPI != EPI_NONE && !RW) *FP8P_TMAX() = make_uint2(0u, 0u);
+  // EPI_ACT with keys: those instead, in the first KB
+#define FP8P_KEYS() (reinterpret_cast<v4u *>(epi) + hw_lane())
+  if constexpr (may_key(EPI, RW)) {
+    if (g.keys) *FP8P_KEYS() = (v4u){0u, ~0u, 0u, 0u};
+  }
   int st = 0;          // stage of the current unit
   for (int tile = 0;; ++tile) {
     const TileCoord tc = {a_pi, a_m0, a_n0, a_ok};
@@ -1190,10 +1209,12 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
       // l / 8 + 8.  The next pass is staged and read back, and its part of the
       // residual or of z loaded, before this one is computed.
       constexpr bool ACT = is_act(EPI);
-      constexpr int FORM = EPI - (ACT ? EPI_ACT : EPI_DACT);
+      constexpr int FORM = form_of(EPI);
+      constexpr bool HAS_IN = is_act_res(EPI) || (!ACT && FORM != ACT_ID);
       uint8_t *sf = epi + RW_STAGE_OFF;
-      const bool has_z = ACT ? g.a != nullptr : FORM != ACT_ID;
-      const bool has_in = ACT ? g.res != nullptr : has_z;     // uniform
+      // (with loads to wait for, the stores between them are not conditional: without
+      // a z they go to an empty buffer and are dropped)
+      const bool has_z = ACT && (HAS_IN || g.a != nullptr);   // uniform
       const __amdgpu_buffer_rsrc_t rsZ =
           __builtin_amdgcn_make_buffer_rsrc(g.a, (short)0, g.a ? M * N * 2 : 0, 0x00020000);
       const __amdgpu_buffer_rsrc_t rsIn =
@@ -1207,7 +1228,16 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
       const int row0 = m0 + wm * WM + r8;
       // (the whole offset is checked against the resource, which drops rows past M)
       const uint32_t row_at = (lane_e & 7) == 0 ? (uint32_t)row0 * 2 : OOB_C;
-      uint32_t tmax = RW ? 0u : FP8P_TMAX()->x;
+      constexpr bool KEYS = may_key(EPI, RW);
+      const bool keyed = KEYS && g.keys;          // uniform
+      uint32_t tmax = RW || keyed ? 0u : FP8P_TMAX()->x;
+      ActKeys keys = {};
+      if constexpr (KEYS) {
+        if (keyed) {
+          const v4u k = *FP8P_KEYS();
+          keys = {k.x, k.y, k.z, k.w};
+        }
+      }
       // row maxima of the left half wait here for the right one's
       uint32_t rmax[RW ? NF : 1][2];
       auto row_off = [&](int i, int u) { return (uint32_t)(i * FR + u * 8) * (uint32_t)N * 2u; };
@@ -1222,7 +1252,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
           in[pass % (IN_AHEAD + 1)][u] = __builtin_amdgcn_raw_buffer_load_b128(
               rsIn, col < N && i * FR + u * 8 < M - row0 ? at : OOB_C, row_off(i, u), 0);
       };
-      if (has_in) {
+      if constexpr (HAS_IN) {
 #pragma unroll
         for (int i = 0; i < IN_AHEAD; ++i) load_in(i);
       }
@@ -1272,7 +1302,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
 #pragma unroll
         for (int i = 0; i < NF; ++i) {
           const int pass = jh * NF + i;
-          if (has_in && pass + IN_AHEAD < 2 * NF) load_in(pass + IN_AHEAD);
+          if (HAS_IN && pass + IN_AHEAD < 2 * NF) load_in(pass + IN_AHEAD);
           if (i + 1 < NF) stage(i + 1);
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
@@ -1288,13 +1318,21 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
               y = pack8(f);                       // z
               if (has_z)
                 __builtin_amdgcn_raw_buffer_store_b128(y, rsZ, off, row_off(i, u), C_STORE_AUX);
+              if constexpr (KEYS) {
+                if (keyed) {
+#pragma unroll
+                  for (int d = 0; d < 4; ++d)
+                    act_keys_add(keys, off != OOB_C ? y[d] : 0u, g.act.peak);
+                  continue;
+                }
+              }
               if (FORM != ACT_ID) {
                 unpack8(f, y);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) f[e] = act_value<FORM>(g.act, f[e]);
-                if (!has_in) y = pack8(f);
+                if (!HAS_IN) y = pack8(f);
               }
-              if (has_in) {
+              if constexpr (HAS_IN) {
                 float r[8];
                 unpack8(r, in[pass % (IN_AHEAD + 1)][u]);
 #pragma unroll
@@ -1302,7 +1340,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
                 y = pack8(f);
               }
             } else {
-              if (has_in) {
+              if constexpr (HAS_IN) {
                 float z[8];
                 unpack8(z, in[pass % (IN_AHEAD + 1)][u]);
 #pragma unroll
@@ -1352,7 +1390,12 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
           }
         }
       }
-      if (!RW) FP8P_TMAX()->x = tmax;
+      if constexpr (KEYS) {
+        if (keyed) *FP8P_KEYS() = (v4u){keys.top, keys.below, keys.above, keys.neg};
+        else FP8P_TMAX()->x = tmax;
+      } else if (!RW) {
+        FP8P_TMAX()->x = tmax;
+      }
     } else if (RW && F32) {
       // rowwise fp32: the tile's columns in two halves of 64, one 16-row
       // block per pass: 16 rows x 256 B (row r's 16-byte chunk c at
@@ -1553,6 +1596,14 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
     // by the barrier of this tile's last k-tile: no barrier here.
     if (RWT) FP8P_SCALES(b_ok, b_pi, b_m0, b_n0, tile & 1);
   }
+  if constexpr (may_key(EPI, RW)) {
+    if (g.keys) {
+      const v4u k = *FP8P_KEYS();
+      const uint32_t m = act_keys_amax<form_of(EPI)>(g.act, {k.x, k.y, k.z, k.w});
+      if (hw_lane() == 0) g.part[0][blockIdx.x * 4 + wave] = m;
+      return;
+    }
+  }
   if constexpr (EPI != EPI_NONE && !RW) {
     if (g.maxima) {
       const uint2 tmax = *FP8P_TMAX();
@@ -1565,6 +1616,7 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
     }
   }
 #undef FP8P_BIAS_TAB
+#undef FP8P_KEYS
 #undef FP8P_TMAX
 #undef FP8P_H2D
 #undef FP8P_H2

@@ -222,6 +222,17 @@ hipError_t with_form(int act, F f) {
 // Slices of the column sums that a call's kernel writes.
 int act_slices(int64_t M, int64_t N) { return (int)col_slices(small_tiles(M, N, BN), M); }
 
+template <int EPI, int FA>
+hipError_t launch_pers(const ActArgs &g, bool rowwise, int blocks, hipStream_t stream) {
+  const bool kfull = g.K[0] % BK == 0;
+  auto kern = rowwise ? (kfull ? k_gemm_fp8_pers<true, true, false, FA, false, EPI>
+                               : k_gemm_fp8_pers<false, true, false, FA, false, EPI>)
+                      : (kfull ? k_gemm_fp8_pers<true, false, false, FA, false, EPI>
+                               : k_gemm_fp8_pers<false, false, false, FA, false, EPI>);
+  hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(THREADS), 0, stream, g);
+  return hipGetLastError();
+}
+
 // One problem, as launch_gate.
 template <int EPI, int FA>
 hipError_t launch_act(ActArgs &g, bool rowwise, int *nparts, hipStream_t stream) {
@@ -244,13 +255,9 @@ hipError_t launch_act(ActArgs &g, bool rowwise, int *nparts, hipStream_t stream)
   constexpr int kComputeUnits = 256;
   const int blocks = g.total < kComputeUnits ? g.total : kComputeUnits;
   *nparts = blocks * 4;                           // one per wave
-  const bool kfull = g.K[0] % BK == 0;
-  auto kern = rowwise ? (kfull ? k_gemm_fp8_pers<true, true, false, FA, false, EPI>
-                               : k_gemm_fp8_pers<false, true, false, FA, false, EPI>)
-                      : (kfull ? k_gemm_fp8_pers<true, false, false, FA, false, EPI>
-                               : k_gemm_fp8_pers<false, false, false, FA, false, EPI>);
-  hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(THREADS), 0, stream, g);
-  return hipGetLastError();
+  return is_act(EPI) && g.res ? launch_pers<is_act(EPI) ? EPI - EPI_ACT + EPI_ACT_RES : EPI, FA>(
+                                    g, rowwise, blocks, stream)
+                              : launch_pers<EPI, FA>(g, rowwise, blocks, stream);
 }
 
 }  // namespace
@@ -320,6 +327,7 @@ hipError_t linear_act_fwd_launch(const LinearActIn &in, int scaling, const Fp8Ou
       }
       measured = o && o->qt;
       g.maxima = measured;
+      g.keys = measured && !rw && !in.y && in.act != FP8L_ACT_NONE;
       if (measured) set_partials(g, 0, src, workspace, rw, BN);
       return launch_act<EPI_ACT + FORM, 0>(g, rw, &src.nparts, stream);
     });
@@ -367,13 +375,15 @@ hipError_t linear_act_bwd_launch(const uint8_t *dyq, const float *sdy, const uin
   CastSource src = {};
   src.x = dz;
   set_partials(g, 0, src, workspace, rw, BN);
-  hipError_t e = with_form(act, [&](auto form) {
+  src.sums = g.colsum;
+  src.slices = act_slices(M, H);
+  src.sums_f32 = dbias_f32;
+  src.sums_out = dbias;
+  const hipError_t e = with_form(act, [&](auto form) {
     constexpr int EPI = EPI_DACT + decltype(form)::value;
     return (scaling & FP8L_E5M2) ? launch_act<EPI, 1>(g, rw, &src.nparts, stream)
                                  : launch_act<EPI, 0>(g, rw, &src.nparts, stream);
   });
-  if (e == hipSuccess && dbias)
-    e = column_sums_launch(sums, act_slices(M, H), H, dbias, dbias_f32, stream);
   if (e != hipSuccess) return e;
   return quantize_cast_launch(&src, 1, M, H, scaling, &o, stream);
 }

@@ -326,11 +326,46 @@ __device__ __forceinline__ void load_param8(float (&f)[8], const void *p, int wf
   }
 }
 // What is quantized: x itself, its norm (CastNorm), or an activation of it.
-constexpr int SRC_X = 0, SRC_NORM = 1, SRC_ACT = 2;
+// SRC_SUMS: x itself, and the last workgroups of the grid finish sums of columns (a
+// bias's gradient) that the pass before left in slices, which spares a launch.
+constexpr int SRC_X = 0, SRC_NORM = 1, SRC_ACT = 2, SRC_SUMS = 3;
 struct CastAct {
   ActConsts c;
   int form;
 };
+struct CastSums {
+  const float *part;
+  int slices, cols, f32, tiles;   // tiles: workgroups of the cast
+  void *out;
+};
+
+// Sums of 64 columns of part[slices][cols] by a workgroup of 64 SL threads: SL slices
+// of the partial rows, joined in LDS in slice order.  slices = 0 gives zeros.
+template <int SL>
+__device__ __forceinline__ void column_sums(const CastSums &s, int tile) {
+  const int c = tile * 64 + (threadIdx.x & 63);
+  const int sl = threadIdx.x >> 6;
+  const int cc = min(c, s.cols - 1);
+  float a = 0.f;
+  for (int i0 = sl; i0 < s.slices; i0 += SL * 8) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      v[u] = s.part[(size_t)min(i0 + SL * u, s.slices - 1) * s.cols + cc];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) a += i0 + SL * u < s.slices ? v[u] : 0.f;
+  }
+  __shared__ float red[SL][64];
+  red[sl][threadIdx.x & 63] = a;
+  __syncthreads();
+  if (sl == 0 && c < s.cols) {
+#pragma unroll
+    for (int i = 1; i < SL; ++i) a += red[i][threadIdx.x];
+    if (s.f32) static_cast<float *>(s.out)[c] = a;
+    else static_cast<uint16_t *>(s.out)[c] = (uint16_t)bf16x2_bits(a, 0.f);
+  }
+}
+
 template <int MODE, int FMT, int SRC>
 __device__ __forceinline__ void cast_tile(
     const uint16_t *__restrict__ x, int rows, int cols, int tiles_c,
@@ -559,7 +594,14 @@ __global__ __launch_bounds__(CT_THREADS) void k_cast_transpose(
     const uint16_t *__restrict__ x, int rows, int cols, int tiles_c,
     float *__restrict__ scale, float *__restrict__ scale_t,
     const uint32_t *__restrict__ part, int nparts, float *__restrict__ amax_out,
-    uint8_t *__restrict__ q, uint8_t *__restrict__ qt, CastNorm nm, RowParts rp, CastAct ca) {
+    uint8_t *__restrict__ q, uint8_t *__restrict__ qt, CastNorm nm, RowParts rp, CastAct ca,
+    CastSums cs) {
+  if constexpr (SRC == SRC_SUMS) {
+    if ((int)blockIdx.x >= cs.tiles) {              // uniform
+      column_sums<CT_THREADS / 64>(cs, (int)blockIdx.x - cs.tiles);
+      return;
+    }
+  }
   cast_tile<MODE, FMT, SRC>(x, rows, cols, tiles_c, scale, scale_t, part, nparts, amax_out, q,
                             qt, nm, rp, ca);
 }
@@ -657,6 +699,9 @@ hipError_t cast_fmt(const CastSource *src, int count, int64_t rows, int64_t cols
   const int R = (int)rows, C = (int)cols, l = count - 1;   // l: the last tensor
   const CastNorm nm = {src->w, src->b, src->wf32, src->mean, src->rstd};
   const CastAct ca = {act_consts(src->act), act_form(src->act)};
+  const CastSums cs = {src->sums, src->slices, C, src->sums_f32,
+                       (int)(cdiv(rows, CT_T) * cdiv(cols, CT_T)), src->sums_out};
+  const unsigned extra = SRC == SRC_SUMS ? (unsigned)cdiv(cols, 64) : 0;
   const bool in_cast = rowwise && scales_in_cast(*src, rows, cols);
   if (rowwise && !in_cast) {
     const int64_t nbr = cdiv(rows, FR_OUT), nbc = cdiv(cols, FR_OUT);
@@ -694,17 +739,20 @@ hipError_t cast_fmt(const CastSource *src, int count, int64_t rows, int64_t cols
         hipLaunchKernelGGL((k_cast_pair<MODE_TW, FMT>), dim3(nb, 2), dim3(CT_THREADS), 0, stream,
                            j, job(1), R, C, (int)ct_c, src->nparts);
     } else if (!rowwise) {
-      hipLaunchKernelGGL((k_cast_transpose<MODE_TW, FMT, SRC>), dim3(nb), dim3(CT_THREADS), 0,
+      hipLaunchKernelGGL((k_cast_transpose<MODE_TW, FMT, SRC>), dim3(nb + extra),
+                         dim3(CT_THREADS), 0,
                          stream, j.x, R, C, (int)ct_c, j.scale, j.scale_t, j.part, src->nparts,
-                         j.amax_out, j.q, j.qt, nm, j.rp, ca);
+                         j.amax_out, j.q, j.qt, nm, j.rp, ca, cs);
     } else if (in_cast) {
-      hipLaunchKernelGGL((k_cast_transpose<MODE_RP, FMT, SRC>), dim3(nb), dim3(CT_THREADS), 0,
+      hipLaunchKernelGGL((k_cast_transpose<MODE_RP, FMT, SRC>), dim3(nb + extra),
+                         dim3(CT_THREADS), 0,
                          stream, j.x, R, C, (int)ct_c, j.scale, j.scale_t, nullptr, 0, j.amax_out,
-                         j.q, j.qt, nm, j.rp, ca);
+                         j.q, j.qt, nm, j.rp, ca, cs);
     } else {
-      hipLaunchKernelGGL((k_cast_transpose<MODE_RW, FMT, SRC>), dim3(nb), dim3(CT_THREADS), 0,
+      hipLaunchKernelGGL((k_cast_transpose<MODE_RW, FMT, SRC>), dim3(nb + extra),
+                         dim3(CT_THREADS), 0,
                          stream, j.x, R, C, (int)ct_c, j.scale, j.scale_t, nullptr, 0, nullptr,
-                         j.q, j.qt, nm, j.rp, ca);
+                         j.q, j.qt, nm, j.rp, ca, cs);
     }
   }
   return hipGetLastError();
@@ -814,7 +862,7 @@ hipError_t quantize_scaled_launch(const void *x, int64_t rows, int64_t cols,
                        dim3(CT_THREADS), 0, stream, static_cast<const uint16_t *>(x), (int)rows,
                        (int)cols, (int)ct_c, const_cast<float *>(scale), nullptr, nullptr, 0,
                        nullptr, static_cast<uint8_t *>(q), static_cast<uint8_t *>(qt),
-                       CastNorm{}, RowParts{}, CastAct{});
+                       CastNorm{}, RowParts{}, CastAct{}, CastSums{});
   return hipGetLastError();
 }
 
@@ -823,6 +871,9 @@ hipError_t quantize_cast_launch(const CastSource *src, int count, int64_t rows, 
   const bool rw = (scaling & FP8L_ROWWISE) != 0;
   if (src->rstd) return cast_fmt<0, SRC_NORM>(src, count, rows, cols, rw, o, stream);  // E4M3 only
   if (src->act) return cast_fmt<0, SRC_ACT>(src, count, rows, cols, rw, o, stream);    // E4M3 only
+  if (src->sums && rows > 0)
+    return (scaling & FP8L_E5M2) ? cast_fmt<1, SRC_SUMS>(src, count, rows, cols, rw, o, stream)
+                                 : cast_fmt<0, SRC_SUMS>(src, count, rows, cols, rw, o, stream);
   if (scaling & FP8L_E5M2) return cast_fmt<1, SRC_X>(src, count, rows, cols, rw, o, stream);
   return cast_fmt<0, SRC_X>(src, count, rows, cols, rw, o, stream);
 }
