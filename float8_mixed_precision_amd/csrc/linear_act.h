@@ -46,6 +46,8 @@ __global__ __launch_bounds__(64 * SK_WAVES) void k_act_skinny(ActSkinnyArgs p) {
   v4f acc[CB];
 #pragma unroll
   for (int c = 0; c < CB; ++c) acc[c] = (v4f){0.f, 0.f, 0.f, 0.f};
+  // (loading a group of k-tiles while the one before it is multiplied gained nothing:
+  // 13.2 us either way at 1 x 4096, K = 14336)
   for (int t0 = wave; t0 < nk; t0 += SK_WAVES * SK_UNROLL) {
     v4u fw[SK_UNROLL][CB][2], fx[SK_UNROLL][2];
 #pragma unroll
@@ -95,7 +97,16 @@ __global__ __launch_bounds__(64 * SK_WAVES) void k_act_skinny(ActSkinnyArgs p) {
   if (p.e.C[0]) *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.e.C[0]) + at) = y;
 }
 
-bool act_few_tokens(int64_t M, int64_t N) { return M <= SKINNY_M; }
+// Which calls it takes: up to 16 tokens, but where the contraction is long and a split
+// one (below) has enough parts.  A workgroup's loads, half cache lines of 16 rows, take
+// about 3 us for every 4096 of K at one token and 4.5 at 16, whatever N is.  Measured, six
+// sets of weights in turn, this kernel / split, us, M x N x K: 1 x 14336 x 4096 14.9 /
+// 17.0, 1 x 4096 x 14336 15.5 / 17.3, 4 x 4096 x 14336 16.2 / 17.8, 8 x 4096 x 14336 17.5 /
+// 17.1, 16 x 4096 x 14336 20.4 / 17.9, 16 x 14336 x 4096 17.9 / 17.7, 16 x 4096 x 4096 6.8 /
+// 9.8, 4 x 1024 x 14336 13.1 / 10.2, 8 x 512 x 14336 14.3 / 9.7.
+bool act_few_tokens(int64_t M, int64_t N, int64_t K) {
+  return M <= SKINNY_M && !(K >= 64 * BK && (M > 4 || N < 4096));
+}
 
 template <int FORM>
 hipError_t act_skinny_launch(const ActSkinnyArgs &p, hipStream_t stream) {
@@ -113,63 +124,64 @@ hipError_t act_skinny_launch(const ActSkinnyArgs &p, hipStream_t stream) {
 //
 // Where one small tile per output leaves most of the compute units idle and the
 // contraction is long, its k-tiles go to several workgroups (EPI_SPLIT), whose fp32
-// sums this kernel adds in order and finishes.  A thread has 8 columns of a row.
+// sums this kernel adds in order and finishes.  A thread has 4 columns of a row and
+// loads 8 parts together.
 struct ActJoinArgs {
   ActArgs e;
   const float *sx, *sw;
   int parts, rowwise;
 };
 template <int FORM>
-__global__ __launch_bounds__(256) void k_act_join(ActJoinArgs p, int64_t n8) {
+__global__ __launch_bounds__(256) void k_act_join(ActJoinArgs p, int64_t n4) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n8) return;
+  if (i >= n4) return;
   const int N = p.e.N[0];
-  const int m = (int)(i * 8 / N), n = (int)(i * 8 % N);
-  const size_t mn = (size_t)p.e.M[0] * N;
-  const v4f *src = reinterpret_cast<const v4f *>(p.e.partial + (size_t)i * 8);
-  v4f a[2] = {src[0], src[1]};
-  for (int s = 1; s < p.parts; ++s) {
-    a[0] += src[(size_t)s * (mn / 4)];
-    a[1] += src[(size_t)s * (mn / 4) + 1];
+  const int m = (int)(i * 4 / N), n = (int)(i * 4 % N);
+  const v4f *src = reinterpret_cast<const v4f *>(p.e.partial) + i;
+  uint2 r = make_uint2(0u, 0u), z;
+  if (p.e.res) r = *reinterpret_cast<const uint2 *>(p.e.res + (size_t)i * 4);
+  v4f a = {0.f, 0.f, 0.f, 0.f};
+  for (int s0 = 0; s0 < p.parts; s0 += 8) {
+    v4f v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = src[(size_t)min(s0 + u, p.parts - 1) * n4];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (s0 + u < p.parts) a += v[u];
   }
   const float ia = 1.0f / p.sx[p.rowwise ? m : 0];
+  float f[4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int c = n + 4 * h;
-    float f[4];
-#pragma unroll
-    for (int j = 0; j < 4; j += 2) {
-      const float2 b = bias_pair(p.e, c + j);
-      f[j] = add32((a[h][j] * ia) * (1.0f / p.sw[p.rowwise ? c + j : 0]), b.x);
-      f[j + 1] = add32((a[h][j + 1] * ia) * (1.0f / p.sw[p.rowwise ? c + j + 1 : 0]), b.y);
-    }
-    const size_t at = (size_t)i * 8 + 4 * h;
-    uint2 r = make_uint2(0u, 0u), z;
-    if (p.e.res) r = *reinterpret_cast<const uint2 *>(p.e.res + at);
-    const uint2 y = act_out4<FORM>(p.e.act, f, p.e.res != nullptr, r, z);
-    if (p.e.a) *reinterpret_cast<uint2 *>(p.e.a + at) = z;
-    if (p.e.C[0]) *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.e.C[0]) + at) = y;
+  for (int j = 0; j < 4; j += 2) {
+    const float2 b = bias_pair(p.e, n + j);
+    f[j] = add32((a[j] * ia) * (1.0f / p.sw[p.rowwise ? n + j : 0]), b.x);
+    f[j + 1] = add32((a[j + 1] * ia) * (1.0f / p.sw[p.rowwise ? n + j + 1 : 0]), b.y);
   }
+  const uint2 y = act_out4<FORM>(p.e.act, f, p.e.res != nullptr, r, z);
+  if (p.e.a) *reinterpret_cast<uint2 *>(p.e.a + (size_t)i * 4) = z;
+  if (p.e.C[0]) *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.e.C[0]) + (size_t)i * 4) = y;
 }
 
-// Parts of the contraction of an [M, N] output; 1: not split.
-constexpr int64_t SPLIT_TILES = 512;              // workgroups: two a compute unit
-#ifndef FP8L_SPLIT_KT
-#define FP8L_SPLIT_KT 4
-#endif
+// Parts of the contraction of an [M, N] output; 1: not split.  As many as fill the
+// compute units with workgroups of 8 k-tiles or more (of 4 where there are fewer than 32
+// k-tiles).  Measured, at most 256 workgroups of 8 / 512 of 8 / 256 of 4 k-tiles / not
+// split, us: 50 x 4096 x 14336 17.0 / 18.8 / 16.9 / 45, 64 x 4096 x 4096 10.9 / 10.9 / 12.5 /
+// 14.0, 128 x 4096 x 14336 21.0 / 22.3 / 20.9, 50 x 1024 x 14336 10.7 / 10.7 / 12.2, 64 x 2048
+// x 2048 9.3 / 9.3 / 8.1, 20 x 512 x 1024 7.0 / 7.0 / 6.6.
+constexpr int64_t SPLIT_TILES = 256;              // workgroups
 int act_parts(int64_t M, int64_t N, int64_t K, int *part_kt) {
   const int64_t t = tiles(M, TM) * tiles(N, TB), nk = tiles(K, BK);
+  const int64_t least = nk >= 32 ? 8 : 4;         // k-tiles of a part
   int64_t s = SPLIT_TILES / t;
-  if (s > nk / FP8L_SPLIT_KT) s = nk / FP8L_SPLIT_KT;
+  if (s > nk / least) s = nk / least;
   if (t > 128 || s < 2) return 1;
   *part_kt = (int)tiles(nk, s);
   return (int)tiles(nk, *part_kt);
 }
 size_t act_split_bytes(int64_t M, int64_t N) {
   // at most SPLIT_TILES tiles of partial sums
-  size_t b = (size_t)SPLIT_TILES * TM * TB * sizeof(float);
-  const size_t all = (size_t)(SPLIT_TILES * M * N) * sizeof(float);
-  return b < all ? b : all;
+  const size_t tile = (size_t)TM * TB, mn = (size_t)M * (size_t)N;
+  return (size_t)SPLIT_TILES * (mn < tile ? mn : tile) * sizeof(float);
 }
 
 template <int FORM>
@@ -181,9 +193,9 @@ hipError_t act_split_launch(ActArgs &g, const float *sx, const float *sw, bool r
   hipLaunchKernelGGL((k_gate_tile<EPI_SPLIT, 0, false>), dim3((unsigned)g.total, (unsigned)parts),
                      dim3(256), 0, stream, g);
   const ActJoinArgs p = {g, sx, sw, parts, rw};
-  const int64_t n8 = (int64_t)g.M[0] * g.N[0] / 8;
-  hipLaunchKernelGGL((k_act_join<FORM>), dim3((unsigned)((n8 + 255) / 256)), dim3(256), 0, stream,
-                     p, n8);
+  const int64_t n4 = (int64_t)g.M[0] * g.N[0] / 4;
+  hipLaunchKernelGGL((k_act_join<FORM>), dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, stream,
+                     p, n4);
   return hipGetLastError();
 }
 
@@ -315,7 +327,7 @@ hipError_t linear_act_fwd_launch(const LinearActIn &in, int scaling, const Fp8Ou
                            stream, g, n8);
         return hipGetLastError();
       }
-      if (act_few_tokens(M, N)) {
+      if (act_few_tokens(M, N, K)) {
         const ActSkinnyArgs p = {in.xq, in.wq, in.sx, in.sw, g, (int)M, (int)N, (int)K, rw};
         return act_skinny_launch<FORM>(p, stream);
       }

@@ -623,7 +623,7 @@ template <class TS, int LAY, int MODE>
 hipError_t launch_res_bwd(const ResBwdArgs &a, int *blocks, hipStream_t stream) {
   auto launch = [&](auto tpr, auto ch) {
     constexpr int TPR = decltype(tpr)::value, CH = decltype(ch)::value;
-    constexpr int BLK = TPR > 512 ? TPR : 512;
+    constexpr int BLK = TPR > 512 ? TPR : 512 / TPR * TPR < 512 ? 2 * TPR : 512;
     int64_t nb = cdiv(a.rows, BLK / TPR);
     if (nb > kComputeUnits) nb = kComputeUnits;
     *blocks = (int)nb;
@@ -633,6 +633,10 @@ hipError_t launch_res_bwd(const ResBwdArgs &a, int *blocks, hipStream_t stream) 
   };
   if constexpr (LAY == LAY_SCALAR)
     return launch(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
+  else if (a.cols > 256 * 8 && a.cols <= 320 * 8)
+    return launch(std::integral_constant<int, 320>(), std::integral_constant<int, 1>());
+  else if (a.cols > 512 * 8 && a.cols <= 640 * 8)
+    return launch(std::integral_constant<int, 640>(), std::integral_constant<int, 1>());
   else
     return with_shape<false>(a.cols, false, launch);
 }

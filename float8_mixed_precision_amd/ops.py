@@ -411,11 +411,12 @@ def _checked(device, *tensors) -> None:
     and shape, and dense."""
     index = -1 if device.type == "cpu" else device.index
     for name, t, dtype, shape in tensors:
-        if t is not None and (t.dtype is not dtype or t.shape != shape
-                              or t.get_device() != index or not t.is_contiguous()):
-            raise ValueError("%s must be a dense %s %s on %s, not a %s%s %s on %s" % (
-                name, dtype, tuple(shape), device, "" if t.is_contiguous() else "strided ",
-                t.dtype, tuple(t.shape), t.device))
+        if t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == index
+                         and t.is_contiguous()):
+            continue
+        raise ValueError("%s must be a dense %s %s on %s, not a %s%s %s on %s" % (
+            name, dtype, tuple(shape), device, "" if t.is_contiguous() else "strided ",
+            t.dtype, tuple(t.shape), t.device))
 
 
 _NO_GUARD = contextlib.nullcontext()
@@ -649,22 +650,28 @@ def _resnorm_params(b, post, pre, gate):
         raise ValueError("b must be a [rows, cols] bf16 matrix")
     if post is None and pre is None:
         raise ValueError("post or pre must be a (weight, bias) pair")
+    post, pre = post or _NO_PAIR, pre or _NO_PAIR
     pd = None
-    for pair in (post, pre, (gate,)):
-        for p in pair or ():
-            if p is not None:
-                if p.dtype not in _DTYPES or pd not in (None, p.dtype):
-                    raise ValueError("the parameters must be all bf16 or all fp32")
-                pd = p.dtype
-    return post or _NO_PAIR, pre or _NO_PAIR, pd or torch.bfloat16
+    for p in (*post, *pre, gate):
+        if p is not None and p.dtype is not pd:
+            if pd is not None or p.dtype not in _DTYPES:
+                raise ValueError("the parameters must be all bf16 or all fp32")
+            pd = p.dtype
+    return post, pre, pd or torch.bfloat16
 
 
 def _pack_resnorm(b, x, s, y, post, pre, gate, pd, xd, norms, alpha, eps, rms, st):
-    rows, cols = b.shape
-    a = lambda t: 0 if t is None else t.data_ptr()
-    return _RESNORM.pack(rows, cols, int(rms), norms, _DTYPES[xd], _DTYPES[pd], alpha, eps, a(b),
-                         a(x), a(post[0]), a(post[1]), a(pre[0]), a(pre[1]), a(gate), a(s), a(y),
-                         a(st.mean_post), a(st.rstd_post), a(st.mean_pre), a(st.rstd_pre))
+    # (each field spelled out: a helper's calls take as long as the checks do)
+    (rows, cols), (pw, pb), (qw, qb) = b.shape, post, pre
+    mp, rp, mq, rq = st.mean_post, st.rstd_post, st.mean_pre, st.rstd_pre
+    return _RESNORM.pack(
+        rows, cols, int(rms), norms, _DTYPES[xd], _DTYPES[pd], alpha, eps, b.data_ptr(),
+        0 if x is None else x.data_ptr(), 0 if pw is None else pw.data_ptr(),
+        0 if pb is None else pb.data_ptr(), 0 if qw is None else qw.data_ptr(),
+        0 if qb is None else qb.data_ptr(), 0 if gate is None else gate.data_ptr(),
+        s.data_ptr(), 0 if y is None else y.data_ptr(), 0 if mp is None else mp.data_ptr(),
+        0 if rp is None else rp.data_ptr(), 0 if mq is None else mq.data_ptr(),
+        0 if rq is None else rq.data_ptr())
 
 
 def _resnorm_forward(b, x, post, pre, gate, rms, s, y, stats):
