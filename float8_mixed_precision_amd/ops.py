@@ -1544,3 +1544,105 @@ class SwiGLUFFNStep:
         for ev in done.values():      # the step ends with the side stream joined
             main.wait_event(ev)
         return rec
+
+
+# ------------------------------------------ feed-forward block with bias --
+
+class MLPStep:
+    """One Float8 feed-forward block y = W2 act(W1 y + b1) + b2 between two norms
+    of a residual stream, fwd+bwd on preallocated buffers.
+
+    y_in is the normed stream in front of the block (bf16 [M, D]: its fp8 copies
+    are what a residual norm in front of it leaves; here they are taken from
+    ``qy``, a Quantized of y_in), x the stream [M, D] (bf16 or fp32) that the block
+    adds to, w1 [H, D], b1 [H], w2 [D, H], b2 [D], d_s and d_y the gradients of the
+    outputs s [M, D] (the stream's type; None for 0) and of the next block's normed
+    input (bf16 [M, D]).  ``run()`` enqueues, on the current stream:
+
+      quantize w1, w2
+      z, codes of h = act(y_in W1^T + b1)             (fp8_linear_act_fwd)
+      out = h W2^T + b2                               (fp8_linear_act_fwd)
+      s = alpha x + gate N(out; post), codes of N(s; pre)   (fp8_resnorm_quantize)
+      grad_x, d_out and its codes, the norms' and gate's gradients
+                                                      (fp8_resnorm_bwd)
+      grad_b2                                         (fp8_bias_act_bwd)
+      dz, its codes, grad_b1                          (fp8_linear_act_bwd)
+      grad_y = dz W1, grad_w1 = dz^T y_in, grad_w2 = d_out^T h  (one grouped launch)
+
+    ``qs`` holds the next block's input, ``qy`` of the step after this one.  post
+    and pre are (weight, bias) pairs (each a tensor or None), post None for no norm
+    behind the block; gate [D] or None.  With ``e5m2_grad`` the codes of d_out and
+    dz are E5M2.  An fp32 stream keeps the next block's input in bf16 too (``y``).
+    Without biases b1 or b2 (None) their gradients are not computed; d_out's codes
+    then come from fp8_resnorm_bwd, else with grad_b2 from fp8_bias_act_bwd.
+    """
+
+    def __init__(self, qy: Quantized, x, w1, b1, w2, b2, d_s, d_y, act: str = "gelu",
+                 post=None, pre=_NO_PAIR, gate=None, alpha: float = 1.0, eps: float = 1e-5,
+                 rms: bool = False, rowwise: bool = False, e5m2_grad: bool = False):
+        self.qy, self.x, self.w1, self.b1, self.w2, self.b2 = qy, x, w1, b1, w2, b2
+        self.d_s, self.d_y, self.act = d_s, d_y, act
+        self.post, self.pre, self.gate, self.alpha = post, pre, gate, alpha
+        self.eps, self.rms, self.rowwise, self.e5m2_grad = eps, rms, rowwise, e5m2_grad
+        (M, D), H, dev = x.shape, w1.shape[0], x.device
+        assert w1.shape == (H, D) and w2.shape == (D, H) and d_y.shape == (M, D)
+        self.M, self.D, self.H = M, D, H
+        new = lambda *shape: torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        self.qw1, self.qw2 = (alloc_quantized(r, c, rowwise, dev) for r, c in ((H, D), (D, H)))
+        self.qh, self.qdz = (alloc_quantized(M, H, rowwise, dev) for _ in range(2))
+        self.qs, self.qdo = (alloc_quantized(M, D, rowwise, dev) for _ in range(2))
+        self.z, self.dz, self.out = new(M, H), new(M, H), new(M, D)
+        self.grad_y, self.grad_w1, self.grad_w2 = new(M, D), new(H, D), new(D, H)
+        like = lambda t: torch.empty_like(t) if t is not None else None
+        self.grad_b1, self.grad_b2 = like(b1), like(b2)
+        self.s = torch.empty_like(x)
+        self.y = new(M, D) if x.dtype == torch.float32 else None
+        self.stats = alloc_resnorm_stats(M, dev, post is not None, True, rms)
+        f32 = lambda t: (torch.empty(D, dtype=torch.float32, device=dev) if t is not None else None)
+        pw, pb = post or _NO_PAIR
+        self.grads = ResNormGrads(torch.empty_like(x), new(M, D), f32(gate), f32(pw), f32(pb),
+                                  f32(pre[0]), f32(pre[1]))
+        self.ws = torch.empty(max(
+            [256] + [fp8_linear_workspace_bytes(r, c, rowwise) for r, c in ((H, D), (D, H))]
+            + [fp8_linear_act_workspace_bytes(M, c, rowwise) for c in (H, D)]
+            + [fp8_resnorm_workspace_bytes(M, D, rowwise)]), dtype=torch.uint8, device=dev)
+
+    @property
+    def flops(self) -> int:
+        """Five GEMMs of 2*M*D*H each."""
+        return 10 * self.M * self.D * self.H
+
+    def forward(self, stream=None):
+        rw, ws = self.rowwise, self.ws
+        fp8_linear_quantize(self.w1, rw, self.qw1, ws, stream)
+        fp8_linear_quantize(self.w2, rw, self.qw2, ws, stream)
+        fp8_linear_act_fwd(self.qy.q, self.qy.scale, self.qw1.q, self.qw1.scale, self.b1, self.act,
+                           rowwise=rw, z=self.z, out=self.qh, workspace=ws, stream=stream)
+        fp8_linear_act_fwd(self.qh.q, self.qh.scale, self.qw2.q, self.qw2.scale, self.b2,
+                           rowwise=rw, y=self.out, workspace=ws, stream=stream)
+        fp8_resnorm_quantize(self.out, self.x, self.post, self.pre, self.gate, self.alpha, self.eps,
+                             self.rms, rw, s=self.s, y=self.y, out=self.qs, stats=self.stats,
+                             workspace=ws, stream=stream)
+
+    def backward(self, stream=None):
+        rw, ws, e5 = self.rowwise, self.ws, self.e5m2_grad
+        bias2 = self.b2 is not None
+        fp8_resnorm_bwd(self.d_y, self.d_s, self.out, self.s, self.stats, self.post, self.pre,
+                        self.gate, self.alpha, self.rms, self.grads,
+                        None if bias2 else self.qdo, rw, e5, ws, stream)
+        if bias2:
+            fp8_bias_act_bwd(self.grads.db, rowwise=rw, e5m2=e5, out=self.qdo, dbias=self.grad_b2,
+                             workspace=ws, stream=stream)
+        fp8_linear_act_bwd(self.qdo.q, self.qdo.scale, self.qw2.qt, self.qw2.scale_t, self.z,
+                           self.act, rw, e5, self.dz, self.qdz, self.grad_b1, workspace=ws,
+                           stream=stream)
+        # the longest contraction first (H), then the tokens'
+        fp8_linear_gemm_grouped([
+            (self.qdz.q, self.qdz.scale, self.qw1.qt, self.qw1.scale_t, self.grad_y),
+            (self.qdz.qt, self.qdz.scale_t, self.qy.qt, self.qy.scale_t, self.grad_w1),
+            (self.qdo.qt, self.qdo.scale_t, self.qh.qt, self.qh.scale_t, self.grad_w2)],
+            rw, stream, e5m2=e5)
+
+    def run(self, stream=None):
+        self.forward(stream)
+        self.backward(stream)
