@@ -57,6 +57,9 @@ def parse():
     p.add_argument("--fused", action="store_true",
                    help="with --ffn-block-only: the block with its norm in front and the gate "
                         "in the GEMMs' kernels")
+    p.add_argument("--mlp-block-only", action="store_true",
+                   help="only measure the biased GELU feed-forward block between two norms of a "
+                        "residual stream; prints its JSON object and exits")
     p.add_argument("--phase-timing", action="store_true",
                    help="only time the GEMM's phases per workgroup (the measurement build "
                         "libfp8phase.so) at the 8B FFN GEMM shapes and exit")
@@ -201,6 +204,44 @@ def measure_pipelined(steps, flops_per_step: int, stream, reps: int = 20):
             "steps": reps, "ms_per_step": round(el * 1e3 / reps, 4),
             "gemm_achieved_tflops": round(gt, 2), "gemm_frac": round(gt / PEAK_FP8_TFLOPS, 4),
             "gemm_avg_launch_us": round(sum(t for _, _, t in g) * 1e3 / sum(n for _, n, _ in g), 2)}
+
+
+def measure_mlp_block(steps, wl, reps: int = 5):
+    """The biased GELU block between two norms of a residual stream (MLPStep) on the
+    FFN workload's tensors (x and W1 of w1, W2 and dY of w2): five GEMMs, the
+    linears' epilogues and the residual norm as producers of the fp8 operands.  Wall
+    time per step bracketed by device synchronisation."""
+    import torch
+    from float8_mixed_precision_amd import ops
+
+    names = [l.name for l in wl.linears]
+    if names != ["w1", "w3", "w2"]:
+        return None
+    w1, w2 = steps[0], steps[2]
+    rw, dev = w1.rowwise, w1.x.device
+    vec = lambda n, v: torch.full((n,), v, dtype=torch.bfloat16, device=dev)
+    one, zero = vec(w1.K, 1.0), vec(w1.K, 0.0)
+    blk = ops.MLPStep(ops.fp8_linear_quantize(w1.x, rw), w1.x, w1.w, vec(w1.N, 0.1), w2.w, zero,
+                      w2.dy, w2.dy, "gelu", (one, zero), (one, zero), vec(w1.K, 0.5), rms=True,
+                      rowwise=rw)
+    times = {}
+    for name, fn in (("forward", blk.forward), ("backward", blk.backward), ("step", blk.run)):
+        for _ in range(2):
+            fn()
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        for _ in range(reps):
+            fn()
+        torch.cuda.synchronize()
+        times[name] = (time.perf_counter() - t0) / reps
+    flops = blk.flops
+    return {"metric": "biased GELU FFN block fwd+bwd between two norms of a residual stream",
+            "value": round(flops / times["step"] / 1e12, 2), "unit": "TFLOP/s",
+            "ms_per_step": round(times["step"] * 1e3, 4),
+            "forward_ms": round(times["forward"] * 1e3, 4),
+            "backward_ms": round(times["backward"] * 1e3, 4),
+            "shape": {"M": blk.M, "D": blk.D, "H": blk.H}, "flops_per_step": flops,
+            "steps": reps}
 
 
 def measure_ffn_block(steps, wl, stream, reps: int = 5, e5m2_grad: bool = False,
@@ -830,6 +871,11 @@ def main():
         print("[bench] ffn block only", file=sys.stderr, flush=True)
         print(json.dumps(measure_ffn_block(steps, wl, stream, reps=args.steps,
                                            fused=args.fused)), flush=True)
+        return
+
+    if args.mlp_block_only:
+        print("[bench] mlp block only", file=sys.stderr, flush=True)
+        print(json.dumps(measure_mlp_block(steps, wl, reps=args.steps)), flush=True)
         return
 
     # one step on the current stream: per linear its quantizes, forward GEMM
