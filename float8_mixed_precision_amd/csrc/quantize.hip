@@ -328,11 +328,21 @@ __device__ __forceinline__ void load_param8(float (&f)[8], const void *p, int wf
 // What is quantized: x itself, its norm (CastNorm), or an activation of it.
 // SRC_SUMS: x itself, and the last workgroups of the grid finish sums of columns (a
 // bias's gradient) that the pass before left in slices, which spares a launch.
-constexpr int SRC_X = 0, SRC_NORM = 1, SRC_ACT = 2, SRC_SUMS = 3;
-struct CastAct {
-  ActConsts c;
-  int form;
-};
+// SRC_ACT + a form of act.h (not ACT_ID): that activation of x. A kernel a form: with
+// the form as an argument the cast alone of 8192x14336 took 101 (relu), 102 (silu) and
+// 102 us (gelu_tanh) against 92, 98 and 96; erf's 102-104 us either way; a cast without
+// an activation takes 90-94, and a copy of its 470 MB 88.
+constexpr int SRC_X = 0, SRC_NORM = 1, SRC_SUMS = 3, SRC_ACT = 4;
+constexpr bool is_src_act(int src) { return src >= SRC_ACT; }
+// fp8x4<0> in two instructions a value instead of three: the vector instructions bound
+// a cast that evaluates an activation
+__device__ __forceinline__ uint32_t e4m3x4_act(float a, float b, float c, float d) {
+  auto sat = [](float v) {
+    return min_nan(max_nan(v, -FP8L_E4M3_MAX), FP8L_E4M3_MAX);
+  };
+  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(sat(a), sat(b), 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(sat(c), sat(d), w, true);
+}
 struct CastSums {
   const float *part;
   int slices, cols, f32, tiles;   // tiles: workgroups of the cast
@@ -372,8 +382,12 @@ __device__ __forceinline__ void cast_tile(
     float *__restrict__ scale, float *__restrict__ scale_t,
     const uint32_t *__restrict__ part, int nparts, float *__restrict__ amax_out,
     uint8_t *__restrict__ q, uint8_t *__restrict__ qt, const CastNorm &nm,
-    const RowParts &rp, const CastAct &ca) {
-  constexpr bool NORM = SRC == SRC_NORM;
+    const RowParts &rp, const ActConsts &ca) {
+  constexpr bool NORM = SRC == SRC_NORM, ACT = is_src_act(SRC);
+  auto code4 = [](float a, float b, float c, float d) {
+    if constexpr (ACT) return e4m3x4_act(a, b, c, d);
+    else return fp8x4<FMT>(a, b, c, d);
+  };
   __shared__ __attribute__((aligned(16))) uint8_t lds[CT_T * CT_T];
   const int tid = threadIdx.x;
   // block -> (tile_r, tile_c): groups of CT_GROUP row tiles (the last one
@@ -489,16 +503,9 @@ __device__ __forceinline__ void cast_tile(
           for (int j = 0; j < 4; ++j) srs[j] = scale[r + j];
         }
       }
-      // (with an activation, whose code is not one block, the loads come first, or
-      // each row's would wait for the row before)
-      U4 vs[4];
-      if (SRC == SRC_ACT) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) vs[j] = load16(x + (size_t)(r + j) * cols + c);
-      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const U4 v = SRC == SRC_ACT ? vs[j] : load16(x + (size_t)(r + j) * cols + c);
+        const U4 v = load16(x + (size_t)(r + j) * cols + c);
         float f[8];
         f[0] = bf16_to_f32(v.x & 0xFFFFu); f[1] = bf16_to_f32(v.x >> 16);
         f[2] = bf16_to_f32(v.y & 0xFFFFu); f[3] = bf16_to_f32(v.y >> 16);
@@ -514,26 +521,26 @@ __device__ __forceinline__ void cast_tile(
             f[e + 1] = bf16_to_f32(y >> 16);
           }
         }
-        if (SRC == SRC_ACT) {
+        if constexpr (ACT) {
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
-            const uint32_t y = bf16x2_bits(act_value_any(ca.c, ca.form, f[e]),
-                                           act_value_any(ca.c, ca.form, f[e + 1]));
+            const uint32_t y = bf16x2_bits(act_value<SRC - SRC_ACT>(ca, f[e]),
+                                           act_value<SRC - SRC_ACT>(ca, f[e + 1]));
             f[e] = bf16_to_f32(y & 0xFFFFu);
             f[e + 1] = bf16_to_f32(y >> 16);
           }
         }
         const float s = srs[j];
-        const uint32_t q0 = fp8x4<FMT>(f[0] * s, f[1] * s, f[2] * s, f[3] * s);
-        const uint32_t q1 = fp8x4<FMT>(f[4] * s, f[5] * s, f[6] * s, f[7] * s);
+        const uint32_t q0 = code4(f[0] * s, f[1] * s, f[2] * s, f[3] * s);
+        const uint32_t q1 = code4(f[4] * s, f[5] * s, f[6] * s, f[7] * s);
         v2u_t *qdst = reinterpret_cast<v2u_t *>(q + (size_t)(r + j) * cols + c);
         if (CT_NT)
           __builtin_nontemporal_store((v2u_t){q0, q1}, qdst);
         else
           *qdst = (v2u_t){q0, q1};
         if (ROWWISE) {
-          lo[j] = fp8x4<FMT>(f[0] * sc[0], f[1] * sc[1], f[2] * sc[2], f[3] * sc[3]);
-          hi[j] = fp8x4<FMT>(f[4] * sc[4], f[5] * sc[5], f[6] * sc[6], f[7] * sc[7]);
+          lo[j] = code4(f[0] * sc[0], f[1] * sc[1], f[2] * sc[2], f[3] * sc[3]);
+          hi[j] = code4(f[4] * sc[4], f[5] * sc[5], f[6] * sc[6], f[7] * sc[7]);
         } else {
           lo[j] = q0;
           hi[j] = q1;
@@ -594,7 +601,7 @@ __global__ __launch_bounds__(CT_THREADS) void k_cast_transpose(
     const uint16_t *__restrict__ x, int rows, int cols, int tiles_c,
     float *__restrict__ scale, float *__restrict__ scale_t,
     const uint32_t *__restrict__ part, int nparts, float *__restrict__ amax_out,
-    uint8_t *__restrict__ q, uint8_t *__restrict__ qt, CastNorm nm, RowParts rp, CastAct ca,
+    uint8_t *__restrict__ q, uint8_t *__restrict__ qt, CastNorm nm, RowParts rp, ActConsts ca,
     CastSums cs) {
   if constexpr (SRC == SRC_SUMS) {
     if ((int)blockIdx.x >= cs.tiles) {              // uniform
@@ -622,10 +629,10 @@ __global__ __launch_bounds__(CT_THREADS) void k_cast_pair(CastJob a, CastJob b, 
                                                           int tiles_c, int nparts) {
   if (blockIdx.y == 0)
     cast_tile<MODE, FMT, SRC_X>(a.x, rows, cols, tiles_c, a.scale, a.scale_t, a.part, nparts,
-                                a.amax_out, a.q, a.qt, CastNorm{}, a.rp, CastAct{});
+                                a.amax_out, a.q, a.qt, CastNorm{}, a.rp, ActConsts{});
   else
     cast_tile<MODE, FMT, SRC_X>(b.x, rows, cols, tiles_c, b.scale, b.scale_t, b.part, nparts,
-                                b.amax_out, b.q, b.qt, CastNorm{}, b.rp, CastAct{});
+                                b.amax_out, b.q, b.qt, CastNorm{}, b.rp, ActConsts{});
 }
 
 // --------------------------------------------------------------- encode --
@@ -698,7 +705,7 @@ hipError_t cast_fmt(const CastSource *src, int count, int64_t rows, int64_t cols
                     const Fp8Out *o, hipStream_t stream) {
   const int R = (int)rows, C = (int)cols, l = count - 1;   // l: the last tensor
   const CastNorm nm = {src->w, src->b, src->wf32, src->mean, src->rstd};
-  const CastAct ca = {act_consts(src->act), act_form(src->act)};
+  const ActConsts ca = act_consts(src->act);
   const CastSums cs = {src->sums, src->slices, C, src->sums_f32,
                        (int)(cdiv(rows, CT_T) * cdiv(cols, CT_T)), src->sums_out};
   const unsigned extra = SRC == SRC_SUMS ? (unsigned)cdiv(cols, 64) : 0;
@@ -862,7 +869,7 @@ hipError_t quantize_scaled_launch(const void *x, int64_t rows, int64_t cols,
                        dim3(CT_THREADS), 0, stream, static_cast<const uint16_t *>(x), (int)rows,
                        (int)cols, (int)ct_c, const_cast<float *>(scale), nullptr, nullptr, 0,
                        nullptr, static_cast<uint8_t *>(q), static_cast<uint8_t *>(qt),
-                       CastNorm{}, RowParts{}, CastAct{}, CastSums{});
+                       CastNorm{}, RowParts{}, ActConsts{}, CastSums{});
   return hipGetLastError();
 }
 
@@ -870,7 +877,12 @@ hipError_t quantize_cast_launch(const CastSource *src, int count, int64_t rows, 
                                 int scaling, const Fp8Out *o, hipStream_t stream) {
   const bool rw = (scaling & FP8L_ROWWISE) != 0;
   if (src->rstd) return cast_fmt<0, SRC_NORM>(src, count, rows, cols, rw, o, stream);  // E4M3 only
-  if (src->act) return cast_fmt<0, SRC_ACT>(src, count, rows, cols, rw, o, stream);    // E4M3 only
+  switch (src->act ? act_form(src->act) : ACT_ID) {            // E4M3 only
+    case ACT_RELUS: return cast_fmt<0, SRC_ACT + ACT_RELUS>(src, count, rows, cols, rw, o, stream);
+    case ACT_SIG: return cast_fmt<0, SRC_ACT + ACT_SIG>(src, count, rows, cols, rw, o, stream);
+    case ACT_ERF: return cast_fmt<0, SRC_ACT + ACT_ERF>(src, count, rows, cols, rw, o, stream);
+    default: break;
+  }
   if (src->sums && rows > 0)
     return (scaling & FP8L_E5M2) ? cast_fmt<1, SRC_SUMS>(src, count, rows, cols, rw, o, stream)
                                  : cast_fmt<0, SRC_SUMS>(src, count, rows, cols, rw, o, stream);
