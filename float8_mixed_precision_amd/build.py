@@ -28,6 +28,7 @@ HIPCC_FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-fvisibility=hidden",
     "-Wall", "-Wno-unused-function",
+    "-parallel-jobs=4",                  # the sources of a library side by side
 ]
 
 

@@ -6,7 +6,8 @@
 //
 // Bound: HBM.  The pass reads dy (and z) once, writes dz (unless it is dy) and takes
 // the amax partial maxima and the column sums on the way; the cast reads dz again,
-// mostly from the Infinity Cache.
+// mostly from the Infinity Cache.  8192 x 4096 without an activation: 14.5 us for the
+// pass (67 MB read, 4.6 TB/s), 22.2 for the cast (134 MB, 6.0 TB/s).
 //
 // Part of quantize.hip (included at its end).
 #pragma once
@@ -160,7 +161,8 @@ __global__ __launch_bounds__(64 * FIN_SLICES) void k_column_sums(CastSums s) {
 // ----------------------------------------------------------- rows alone --
 
 // Codes, scale and amax of each row of act(x), for serving: a workgroup per row,
-// which stays in the cache between the maximum and the cast.
+// which stays in the cache between the maximum and the cast.  Bound: latency, 3.9 us for
+// one row of 14336.
 __global__ __launch_bounds__(1024) void k_quantize_rows(const uint16_t *__restrict__ x,
                                                         ActConsts act, int form, int cols,
                                                         uint8_t *__restrict__ q,

@@ -177,6 +177,15 @@ struct Fp8Out {
 // colpart[col_slices][cols].  With rstd, the values quantized are not x but
 // its layer norm (norm_value of the row's mean and rstd, weight w and bias b,
 // rounded to bf16); mean NULL counts as 0, w as 1, b as 0.
+// The parameters' gradients of a residual norm from the sums of its backward pass,
+// sums[parts][4][cols] (resnorm.h).
+struct ResFinish {
+  const float *sums;
+  int parts, cols, wf32, post;
+  int tiles;                   // workgroups of the cast that it is finished beside
+  const void *post_w, *post_b, *gate;
+  float *dgate, *dpost_w, *dpost_b, *dpre_w, *dpre_b;
+};
 struct CastSource {
   const void *x;
   const void *w, *b;
@@ -192,6 +201,7 @@ struct CastSource {
   const float *sums;
   int slices, sums_f32;
   void *sums_out;
+  const ResFinish *res;        // or a residual norm's gradients; NULL: none
 };
 // count (1, or 2 with none of rstd, act and sums) tensors of one shape and one count of partials, in
 // the same launches.

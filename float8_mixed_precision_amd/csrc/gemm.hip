@@ -374,10 +374,9 @@ constexpr int EPI_STORES = 32;
 // become reciprocals between the MFMAs of the last k-tile of the tile
 // before it.
 constexpr int SCALE_DMAS = 2;
-#ifndef FP8L_IN_AHEAD
-#define FP8L_IN_AHEAD 2
-#endif
-constexpr int IN_AHEAD = FP8L_IN_AHEAD;
+// passes ahead that an epilogue loads its z or residual (8192 x 14336 x 4096, us a call
+// with codes for silu / gelu: 1 497 / 497, 2 482 / 490, 4 481 / 493)
+constexpr int IN_AHEAD = 2;
 constexpr int RW_STAGE_OFF = EPI_WAVE_BYTES / 2;
 static_assert(2 * SCALE_BYTES <= RW_STAGE_OFF, "two scale tables below the rowwise staging");
 static_assert(EPI_WAVE_BYTES == 64 * BK, "a wave's staging is at its operand offset + EPI_OFF");
@@ -1206,8 +1205,12 @@ __global__ __launch_bounds__(THREADS) void k_gemm_fp8_pers(typename ArgsOf<EPI>:
       // The tile's columns in two halves of 64, one 16-row block per pass, staged
       // as fp32 in 4 KB (16 rows x 256 B, row r's 16-byte chunk c at c ^ r) and
       // taken up by rows: lane l has columns 8 (l % 8) .. + 7 of rows l / 8 and
-      // l / 8 + 8.  The next pass is staged and read back, and its part of the
-      // residual or of z loaded, before this one is computed.
+      // l / 8 + 8.  The next pass is staged and read back, and a later one's part of
+      // the residual or of z loaded, before this one is computed.  (Rows: bias, z,
+      // residual and y are 16-byte accesses of whole 128-byte lines, and a column's
+      // sum stays in one lane's registers.)  Bound: vector instructions, an
+      // instruction an element costs 3.4 us at 8192 x 14336; z's and y's bytes, which
+      // all workgroups move at the same time (z read: 45 us).
       constexpr bool ACT = is_act(EPI);
       constexpr int FORM = form_of(EPI);
       constexpr bool HAS_IN = is_act_res(EPI) || (!ACT && FORM != ACT_ID);

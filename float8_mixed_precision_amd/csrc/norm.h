@@ -676,7 +676,6 @@ __global__ __launch_bounds__(BWD_THREADS) void k_norm_bwd(NormBwdArgs p) {
 // dw and db from `parts` partial rows.  Workgroup: 64 columns of one of the
 // two, 16 slices of the partial rows (slice s takes rows s, s + 16, ...),
 // joined in LDS in slice order.  parts = 0 (no rows) gives zeros.
-constexpr int FIN_SLICES = 16;
 __global__ __launch_bounds__(64 * FIN_SLICES) void k_norm_bwd_finish(
     const float *__restrict__ part, int parts, int cols, float *dw, float *db) {
   const int tiles = (cols + 63) / 64;

@@ -326,13 +326,14 @@ __device__ __forceinline__ void load_param8(float (&f)[8], const void *p, int wf
   }
 }
 // What is quantized: x itself, its norm (CastNorm), or an activation of it.
-// SRC_SUMS: x itself, and the last workgroups of the grid finish sums of columns (a
-// bias's gradient) that the pass before left in slices, which spares a launch.
+// SRC_SUMS, SRC_RES: x itself, and the last workgroups of the grid finish sums of columns
+// (a bias's gradient, a residual norm's) that the pass before left in slices, which
+// spares a launch.
 // SRC_ACT + a form of act.h (not ACT_ID): that activation of x. A kernel a form: with
 // the form as an argument the cast alone of 8192x14336 took 101 (relu), 102 (silu) and
 // 102 us (gelu_tanh) against 92, 98 and 96; erf's 102-104 us either way; a cast without
 // an activation takes 90-94, and a copy of its 470 MB 88.
-constexpr int SRC_X = 0, SRC_NORM = 1, SRC_SUMS = 3, SRC_ACT = 4;
+constexpr int SRC_X = 0, SRC_NORM = 1, SRC_RES = 2, SRC_SUMS = 3, SRC_ACT = 4;
 constexpr bool is_src_act(int src) { return src >= SRC_ACT; }
 // fp8x4<0> in two instructions a value instead of three: the vector instructions bound
 // a cast that evaluates an activation
@@ -343,6 +344,9 @@ __device__ __forceinline__ uint32_t e4m3x4_act(float a, float b, float c, float 
   const int w = __builtin_amdgcn_cvt_pk_fp8_f32(sat(a), sat(b), 0, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(sat(c), sat(d), w, true);
 }
+// slices of partial rows that a kernel's workgroup of 16 waves adds up
+constexpr int FIN_SLICES = 16;
+
 struct CastSums {
   const float *part;
   int slices, cols, f32, tiles;   // tiles: workgroups of the cast
@@ -375,6 +379,75 @@ __device__ __forceinline__ void column_sums(const CastSums &s, int tile) {
     else static_cast<uint16_t *>(s.out)[c] = (uint16_t)bf16x2_bits(a, 0.f);
   }
 }
+
+__device__ __forceinline__ float param1(const void *p, int wf32, float none, int c) {
+  if (!p) return none;
+  return wf32 ? static_cast<const float *>(p)[c]
+              : bf16_to_f32(static_cast<const uint16_t *>(p)[c]);
+}
+
+// 64 columns of one norm's pair of sums by a workgroup of W waves: FIN_SLICES slices of
+// the partial rows, joined in LDS in slice order whatever W is.  parts = 0 (no rows)
+// gives zeros.
+template <int W>
+__device__ __forceinline__ void res_finish(const ResFinish &p, int tile) {
+  const int half = (p.cols + 63) / 64;
+  const bool pre = tile >= half;
+  if (pre ? !p.dpre_w && !p.dpre_b : !p.dgate && !p.dpost_w && !p.dpost_b) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = (pre ? tile - half : tile) * 64 + lane;
+  const int cc = min(c, p.cols - 1);
+  const float *src = p.sums + (pre ? 2 * (size_t)p.cols : 0) + cc;
+  __shared__ float2 red[FIN_SLICES][64];
+#pragma unroll
+  for (int sl = wave; sl < FIN_SLICES; sl += W) {
+    float a = 0.f, b = 0.f;
+    for (int i0 = sl; i0 < p.parts; i0 += FIN_SLICES * 8) {
+      float u[8], v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const size_t at = (size_t)min(i0 + FIN_SLICES * k, p.parts - 1) * 4 * p.cols;
+        u[k] = src[at];
+        v[k] = src[at + p.cols];
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        a += i0 + FIN_SLICES * k < p.parts ? u[k] : 0.f;
+        b += i0 + FIN_SLICES * k < p.parts ? v[k] : 0.f;
+      }
+    }
+    red[sl][lane] = make_float2(a, b);
+  }
+  __syncthreads();
+  if (wave > 0 || c >= p.cols) return;
+  float a = red[0][lane].x, b = red[0][lane].y;
+#pragma unroll
+  for (int i = 1; i < FIN_SLICES; ++i) {
+    a += red[i][lane].x;
+    b += red[i][lane].y;
+  }
+  if (pre) {
+    if (p.dpre_w) p.dpre_w[c] = a;
+    if (p.dpre_b) p.dpre_b[c] = b;
+    return;
+  }
+  const float gate = param1(p.gate, p.wf32, 1.f, c);
+  if (p.dpost_w) p.dpost_w[c] = gate * a;
+  if (p.dpost_b) p.dpost_b[c] = gate * b;
+  if (p.dgate)
+    p.dgate[c] = p.post ? __builtin_fmaf(param1(p.post_w, p.wf32, 1.f, c), a,
+                                         param1(p.post_b, p.wf32, 0.f, c) * b)
+                        : a;
+}
+
+template <int SRC>
+struct TailOf {
+  typedef CastSums type;
+};
+template <>
+struct TailOf<SRC_RES> {
+  typedef ResFinish type;
+};
 
 template <int MODE, int FMT, int SRC>
 __device__ __forceinline__ void cast_tile(
@@ -602,10 +675,13 @@ __global__ __launch_bounds__(CT_THREADS) void k_cast_transpose(
     float *__restrict__ scale, float *__restrict__ scale_t,
     const uint32_t *__restrict__ part, int nparts, float *__restrict__ amax_out,
     uint8_t *__restrict__ q, uint8_t *__restrict__ qt, CastNorm nm, RowParts rp, ActConsts ca,
-    CastSums cs) {
-  if constexpr (SRC == SRC_SUMS) {
+    typename TailOf<SRC>::type cs) {
+  if constexpr (SRC == SRC_SUMS || SRC == SRC_RES) {
     if ((int)blockIdx.x >= cs.tiles) {              // uniform
-      column_sums<CT_THREADS / 64>(cs, (int)blockIdx.x - cs.tiles);
+      if constexpr (SRC == SRC_SUMS)
+        column_sums<CT_THREADS / 64>(cs, (int)blockIdx.x - cs.tiles);
+      else
+        res_finish<CT_THREADS / 64>(cs, (int)blockIdx.x - cs.tiles);
       return;
     }
   }
@@ -706,9 +782,16 @@ hipError_t cast_fmt(const CastSource *src, int count, int64_t rows, int64_t cols
   const int R = (int)rows, C = (int)cols, l = count - 1;   // l: the last tensor
   const CastNorm nm = {src->w, src->b, src->wf32, src->mean, src->rstd};
   const ActConsts ca = act_consts(src->act);
-  const CastSums cs = {src->sums, src->slices, C, src->sums_f32,
-                       (int)(cdiv(rows, CT_T) * cdiv(cols, CT_T)), src->sums_out};
-  const unsigned extra = SRC == SRC_SUMS ? (unsigned)cdiv(cols, 64) : 0;
+  const int tiles = (int)(cdiv(rows, CT_T) * cdiv(cols, CT_T));
+  const unsigned extra = SRC == SRC_SUMS ? (unsigned)cdiv(cols, 64)
+                         : SRC == SRC_RES ? (unsigned)(2 * cdiv(cols, 64)) : 0;
+  typename TailOf<SRC>::type cs;
+  if constexpr (SRC == SRC_RES) {
+    cs = *src->res;
+    cs.tiles = tiles;
+  } else {
+    cs = {src->sums, src->slices, C, src->sums_f32, tiles, src->sums_out};
+  }
   const bool in_cast = rowwise && scales_in_cast(*src, rows, cols);
   if (rowwise && !in_cast) {
     const int64_t nbr = cdiv(rows, FR_OUT), nbc = cdiv(cols, FR_OUT);
@@ -883,6 +966,9 @@ hipError_t quantize_cast_launch(const CastSource *src, int count, int64_t rows, 
     case ACT_ERF: return cast_fmt<0, SRC_ACT + ACT_ERF>(src, count, rows, cols, rw, o, stream);
     default: break;
   }
+  if (src->res)
+    return (scaling & FP8L_E5M2) ? cast_fmt<1, SRC_RES>(src, count, rows, cols, rw, o, stream)
+                                 : cast_fmt<0, SRC_RES>(src, count, rows, cols, rw, o, stream);
   if (src->sums && rows > 0)
     return (scaling & FP8L_E5M2) ? cast_fmt<1, SRC_SUMS>(src, count, rows, cols, rw, o, stream)
                                  : cast_fmt<0, SRC_SUMS>(src, count, rows, cols, rw, o, stream);

@@ -1552,12 +1552,11 @@ class MLPStep:
     """One Float8 feed-forward block y = W2 act(W1 y + b1) + b2 between two norms
     of a residual stream, fwd+bwd on preallocated buffers.
 
-    y_in is the normed stream in front of the block (bf16 [M, D]: its fp8 copies
-    are what a residual norm in front of it leaves; here they are taken from
-    ``qy``, a Quantized of y_in), x the stream [M, D] (bf16 or fp32) that the block
-    adds to, w1 [H, D], b1 [H], w2 [D, H], b2 [D], d_s and d_y the gradients of the
-    outputs s [M, D] (the stream's type; None for 0) and of the next block's normed
-    input (bf16 [M, D]).  ``run()`` enqueues, on the current stream:
+    ``qy`` is the Quantized of y_in [M, D], the normed stream in front of the block,
+    as the residual norm before it leaves it.  x is the stream [M, D] (bf16 or fp32)
+    that the block adds to; w1 [H, D], b1 [H], w2 [D, H], b2 [D]; d_s and d_y are the
+    gradients of the outputs: of s [M, D] (the stream's type; None for 0) and of the
+    next block's normed input (bf16 [M, D]).  ``run()`` enqueues, on the current stream:
 
       quantize w1, w2
       z, codes of h = act(y_in W1^T + b1)             (fp8_linear_act_fwd)

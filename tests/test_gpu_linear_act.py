@@ -363,6 +363,29 @@ def test_bias_act_backward(shape, rowwise, e5m2):
             G.assert_quantize_equal(_hq(q), ref, "codes of dz " + label)
 
 
+@pytest.mark.parametrize("at", [(0, 0), (8207, 4111), (4100, 2000)], ids=str)
+def test_maxima_of_many_tiles(at):
+    """More tiles than maxima that the cast reads: they are reduced in between, and the
+    largest value counts wherever it lies."""
+    M, N = 8208, 4112
+    dy = G.dev_bf16(W.random_bf16(87, (M, N), 1e-2, 0))
+    dy[at] = -37.5
+    _, q, _ = ops.fp8_bias_act_bwd(dy, None, "none")
+    z = G.dev_bf16(W.random_bf16(88, (M, N), 1.0, 1)).clamp_(min=0.25)
+    dz, q2, db = ops.fp8_bias_act_bwd(dy, z, "relu", bias_dtype=F32)
+    ref = ops.fp8_linear_quantize(dy)
+    torch.cuda.synchronize()
+    assert torch.equal(_bits(dz), _bits(dy))
+    for got in (q, q2):
+        assert got.amax.item() == 37.5
+        for a, b in zip(_hq(got), _hq(ref)):
+            assert torch.equal(torch.as_tensor(a), torch.as_tensor(b))
+    # fp32 sums of 8208 terms, 64 rows in a tile and its 8 row phases, then 129 tiles
+    exact = dy.double().sum(0)
+    err = (dy.double().abs().sum(0) * (64 + 129)) * 2.0 ** -24
+    assert bool(((db.double() - exact).abs() <= err).all())
+
+
 def _every_bf16():
     z = (torch.arange(1 << 16, dtype=torch.int32) << 16).view(torch.float32).to(BF)
     return z
