@@ -22,7 +22,8 @@
 //
 // Bound: HBM, few rows: latency.  8192 x 4096, bf16 stream, RMS, both norms and a gate:
 // forward with maxima 35.3 us (201 MB, 5.7 TB/s) and its cast 23.2 (134 MB, 5.8),
-// backward 79 us (403 MB, 5.1 TB/s) and its cast 23.5; a large copy runs at 5.4 TB/s.
+// backward 79 us (420 MB with the partial sums, 5.3 TB/s) and its cast, which finishes
+// them, 27.5 (a kernel of their own 6.3 beside a cast of 23.5); a large copy runs at 5.4 TB/s.
 //
 // Part of quantize.hip (included at its end).
 #pragma once
