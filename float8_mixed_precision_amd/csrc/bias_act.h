@@ -267,10 +267,10 @@ hipError_t column_sums_launch(const float *part, int slices, int64_t cols, void 
 
 hipError_t quantize_rows_launch(const void *x, int act, int64_t rows, int64_t cols,
                                 const Fp8Out &o, hipStream_t stream) {
-  if (rows > 0)
-    hipLaunchKernelGGL(k_quantize_rows, dim3((unsigned)rows), dim3(1024), 0, stream,
-                       static_cast<const uint16_t *>(x), act_consts(act), act_form(act), (int)cols,
-                       static_cast<uint8_t *>(o.q), o.scale, o.amax);
+  if (rows == 0) return hipSuccess;
+  hipLaunchKernelGGL(k_quantize_rows, dim3((unsigned)rows), dim3(1024), 0, stream,
+                     static_cast<const uint16_t *>(x), act_consts(act), act_form(act), (int)cols,
+                     static_cast<uint8_t *>(o.q), o.scale, o.amax);
   return hipGetLastError();
 }
 

@@ -351,7 +351,8 @@ hipError_t linear_act_fwd_launch(const LinearActIn &in, int scaling, const Fp8Ou
     if (e != hipSuccess) return e;
   }
   if (!o) return hipSuccess;
-  if (!o->qt && rw && M > 0) return quantize_rows_launch(y, cast_act, M, N, *o, stream);
+  // (rows alone: neither qt nor its scales; also of no rows)
+  if (!o->qt && !o->scale_t && rw) return quantize_rows_launch(y, cast_act, M, N, *o, stream);
   if (measured) return quantize_cast_launch(&src, 1, M, N, scaling, o, stream);
   return quantize_act_launch(y, cast_act, M, N, scaling, *o, workspace, stream);
 }
