@@ -267,11 +267,18 @@ hipError_t column_sums_launch(const float *part, int slices, int64_t cols, void 
 
 hipError_t quantize_rows_launch(const void *x, int act, int64_t rows, int64_t cols,
                                 const Fp8Out &o, hipStream_t stream) {
-  if (rows == 0) return hipSuccess;
-  hipLaunchKernelGGL(k_quantize_rows, dim3((unsigned)rows), dim3(1024), 0, stream,
-                     static_cast<const uint16_t *>(x), act_consts(act), act_form(act), (int)cols,
-                     static_cast<uint8_t *>(o.q), o.scale, o.amax);
-  return hipGetLastError();
+  // (a launch takes fewer than 2^32 threads)
+  constexpr int64_t PIECE = (int64_t)1 << 21;
+  for (int64_t r = 0; r < rows; r += PIECE) {
+    const int64_t n = rows - r < PIECE ? rows - r : PIECE;
+    hipLaunchKernelGGL(k_quantize_rows, dim3((unsigned)n), dim3(1024), 0, stream,
+                       static_cast<const uint16_t *>(x) + r * cols, act_consts(act), act_form(act),
+                       (int)cols, static_cast<uint8_t *>(o.q) + r * cols, o.scale + r,
+                       o.amax ? o.amax + r : nullptr);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t quantize_act_launch(const void *x, int act, int64_t rows, int64_t cols, int scaling,
