@@ -19,7 +19,8 @@ bool bad_scaling(int scaling) { return (scaling & ~(FP8L_ROWWISE | FP8L_E5M2)) !
 
 // Dimensions are capped at 2^30 so that every 32-bit index in the kernels
 // stays in range (addresses are formed in 64 bits), and a matrix at 2^40
-// elements so that grid sizes fit in 32 bits.
+// elements; a quantized one further, so that each launch has fewer than 2^32
+// threads (quantize_fits).
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 // GEMM operands and outputs are addressed through buffer resources with
 // 32-bit byte offsets: each must stay below 2^31 bytes.
@@ -91,6 +92,7 @@ int check_quantize_args(const void *x, int64_t rows, int64_t cols, int scaling, 
                         const float *amax_out) {
   if (bad_scaling(scaling)) return FP8L_EINVAL;
   if (bad_dim(rows) || bad_dim(cols) || rows * cols > kMaxElems) return FP8L_ESHAPE;
+  if (!fp8l::quantize_fits(rows, cols, scaling)) return FP8L_ESHAPE;
   const bool empty = rows == 0 || cols == 0;
   // scale vectors may be NULL only where they have no entries (rowwise, 0 rows
   // or 0 columns); tensorwise scales always have one entry
@@ -361,6 +363,7 @@ int fp8_swiglu_fwd(const void *a, const void *b, int64_t rows, int64_t hidden, i
                    void *workspace, size_t workspace_bytes, void *stream) {
   if (scaling != FP8L_TENSORWISE && scaling != FP8L_ROWWISE) return FP8L_EINVAL;
   if (bad_dim(rows) || bad_dim(hidden) || rows * hidden > kMaxElems) return FP8L_ESHAPE;
+  if (!fp8l::quantize_fits(rows, hidden, scaling)) return FP8L_ESHAPE;
   const bool rw = scaling == FP8L_ROWWISE;
   if ((!scale && (!rw || rows > 0)) || (!scale_t && (!rw || hidden > 0))) return FP8L_EINVAL;
   if (rows * hidden > 0 && (!a || !b || !h || !hq || !hqt)) return FP8L_EINVAL;
@@ -386,6 +389,7 @@ int fp8_swiglu_bwd(const void *dh, const void *a, const void *b, int64_t rows, i
                    void *stream) {
   if (bad_scaling(scaling)) return FP8L_EINVAL;
   if (bad_dim(rows) || bad_dim(hidden) || rows * hidden > kMaxElems) return FP8L_ESHAPE;
+  if (!fp8l::quantize_fits(rows, hidden, scaling)) return FP8L_ESHAPE;
   const bool rw = (scaling & FP8L_ROWWISE) != 0;
   if ((!da_scale || !db_scale) && (!rw || rows > 0)) return FP8L_EINVAL;
   if ((!da_scale_t || !db_scale_t) && (!rw || hidden > 0)) return FP8L_EINVAL;
@@ -587,8 +591,7 @@ int fp8_bias_act_bwd(const void *dy, const void *z, int64_t M, int64_t N, int sc
   if (bad_scaling(scaling) || bad_act(act, pdtype)) return FP8L_EINVAL;
   int s = check_quantize_args(dy, M, N, scaling, q, qt, scale, scale_t, amax_out);
   if (s != FP8L_OK) return s;
-  // (tiles of the pass and their column sums are counted in 32 bits)
-  if (M * N > (int64_t)1 << 38) return FP8L_ESHAPE;
+  if (dbias && !fp8l::quantize_fits(M, N, scaling, (N + 63) / 64)) return FP8L_ESHAPE;
   if (act == FP8L_ACT_NONE) z = nullptr;
   else if (M * N > 0 && (!z || !dz)) return FP8L_EINVAL;
   if (misaligned(z) || misaligned(dz) || misaligned(dbias)) return FP8L_EALIGN;
@@ -649,6 +652,7 @@ int fp8_layernorm_quantize(const void *x, int64_t rows, int64_t cols, int kind,
   const bool rw = scaling == FP8L_ROWWISE;
   const bool rows_only = rw && !qt && rows > 0;
   if (cols % 16 != 0 || (!rows_only && rows % 16 != 0)) return FP8L_ESHAPE;
+  if (!rows_only && !fp8l::quantize_fits(rows, cols, scaling)) return FP8L_ESHAPE;
   if (rows > 0 && (!x || !q || (!qt && !rows_only))) return FP8L_EINVAL;
   // scale vectors may be NULL only where they have no entries
   if (!scale && (!rw || rows > 0)) return FP8L_EINVAL;
@@ -753,6 +757,7 @@ int fp8_resnorm_quantize(const fp8l_resnorm *r, int scaling, void *q, void *qt, 
   const bool rw = scaling == FP8L_ROWWISE;
   const bool rows_only = rw && !qt && in.rows > 0;
   if (in.cols % 16 != 0 || (!rows_only && in.rows % 16 != 0)) return FP8L_ESHAPE;
+  if (!rows_only && !fp8l::quantize_fits(in.rows, in.cols, scaling)) return FP8L_ESHAPE;
   if (in.rows > 0 && (!in.x || !q || (!qt && !rows_only))) return FP8L_EINVAL;
   // scale vectors may be NULL only where they have no entries
   if (!scale && (!rw || in.rows > 0)) return FP8L_EINVAL;
@@ -809,6 +814,8 @@ int fp8_resnorm_bwd(const fp8l_resnorm *r, const void *dy, const void *ds,
   if (misaligned(dy) || misaligned(ds) || misaligned(g->dx) || misaligned(g->db))
     return FP8L_EALIGN;
   const bool wants = g->dgate || g->dpost_w || g->dpost_b || g->dpre_w || g->dpre_b;
+  if (quant && !fp8l::quantize_fits(in.rows, in.cols, scaling, wants ? 2 * ((in.cols + 63) / 64) : 0))
+    return FP8L_ESHAPE;
   for (const float *f : {g->dgate, g->dpost_w, g->dpost_b, g->dpre_w, g->dpre_b})
     if (misaligned4(f)) return FP8L_EALIGN;
   if (quant) {

@@ -140,6 +140,9 @@ __device__ __forceinline__ float norm_value(float x, float mean, float rstd, flo
 // Quantize (amax partials -> scales -> cast + transpose), all enqueued on
 // `stream`.  Arguments were validated by the C ABI.
 size_t quantize_workspace_bytes(int64_t rows, int64_t cols, int scaling);
+// Whether every launch of a quantize of [rows, cols] has fewer than 2^32 threads, the
+// most that HIP takes.  beside: workgroups of the cast that finish sums of columns.
+bool quantize_fits(int64_t rows, int64_t cols, int scaling, int64_t beside = 0);
 hipError_t quantize_launch(const void *x, int64_t rows, int64_t cols,
                            int scaling, void *q, void *qt, float *scale,
                            float *scale_t, float *amax_out, void *workspace,

@@ -31,7 +31,11 @@
  *    overlap.
  *  - Dimensions must be >= 0 and multiples of 16 (FP8L_ESHAPE otherwise);
  *    every fp8 GEMM operand and every bf16 GEMM output must be smaller than
- *    2^31 bytes.
+ *    2^31 bytes.  A matrix that is quantized with its transpose has fewer than
+ *    2^23 tiles of 128 x 128 values (less a workgroup or two per 64 columns
+ *    where sums of columns are finished beside its cast) and, rowwise, fewer
+ *    than 2^29 - 128 rows and columns together: a launch takes fewer than 2^32
+ *    threads.
  *    A zero dimension is an empty matrix: the call is valid and writes only
  *    what its definition gives (scales of the empty set, zero outputs).
  *  - Argument errors are detected on the host before anything is enqueued
