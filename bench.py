@@ -208,7 +208,7 @@ def measure_pipelined(steps, flops_per_step: int, stream, reps: int = 20):
 
 def measure_mlp_block(steps, wl, reps: int = 5):
     """The biased GELU block between two norms of a residual stream (MLPStep) on the
-    FFN workload's tensors (x and W1 of w1, W2 and dY of w2): five GEMMs, the
+    FFN workload's tensors (x and W1 of w1, W2 and dY of w2): six GEMMs, the
     linears' epilogues and the residual norm as producers of the fp8 operands.  Wall
     time per step bracketed by device synchronisation."""
     import torch

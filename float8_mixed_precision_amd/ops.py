@@ -1608,8 +1608,8 @@ class MLPStep:
 
     @property
     def flops(self) -> int:
-        """Five GEMMs of 2*M*D*H each."""
-        return 10 * self.M * self.D * self.H
+        """Six GEMMs of 2*M*D*H each."""
+        return 12 * self.M * self.D * self.H
 
     def forward(self, stream=None):
         rw, ws = self.rowwise, self.ws
