@@ -280,6 +280,7 @@ int fp8_linear_quantize_scaled(const void *x, int64_t rows, int64_t cols, const 
                                void *q, void *qt, void *stream) {
   if (bad_dim(rows) || bad_dim(cols) || rows * cols > kMaxElems) return FP8L_ESHAPE;
   if (rows * cols == 0) return FP8L_OK;
+  if (!fp8l::quantize_fits(rows, cols, FP8L_TENSORWISE)) return FP8L_ESHAPE;
   if (!x || !scale || !q || !qt) return FP8L_EINVAL;
   if (misaligned(x) || misaligned(q) || misaligned(qt) ||
       (reinterpret_cast<uintptr_t>(scale) & 3u))

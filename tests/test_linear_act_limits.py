@@ -112,3 +112,18 @@ def test_sums_beside_the_cast_count():
     assert _resnorm(0, M, 16, True) == E.FP8L_ESHAPE
     assert _resnorm(0, M - 128, 16, True) == E.FP8L_ESHAPE
     assert _resnorm(0, M - 256, 16, True) == E.FP8L_EHIP
+
+
+@no_gpu
+def test_casts_past_a_launch():
+    """The cast with a given scale, whatever scaling its scale came from."""
+    def call(M, N):
+        new = _apart()
+        return E.lib().fp8_linear_quantize_scaled(new(), M, N, new(), new(), new(), None)
+
+    for scaling, M, N in TOO_MANY:
+        if scaling in (0, 2):
+            assert call(M, N) == E.FP8L_ESHAPE, (M, N)
+    for _, M, N in FIT:
+        assert call(M, N) == E.FP8L_EHIP, (M, N)
+    assert call(TILES, 0) == E.FP8L_OK
