@@ -815,8 +815,8 @@ int fp8_resnorm_bwd(const fp8l_resnorm *r, const void *dy, const void *ds,
   if (misaligned(dy) || misaligned(ds) || misaligned(g->dx) || misaligned(g->db))
     return FP8L_EALIGN;
   const bool wants = g->dgate || g->dpost_w || g->dpost_b || g->dpre_w || g->dpre_b;
-  if (quant && !fp8l::quantize_fits(in.rows, in.cols, scaling, wants ? 2 * ((in.cols + 63) / 64) : 0))
-    return FP8L_ESHAPE;
+  const int64_t beside = wants ? 2 * ((in.cols + 63) / 64) : 0;
+  if (quant && !fp8l::quantize_fits(in.rows, in.cols, scaling, beside)) return FP8L_ESHAPE;
   for (const float *f : {g->dgate, g->dpost_w, g->dpost_b, g->dpre_w, g->dpre_b})
     if (misaligned4(f)) return FP8L_EALIGN;
   if (quant) {

@@ -175,11 +175,6 @@ struct Fp8Out {
   float *scale, *scale_t, *amax;
 };
 
-// The cast half of a quantize with its partial maxima wherever a producer
-// put them: tensorwise part[nparts]; rowwise rowpart[row_slices][rows] and
-// colpart[col_slices][cols].  With rstd, the values quantized are not x but
-// its layer norm (norm_value of the row's mean and rstd, weight w and bias b,
-// rounded to bf16); mean NULL counts as 0, w as 1, b as 0.
 // The parameters' gradients of a residual norm from the sums of its backward pass,
 // sums[parts][4][cols] (resnorm.h).
 struct ResFinish {
@@ -189,6 +184,11 @@ struct ResFinish {
   const void *post_w, *post_b, *gate;
   float *dgate, *dpost_w, *dpost_b, *dpre_w, *dpre_b;
 };
+// The cast half of a quantize with its partial maxima wherever a producer
+// put them: tensorwise part[nparts]; rowwise rowpart[row_slices][rows] and
+// colpart[col_slices][cols].  With rstd, the values quantized are not x but
+// its layer norm (norm_value of the row's mean and rstd, weight w and bias b,
+// rounded to bf16); mean NULL counts as 0, w as 1, b as 0.
 struct CastSource {
   const void *x;
   const void *w, *b;
@@ -206,8 +206,8 @@ struct CastSource {
   void *sums_out;
   const ResFinish *res;        // or a residual norm's gradients; NULL: none
 };
-// count (1, or 2 with none of rstd, act and sums) tensors of one shape and one count of partials, in
-// the same launches.
+// count (1, or 2 with none of rstd, act, sums and res) tensors of one shape and one
+// count of partials, in the same launches.
 hipError_t quantize_cast_launch(const CastSource *src, int count, int64_t rows, int64_t cols,
                                 int scaling, const Fp8Out *o, hipStream_t stream);
 

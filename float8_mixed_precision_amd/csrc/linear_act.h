@@ -6,7 +6,8 @@
 //   dz = (dy W2) act'(z),  dbias = sum_m dz
 //
 // Large M: the persistent GEMM with EPI_ACT / EPI_DACT (gemm.hip).  Where its tiles
-// are too few, the small tiles of gated.h with the same forms.  Few tokens: below.
+// are too few, the small tiles of gated.h (64 x 128) with the same forms.  Few tokens:
+// below.
 // The activations: act.h.
 //
 // Part of gemm.hip (included at its end).
@@ -105,7 +106,10 @@ __global__ __launch_bounds__(64 * SK_WAVES) void k_act_skinny(ActSkinnyArgs p) {
 // sets of weights in turn, this kernel / split, us, M x N x K: 1 x 14336 x 4096 14.9 /
 // 17.0, 1 x 4096 x 14336 15.5 / 17.3, 4 x 4096 x 14336 16.2 / 17.8, 8 x 4096 x 14336 17.5 /
 // 17.1, 16 x 4096 x 14336 20.4 / 17.9, 16 x 14336 x 4096 17.9 / 17.7, 16 x 4096 x 4096 6.8 /
-// 9.8, 4 x 1024 x 14336 13.1 / 10.2, 8 x 512 x 14336 14.3 / 9.7.
+// 9.8, 4 x 1024 x 14336 13.1 / 10.2, 8 x 512 x 14336 14.3 / 9.7.  Past N = 16384, where
+// nothing is split, more than 4 tokens take the small tiles, which are then 128 or more:
+// 8 x 32768 x 8192 42.0 (4 tokens, this kernel: 62.5; not measured against each other at
+// one number of tokens).
 bool act_few_tokens(int64_t M, int64_t N, int64_t K) {
   return M <= SKINNY_M && !(K >= 64 * BK && (M > 4 || N < 4096));
 }
@@ -250,7 +254,14 @@ hipError_t launch_pers(const ActArgs &g, bool rowwise, int blocks, hipStream_t s
 
 // One problem, as launch_gate.  (8192 x 14336 x 4096, the GEMM alone: with gelu, z stored
 // and y measured 345-420 us, 2.3-2.8 PFLOP/s; the gradient through gelu 430-450, where the
-// plain GEMM takes 345.)
+// plain GEMM takes 345.)  Small tiles up to 80 large ones, the limit of the gate's backward
+// pass.  Here, small / large with the cast, us: forward with gelu, z, y and codes 40 large
+// tiles (1040 x 1808 x 784) 16.4 / 36.9, rowwise 19.2 / 37.3, 64 (1024 x 4096 x 4096) 32.9 /
+// 59.9, 35.4 / 61.9, 96 (1536 x 4096 x 4096) 48.4 / 61.6, 52.9 / 63.6, 112 (512 x 14336 x
+// 4096) 55.1 / 62.9, 64.5 / 67.8, 128 (2048 x 4096 x 4096) 62.2 / 63.9, 68.6 / 64.4; gradient
+// through gelu 40 tiles 16.1 / 35.0, 64 32.5 / 59.1, 96 48.8 / 60.4, 112 55.6 / 61.4, 128 59.2
+// / 62.3, without an activation 52.9 / 50.5.  (So from 81 to 112 tiles the small ones would
+// still be ahead, by up to a quarter.)
 template <int EPI, int FA>
 hipError_t launch_act(ActArgs &g, bool rowwise, int *nparts, hipStream_t stream) {
   g.count = 1;

@@ -764,7 +764,8 @@ bool quantize_fits(int64_t rows, int64_t cols, int scaling, int64_t beside) {
   // (the passes in front of the cast have at most twice its tiles and half its threads)
   static_assert(CT_T <= 2 * AM_TR && CT_T <= AM_TC && CT_THREADS >= 2 * AM_THREADS, "");
   if ((cdiv(rows, CT_T) * cdiv(cols, CT_T) + beside) * CT_THREADS > most) return false;
-  return !(scaling & FP8L_ROWWISE) || (cdiv(rows, FR_OUT) + cdiv(cols, FR_OUT)) * FR_THREADS <= most;
+  if (!(scaling & FP8L_ROWWISE)) return true;
+  return (cdiv(rows, FR_OUT) + cdiv(cols, FR_OUT)) * FR_THREADS <= most;
 }
 
 namespace {

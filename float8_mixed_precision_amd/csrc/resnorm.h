@@ -24,6 +24,11 @@
 // forward with maxima 35.3 us (201 MB, 5.7 TB/s) and its cast 23.2 (134 MB, 5.8),
 // backward 79 us (420 MB with the partial sums, 5.3 TB/s) and its cast, which finishes
 // them, 27.5 (a kernel of their own 6.3 beside a cast of 23.5); a large copy runs at 5.4 TB/s.
+// An fp32 stream: forward 76.8 us with y (403 MB, 5.2 TB/s), backward 113.8 (604 MB, 5.3).
+// Above 8192 columns a thread has 16 of them in 128 registers, and the kernels spill: 27 to
+// 85 registers forward, 173 to 233 backward (four sums a column).  2048 x 16384, bf16 / fp32
+// stream: forward 87 / 137 us (3.1 / 2.9 TB/s), with maxima 80 / 149, backward 385 / 464
+// (1.0 / 1.3 TB/s), bound by that scratch memory; 2048 x 8192 26.5 / 35.0 and 38.4 / 63.6.
 //
 // Part of quantize.hip (included at its end).
 #pragma once
@@ -583,7 +588,11 @@ hipError_t launch_res_bwd(const ResBwdArgs &a, int *blocks, hipStream_t stream) 
   if constexpr (LAY == LAY_SCALAR)
     return launch(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
   // (widths a little above a power of two, where twice the threads would be idle by
-  // nearly half: 1539 x 2050 fp32 24.9 us, 26.9 with 512 threads a row)
+  // nearly half.  These / 512 and 1024 threads a row, us, bf16 stream: 1539 x 2050 19.5 /
+  // 22.0, 2048 x 2560 19.0 / 21.7, 8192 x 2560 45.8 / 59.7, 512 x 5120 16.6 / 17.2, 2048 x
+  // 4112 26.3 / 29.1, 8192 x 5120 99 / 103; fp32: 1539 x 2050 20.4 / 22.7, 2048 x 2560 21.2 /
+  // 22.4, 8192 x 2560 75.0 / 70.9, 2048 x 5120 34.9 / 36.5, 8192 x 5120 146 / 143; with codes
+  // these are ahead at each of them, by 0 to 23%.  Further widths have no shape of their own.)
   else if (a.cols > 256 * 8 && a.cols <= 320 * 8)
     return launch(std::integral_constant<int, 320>(), std::integral_constant<int, 1>());
   else if (a.cols > 512 * 8 && a.cols <= 640 * 8)
